@@ -50,7 +50,7 @@ STATUS_NAMES = {
 }
 
 _vp, _i64, _sz, _f32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint64
-_st = ctypes.c_int
+_st, _int = ctypes.c_int, ctypes.c_int
 
 EXPORTS = {
     # name: (restype, argtypes)
@@ -88,6 +88,13 @@ EXPORTS = {
     "coda_fwd_fp8_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "coda_fwd_fp8": (_st, [_vp, _f32, _vp, _f32, _vp, _vp, _vp, _f32, _f32, _f32, _i64, _i64, _i64, _vp,
                            _vp, _vp, _vp, _sz, _vp]),
+    "coda_quant_q8": (_st, [_vp, _i64, _i64, _int, _vp, _vp, _vp]),
+    "coda_dequant_q8": (_st, [_vp, _vp, _i64, _i64, _int, _vp, _vp]),
+    "coda_add_rmsnorm_q8": (_st, [_vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "coda_matmul_q8_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "coda_matmul_q8": (_st, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "coda_bwd_swiglu_dgrad_q8": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
+                                       _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 for _name, (_res, _args) in EXPORTS.items():
@@ -321,6 +328,110 @@ def coda_bwd_swiglu_dgrad(dout, W2, y, W1, h, r, gamma, dy=None, s=None, dh=None
           c.t(dy, bf, (M, N1), "dy"), c.t(s, torch.float32, (M,), "s"), c.t(dh, bf, (M, d), "dh"),
           *c.ws(ws), stream=stream)
     return dy, s, dh
+
+
+# --------------------------------------------------------------------------- 8-bit operators
+def _q8_scales(M: int, n: int, block: int) -> tuple:
+    """Shape of the scales of [M, n] codes: one per row (block 0) or per row and `block` columns."""
+    return (M, -(-n // block)) if block else (M,)
+
+
+def coda_quant_q8(x, block=0, q=None, s=None, stream=None):
+    """INT8 codes and scales of x [M, n]; a scale per row (block=0) or per row and 128
+    columns (block=128, a checkpoint).  Returns (q, s)."""
+    M, n = x.shape
+    dev = x.device
+    if block not in (0, 128):
+        raise ValueError(f"block must be 0 (a scale per row) or 128, got {block}")
+    q = torch.empty((M, n), dtype=torch.int8, device=dev) if q is None else q
+    s = torch.empty(_q8_scales(M, n, block), dtype=torch.float32, device=dev) if s is None else s
+    c = _Call("coda_quant_q8", dev)
+    c.run(_lib.coda_quant_q8, c.t(x, torch.bfloat16, (M, n), "x"), M, n, block,
+          c.t(q, torch.int8, (M, n), "q"), c.t(s, torch.float32, _q8_scales(M, n, block), "s"),
+          stream=stream)
+    return q, s
+
+
+def coda_dequant_q8(q, s, block=0, x=None, stream=None):
+    """The values of codes q with scales s (as coda_quant_q8 gives them) in bf16; returns x."""
+    M, n = q.shape
+    if block not in (0, 128):
+        raise ValueError(f"block must be 0 (a scale per row) or 128, got {block}")
+    x = torch.empty((M, n), dtype=torch.bfloat16, device=q.device) if x is None else x
+    c = _Call("coda_dequant_q8", q.device)
+    c.run(_lib.coda_dequant_q8, c.t(q, torch.int8, (M, n), "q"),
+          c.t(s, torch.float32, _q8_scales(M, n, block), "s"), M, n, block,
+          c.t(x, torch.bfloat16, (M, n), "x"), stream=stream)
+    return x
+
+
+def coda_add_rmsnorm_q8(x, gamma, eps, z=None, h=None, q=None, s=None, stream=None):
+    """Residual addition h = x + z and RMS norm with INT8 codes and a scale per token; returns
+    (h, q, s).  Without z no h is written and x itself is returned in its place."""
+    M, d = x.shape
+    dev = x.device
+    bf = torch.bfloat16
+    if z is None and h is not None:
+        raise ValueError("h is an output of the residual's addition: it needs z")
+    if z is not None and h is None:
+        h = torch.empty((M, d), dtype=bf, device=dev)
+    q = torch.empty((M, d), dtype=torch.int8, device=dev) if q is None else q
+    s = torch.empty((M,), dtype=torch.float32, device=dev) if s is None else s
+    c = _Call("coda_add_rmsnorm_q8", dev)
+    c.run(_lib.coda_add_rmsnorm_q8, c.t(x, bf, (M, d), "x"), c.opt(z, bf, (M, d), "z"),
+          c.t(gamma, bf, (d,), "gamma"), float(eps), M, d, c.opt(h, bf, (M, d), "h"),
+          c.t(q, torch.int8, (M, d), "q"), c.t(s, torch.float32, (M,), "s"), stream=stream)
+    return (x if z is None else h), q, s
+
+
+def coda_matmul_q8_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(_lib.coda_matmul_q8_workspace_bytes(M, K, N))
+
+
+def coda_matmul_q8(a_q, a_s, W_q, w_s, z=None, y=None, ws=None, stream=None):
+    """INT8 product y = a_s * w_s * (a_q @ W_q) (+ z), a scale per token (a_s [M]) and per channel
+    (w_s [N]); W_q [K, N]; returns y (bf16)."""
+    M, K = a_q.shape
+    N = W_q.shape[1]
+    dev = a_q.device
+    bf, f32, i8 = torch.bfloat16, torch.float32, torch.int8
+    y = torch.empty((M, N), dtype=bf, device=dev) if y is None else y
+    if ws is None:
+        ws = workspace(coda_matmul_q8_workspace_bytes(M, K, N), dev)
+    c = _Call("coda_matmul_q8", dev)
+    c.run(_lib.coda_matmul_q8, c.t(a_q, i8, (M, K), "a_q"), c.t(a_s, f32, (M,), "a_s"),
+          c.t(W_q, i8, (K, N), "W_q"), c.t(w_s, f32, (N,), "w_s"), c.opt(z, bf, (M, N), "z"),
+          M, K, N, c.t(y, bf, (M, N), "y"), *c.ws(ws), stream=stream)
+    return y
+
+
+def coda_bwd_swiglu_dgrad_q8(dout, W2, y_q, y_s, W1, h, r, gamma, dy=None, s=None, dh=None, a=None,
+                             want_a=False, ws=None, stream=None):
+    """coda_bwd_swiglu_dgrad from an 8-bit checkpoint of the pre-activation (y_q, y_s as
+    coda_quant_q8 with block=128 gives them); returns (dy, s, dh), or (dy, s, dh, a) with
+    want_a=True (the gated activation recomputed from the checkpoint)."""
+    M, Dout = dout.shape
+    half = W2.shape[0]
+    N1 = 2 * half
+    d = W1.shape[0]
+    dev = dout.device
+    bf, f32 = torch.bfloat16, torch.float32
+    dy = torch.empty((M, N1), dtype=bf, device=dev) if dy is None else dy
+    s = torch.empty((M,), dtype=f32, device=dev) if s is None else s
+    dh = torch.empty((M, d), dtype=bf, device=dev) if dh is None else dh
+    if want_a and a is None:
+        a = torch.empty((M, half), dtype=bf, device=dev)
+    if ws is None:
+        ws = workspace(coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout), dev)
+    c = _Call("coda_bwd_swiglu_dgrad_q8", dev)
+    c.run(_lib.coda_bwd_swiglu_dgrad_q8,
+          c.t(dout, bf, (M, Dout), "dout"), c.t(W2, bf, (half, Dout), "W2"),
+          c.t(y_q, torch.int8, (M, N1), "y_q"), c.t(y_s, f32, _q8_scales(M, N1, 128), "y_s"),
+          c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"), c.t(r, f32, (M,), "r"),
+          c.t(gamma, bf, (d,), "gamma"), M, d, N1, Dout, c.t(dy, bf, (M, N1), "dy"),
+          c.t(s, f32, (M,), "s"), c.t(dh, bf, (M, d), "dh"), c.opt(a, bf, (M, half), "a"),
+          *c.ws(ws), stream=stream)
+    return (dy, s, dh, a) if a is not None else (dy, s, dh)
 
 
 def coda_bwd_workspace_bytes(M: int, d: int, N1: int) -> int:

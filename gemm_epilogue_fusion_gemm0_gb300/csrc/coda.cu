@@ -26,6 +26,7 @@
 #include "coda.h"
 #include "epilogues.cuh"
 #include "gemm_pair.cuh"
+#include "q8.cuh"
 
 namespace coda {
 
@@ -151,6 +152,10 @@ static auto* const kPairWgrad = &gemm_pair_epilogue_kernel<EpiStoreF32, true, tr
 static auto* const kXgrad = &gemm_epilogue_kernel<EpiRowScale, false>;
 static auto* const kPairXgrad = &gemm_pair_epilogue_kernel<EpiRowScale, false>;
 static auto* const kPairSwigluBwd = &gemm_pair_epilogue_kernel<EpiSwiGLUBackward, false>;
+static auto* const kSwigluBwdQ8 = &gemm_epilogue_kernel<EpiSwiGLUBackwardQ8, false>;
+static auto* const kPairSwigluBwdQ8 = &gemm_pair_epilogue_kernel<EpiSwiGLUBackwardQ8, false>;
+static auto* const kProductQ8 = &gemm_epilogue_kernel<EpiTokenChannelScale, true>;
+static auto* const kPairProductQ8 = &gemm_pair_epilogue_kernel<EpiTokenChannelScale, true>;
 static auto* const kDgradGivenS = &gemm_epilogue_kernel<EpiRmsNormBackwardGivenS, false>;
 static auto* const kPairDgradGivenS = &gemm_pair_epilogue_kernel<EpiRmsNormBackwardGivenS, false>;
 
@@ -173,6 +178,10 @@ constexpr uint32_t kPairWgradSmem = pair_smem_bytes<EpiStoreF32>();
 constexpr uint32_t kXgradSmem = cta_smem_bytes<EpiRowScale>();
 constexpr uint32_t kPairXgradSmem = pair_smem_bytes<EpiRowScale>();
 constexpr uint32_t kPairSwigluBwdSmem = pair_smem_bytes<EpiSwiGLUBackward>();
+constexpr uint32_t kSwigluBwdQ8Smem = cta_smem_bytes<EpiSwiGLUBackwardQ8>();
+constexpr uint32_t kPairSwigluBwdQ8Smem = pair_smem_bytes<EpiSwiGLUBackwardQ8>();
+constexpr uint32_t kProductQ8Smem = cta_smem_bytes<EpiTokenChannelScale>();
+constexpr uint32_t kPairProductQ8Smem = pair_smem_bytes<EpiTokenChannelScale>();
 constexpr uint32_t kDgradGivenSSmem = cta_smem_bytes<EpiRmsNormBackwardGivenS>();
 constexpr uint32_t kPairDgradGivenSSmem = pair_smem_bytes<EpiRmsNormBackwardGivenS>();
 
@@ -333,6 +342,14 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
                                  kPairXgradSmem) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kPairSwigluBwd, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kPairSwigluBwdSmem) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kSwigluBwdQ8, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSwigluBwdQ8Smem) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kPairSwigluBwdQ8, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kPairSwigluBwdQ8Smem) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kProductQ8, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kProductQ8Smem) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kPairProductQ8, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kPairProductQ8Smem) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kDgradGivenS, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kDgradGivenSSmem) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kPairDgradGivenS, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -864,6 +881,46 @@ ColPlan plan_dgrad_cols(int64_t mt, int64_t d, int64_t K, int npairs) {
   return best;
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit codes with scales (q8.cuh)
+// ---------------------------------------------------------------------------
+// M rows of n values; n a positive multiple of 8
+coda_status_t check_rows(int64_t M, int64_t n) {
+  if (M < 0 || n <= 0) return CODA_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t(1) << 31) - 256;
+  if (n % 8 != 0 || M > lim || n > lim) return CODA_ERR_UNSUPPORTED_SHAPE;
+  return CODA_OK;
+}
+
+// One scale per row: a warp per row up to 1024 columns, a block of up to 1024
+// threads holding 4 vectors of 8 values each up to 32768, a block that reads the
+// row twice beyond.
+template <bool kNorm, bool kRes>
+cudaError_t launch_row_q8(const RowQ8Params& p, cudaStream_t stream) {
+  const int nvec = p.d / 8;
+  if (nvec <= 32 * kRowQ8Vec)
+    return launch(&row_q8_kernel<kNorm, kRes, kRowQ8Vec, true>, static_cast<int>(cdiv(p.M, 8)), 256,
+                  0, stream, false, p);
+  if (nvec <= 1024 * kRowQ8Vec)
+    return launch(&row_q8_kernel<kNorm, kRes, kRowQ8Vec, false>, p.M,
+                  static_cast<int>(cdiv(nvec, 32 * kRowQ8Vec)) * 32, 0, stream, false, p);
+  return launch(&row_q8_kernel<kNorm, kRes, 0, false>, p.M, 1024, 0, stream, false, p);
+}
+
+// Thread blocks of the kernels that walk a row's blocks of 128 columns; 0: too many.
+int q8_block_grid(int64_t M, int64_t n) {
+  const int64_t grid = cdiv(M * cdiv(n, kQ8Block), kQ8UnitsPerCta);
+  return grid <= 0x7fffffff ? static_cast<int>(grid) : 0;
+}
+
+coda_status_t check_product(int64_t M, int64_t K, int64_t N) {
+  if (M < 0 || K <= 0 || N <= 0) return CODA_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t(1) << 31) - 256;
+  // 16-byte rows of one-byte codes
+  if (K % 16 != 0 || N % 16 != 0 || M > lim || K > lim || N > lim) return CODA_ERR_UNSUPPORTED_SHAPE;
+  return CODA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1229,21 +1286,26 @@ size_t coda_bwd_swiglu_dgrad_workspace_bytes(int64_t M, int64_t d, int64_t N1, i
          align256(static_cast<size_t>(ps) * 2 * 8);
 }
 
-coda_status_t coda_bwd_swiglu_dgrad(const coda_bf16* dout, const coda_bf16* W2, const coda_bf16* y,
-                                    const coda_bf16* W1, const coda_bf16* h, const float* r,
-                                    const coda_bf16* gamma, int64_t M, int64_t d, int64_t N1,
-                                    int64_t Dout, coda_bf16* dy_out, float* s_out,
-                                    coda_bf16* dh_out, void* workspace, size_t workspace_bytes,
-                                    cudaStream_t stream) {
+// The SwiGLU backward from the pre-activation saved as bf16 (y) or as an 8-bit
+// checkpoint (y_q, y_s, with a_out optionally recomputed); the other form is null.
+static coda_status_t swiglu_bwd_impl(const coda_bf16* dout, const coda_bf16* W2, const coda_bf16* y,
+                                     const int8_t* y_q, const float* y_s, const coda_bf16* W1,
+                                     const coda_bf16* h, const float* r, const coda_bf16* gamma,
+                                     int64_t M, int64_t d, int64_t N1, int64_t Dout,
+                                     coda_bf16* dy_out, float* s_out, coda_bf16* dh_out,
+                                     coda_bf16* a_out, bool q8, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream) {
   coda_status_t st = check_common(M, d, N1);
   if (st != CODA_OK) return st;
   if (Dout <= 0) return CODA_ERR_INVALID_ARG;
-  if (N1 % 16 != 0 || Dout % 8 != 0 || Dout > (int64_t(1) << 31) - 256)
+  // bf16 rows of N1 / 2 values, or code rows of N1 / 2 bytes, on 16-byte boundaries
+  if (N1 % (q8 ? 32 : 16) != 0 || Dout % 8 != 0 || Dout > (int64_t(1) << 31) - 256)
     return CODA_ERR_UNSUPPORTED_SHAPE;
   if (M == 0) return CODA_OK;
-  if (!dout || !W2 || !y || !W1 || !h || !r || !gamma || !dy_out || !s_out || !dh_out)
+  if (!dout || !W2 || !(q8 ? y_q && y_s : y != nullptr) || !W1 || !h || !r || !gamma || !dy_out ||
+      !s_out || !dh_out)
     return CODA_ERR_INVALID_ARG;
-  const void* ptrs[] = {dout, W2, y, W1, h, r, gamma, dy_out, s_out, dh_out};
+  const void* ptrs[] = {dout, W2, y, y_q, y_s, W1, h, r, gamma, dy_out, s_out, dh_out, a_out};
   for (const void* p : ptrs)
     if (!aligned16(p)) return CODA_ERR_MISALIGNED;
   if (workspace == nullptr ||
@@ -1277,12 +1339,26 @@ coda_status_t coda_bwd_swiglu_dgrad(const coda_bf16* dout, const coda_bf16* W2, 
   p0.y = reinterpret_cast<const __nv_bfloat16*>(y);
   p0.dy_out = reinterpret_cast<__nv_bfloat16*>(dy_out);
   p0.spart = reinterpret_cast<float*>(static_cast<char*>(workspace) + kSlotBytes);
-  cudaError_t e =
-      pair ? launch(kPairSwigluBwd, 2 * std::min(max_pairs, mtp * nts), kThreads,
-                    kPairSwigluBwdSmem, stream, false, mA0, mB0, Mi, halfi, Douti, kPairGroupM,
-                    p0, kNoSplitTail, kNoColPlan, tmo)
-           : launch(kSwigluBwd, std::min(sms, mt * nts), kThreads, kSwigluBwdSmem, stream, false,
-                    mA0, mB0, Mi, halfi, Douti, kGroupM, p0, tmo);
+  EpiSwiGLUBackwardQ8::Params p0q = {};
+  p0q.y_q = reinterpret_cast<const uint8_t*>(y_q);
+  p0q.y_s = y_s;
+  p0q.nb = static_cast<int>(cdiv(N1, kQ8Block));
+  p0q.dy_out = p0.dy_out;
+  p0q.a_out = reinterpret_cast<__nv_bfloat16*>(a_out);
+  p0q.spart = p0.spart;
+  cudaError_t e;
+  if (q8)
+    e = pair ? launch(kPairSwigluBwdQ8, 2 * std::min(max_pairs, mtp * nts), kThreads,
+                      kPairSwigluBwdQ8Smem, stream, false, mA0, mB0, Mi, halfi, Douti, kPairGroupM,
+                      p0q, kNoSplitTail, kNoColPlan, tmo)
+             : launch(kSwigluBwdQ8, std::min(sms, mt * nts), kThreads, kSwigluBwdQ8Smem, stream,
+                      false, mA0, mB0, Mi, halfi, Douti, kGroupM, p0q, tmo);
+  else
+    e = pair ? launch(kPairSwigluBwd, 2 * std::min(max_pairs, mtp * nts), kThreads,
+                      kPairSwigluBwdSmem, stream, false, mA0, mB0, Mi, halfi, Douti, kPairGroupM,
+                      p0, kNoSplitTail, kNoColPlan, tmo)
+             : launch(kSwigluBwd, std::min(sms, mt * nts), kThreads, kSwigluBwdSmem, stream, false,
+                      mA0, mB0, Mi, halfi, Douti, kGroupM, p0, tmo);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return CODA_ERR_LAUNCH;
@@ -1327,6 +1403,193 @@ coda_status_t coda_bwd_swiglu_dgrad(const coda_bf16* dout, const coda_bf16* W2, 
                     sk3.pieces > 0, mA1, mB1, Mi, di, N1i, kPairGroupM, p1, sk3, kNoColPlan, tmo)
            : launch(kDgradGivenS, std::min(sms, mt * ntd), kThreads, kDgradGivenSSmem, stream,
                     false, mA1, mB1, Mi, di, N1i, kGroupM, p1, tmo);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return CODA_ERR_LAUNCH;
+  }
+  after_launch(2, stream);
+  return CODA_OK;
+}
+
+coda_status_t coda_bwd_swiglu_dgrad(const coda_bf16* dout, const coda_bf16* W2, const coda_bf16* y,
+                                    const coda_bf16* W1, const coda_bf16* h, const float* r,
+                                    const coda_bf16* gamma, int64_t M, int64_t d, int64_t N1,
+                                    int64_t Dout, coda_bf16* dy_out, float* s_out,
+                                    coda_bf16* dh_out, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream) {
+  return swiglu_bwd_impl(dout, W2, y, nullptr, nullptr, W1, h, r, gamma, M, d, N1, Dout, dy_out,
+                         s_out, dh_out, nullptr, false, workspace, workspace_bytes, stream);
+}
+
+coda_status_t coda_bwd_swiglu_dgrad_q8(const coda_bf16* dout, const coda_bf16* W2,
+                                       const int8_t* y_q, const float* y_s, const coda_bf16* W1,
+                                       const coda_bf16* h, const float* r, const coda_bf16* gamma,
+                                       int64_t M, int64_t d, int64_t N1, int64_t Dout,
+                                       coda_bf16* dy_out, float* s_out, coda_bf16* dh_out,
+                                       coda_bf16* a_out, void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream) {
+  return swiglu_bwd_impl(dout, W2, nullptr, y_q, y_s, W1, h, r, gamma, M, d, N1, Dout, dy_out,
+                         s_out, dh_out, a_out, true, workspace, workspace_bytes, stream);
+}
+
+coda_status_t coda_quant_q8(const coda_bf16* x, int64_t M, int64_t n, int block, int8_t* q_out,
+                            float* s_out, cudaStream_t stream) {
+  coda_status_t st = check_rows(M, n);
+  if (st != CODA_OK) return st;
+  if (block != 0 && block != kQ8Block) return CODA_ERR_INVALID_ARG;
+  if (M == 0) return CODA_OK;
+  if (!x || !q_out || !s_out) return CODA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q_out) || !aligned16(s_out)) return CODA_ERR_MISALIGNED;
+  const int grid = q8_block_grid(M, n);
+  if (grid == 0) return CODA_ERR_UNSUPPORTED_SHAPE;
+  int sms = 0;
+  st = device_setup(&sms);
+  if (st != CODA_OK) return st;
+  cudaError_t e;
+  if (block == 0) {
+    RowQ8Params p = {};
+    p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+    p.q_out = reinterpret_cast<uint8_t*>(q_out);
+    p.s_out = s_out;
+    p.M = static_cast<int>(M);
+    p.d = static_cast<int>(n);
+    e = launch_row_q8<false, false>(p, stream);
+  } else {
+    e = launch(block_q8_kernel, grid, 256, 0, stream, false,
+               reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<uint8_t*>(q_out), s_out,
+               static_cast<int>(M), static_cast<int>(n));
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return CODA_ERR_LAUNCH;
+  }
+  after_launch(0, stream);
+  return CODA_OK;
+}
+
+coda_status_t coda_dequant_q8(const int8_t* q, const float* s, int64_t M, int64_t n, int block,
+                              coda_bf16* x_out, cudaStream_t stream) {
+  coda_status_t st = check_rows(M, n);
+  if (st != CODA_OK) return st;
+  if (block != 0 && block != kQ8Block) return CODA_ERR_INVALID_ARG;
+  if (M == 0) return CODA_OK;
+  if (!q || !s || !x_out) return CODA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(s) || !aligned16(x_out)) return CODA_ERR_MISALIGNED;
+  const int grid = q8_block_grid(M, n);
+  if (grid == 0) return CODA_ERR_UNSUPPORTED_SHAPE;
+  int sms = 0;
+  st = device_setup(&sms);
+  if (st != CODA_OK) return st;
+  const uint8_t* qb = reinterpret_cast<const uint8_t*>(q);
+  __nv_bfloat16* xb = reinterpret_cast<__nv_bfloat16*>(x_out);
+  const cudaError_t e = launch(block == 0 ? &dequant_q8_kernel<true> : &dequant_q8_kernel<false>,
+                               grid, 256, 0, stream, false, qb, s, xb, static_cast<int>(M),
+                               static_cast<int>(n));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return CODA_ERR_LAUNCH;
+  }
+  after_launch(0, stream);
+  return CODA_OK;
+}
+
+coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* z, const coda_bf16* gamma,
+                                  float eps, int64_t M, int64_t d, coda_bf16* h_out, int8_t* q_out,
+                                  float* s_out, cudaStream_t stream) {
+  coda_status_t st = check_rows(M, d);
+  if (st != CODA_OK) return st;
+  if (M == 0) return CODA_OK;
+  if (!x || !gamma || !q_out || !s_out) return CODA_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, z, gamma, h_out, q_out, s_out};  // z and h_out may be null
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return CODA_ERR_MISALIGNED;
+  int sms = 0;
+  st = device_setup(&sms);
+  if (st != CODA_OK) return st;
+  RowQ8Params p = {};
+  p.x = reinterpret_cast<const __nv_bfloat16*>(x);
+  p.z = reinterpret_cast<const __nv_bfloat16*>(z);
+  p.gamma = reinterpret_cast<const __nv_bfloat16*>(gamma);
+  p.h_out = reinterpret_cast<__nv_bfloat16*>(h_out);
+  p.q_out = reinterpret_cast<uint8_t*>(q_out);
+  p.s_out = s_out;
+  p.eps = eps;
+  p.M = static_cast<int>(M);
+  p.d = static_cast<int>(d);
+  const cudaError_t e = z ? launch_row_q8<true, true>(p, stream) : launch_row_q8<true, false>(p, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return CODA_ERR_LAUNCH;
+  }
+  after_launch(0, stream);
+  return CODA_OK;
+}
+
+// [slot | a as bf16 integers | W as bf16 integers | split-tail region]
+size_t coda_matmul_q8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  if (check_product(M, K, N) != CODA_OK || M == 0) return 0;
+  return kSlotBytes + align256(static_cast<size_t>(M) * K * 2) +
+         align256(static_cast<size_t>(K) * N * 2) + sk_region_bytes(cdiv(M, kPairBM) * cdiv(N, kBN));
+}
+
+coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* W_q,
+                             const float* w_s, const coda_bf16* z, int64_t M, int64_t K, int64_t N,
+                             coda_bf16* y_out, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+  coda_status_t st = check_product(M, K, N);
+  if (st != CODA_OK) return st;
+  if (M == 0) return CODA_OK;
+  if (!a_q || !a_s || !W_q || !w_s || !y_out) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {a_q, a_s, W_q, w_s, z, y_out};  // z may be null
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return CODA_ERR_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < coda_matmul_q8_workspace_bytes(M, K, N))
+    return CODA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(workspace)) return CODA_ERR_MISALIGNED;
+  int sms = 0, max_pairs = 0;
+  st = device_setup(&sms, &max_pairs);
+  if (st != CODA_OK) return st;
+  const bool pair = g_mma_mode.load() == 1;
+  const uint64_t tmo = g_timeout_ns.load();
+  const int Mi = static_cast<int>(M), Ki = static_cast<int>(K), Ni = static_cast<int>(N);
+
+  char* wsb = static_cast<char*>(workspace);
+  __nv_bfloat16* a = reinterpret_cast<__nv_bfloat16*>(wsb + kSlotBytes);
+  __nv_bfloat16* W =
+      reinterpret_cast<__nv_bfloat16*>(wsb + kSlotBytes + align256(static_cast<size_t>(M) * K * 2));
+  const int64_t mtp = cdiv(M, kPairBM), nt = cdiv(N, kBN);
+  const SkRegion skr = sk_region(reinterpret_cast<char*>(W) + align256(static_cast<size_t>(K) * N * 2),
+                                 mtp * nt, wsb);
+  CUtensorMap mA, mB;
+  bool ok = tmap_2d(&mA, a, K, M, kBK, kBM);  // [M, K] K-major
+  ok &= tmap_2d(&mB, W, N, K, 64, kBK);       // [K, N] MN-major
+  if (!ok) return CODA_ERR_LAUNCH;
+
+  const size_t na = static_cast<size_t>(M) * K / 16, nw = static_cast<size_t>(K) * N / 16;
+  cudaError_t e = launch(q8_to_bf16_kernel, static_cast<int>(cdiv(na, 256)), 256, 0, stream, false,
+                         reinterpret_cast<const uint8_t*>(a_q), a, na);
+  if (e == cudaSuccess) {
+    after_launch(0, stream);
+    e = launch(q8_to_bf16_kernel, static_cast<int>(cdiv(nw, 256)), 256, 0, stream, false,
+               reinterpret_cast<const uint8_t*>(W_q), W, nw);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return CODA_ERR_LAUNCH;
+  }
+  after_launch(1, stream);
+  EpiTokenChannelScale::Params p = {};
+  p.a_s = a_s;
+  p.w_s = w_s;
+  p.z = reinterpret_cast<const __nv_bfloat16*>(z);
+  p.y_out = reinterpret_cast<__nv_bfloat16*>(y_out);
+  const int units = static_cast<int>(std::min<int64_t>(max_pairs, mtp * nt));
+  const SkParams sk = plan_split_tail(skr, mtp * nt, units, cdiv(K, kBK), next_salt());
+  e = pair ? launch(kPairProductQ8, 2 * units, kThreads, kPairProductQ8Smem, stream,
+                    sk.epoch != nullptr, mA, mB, Mi, Ni, Ki, kPairGroupM, p, sk, kNoColPlan, tmo)
+           : launch(kProductQ8, static_cast<int>(std::min<int64_t>(sms, cdiv(M, kBM) * nt)), kThreads,
+                    kProductQ8Smem, stream, false, mA, mB, Mi, Ni, Ki, kGroupM, p, tmo);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return CODA_ERR_LAUNCH;

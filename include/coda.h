@@ -287,6 +287,83 @@ CODA_API coda_status_t coda_bwd(const coda_bf16* dy, const coda_bf16* x, const c
                                 float* dW0_out, float* dW1_out, void* workspace,
                                 size_t workspace_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit operators: INT8 codes with fp32 scales.
+ *
+ * A value v is held as code * scale.  Over the values that share a scale,
+ *   scale = amax / 127,   code = rint(v * 127 / amax),   amax = max |v|,
+ * code in [-127, 127], ties to even; amax = 0 gives code 0 and scale 0.  A value
+ * is then off by at most amax / 254.  Values that share a scale with an infinity
+ * or a NaN get the scale NaN (the codes are then unspecified), so that it is not
+ * lost in whatever the codes are used for.  A scale belongs to a row (block = 0,
+ * scales [M]: one per token) or to 128 columns of a row (block = 128, scales
+ * [M, ceil(n / 128)]; the last block of a row may be ragged).
+ *
+ * The chain in INT8, with scales per token and channel that follow the values (the
+ * FP8 forward's are fixed per tensor):
+ *   coda_quant_q8(x) -> coda_matmul_q8(x, W0, z) = h -> coda_add_rmsnorm_q8(h)
+ *   -> coda_matmul_q8(., W1) = y
+ * and training from 8-bit checkpoints:
+ *   coda_fwd_swiglu(y wanted) -> coda_quant_q8(y, 128), y and a dropped
+ *   -> coda_bwd_swiglu_dgrad_q8 (a recomputed).
+ * Conventions as above; these entry points take no workspace unless they name one,
+ * launch nothing for M == 0, and their results do not depend on earlier calls.
+ * ------------------------------------------------------------------------- */
+
+/* Codes and scales of a tensor.
+ *   x [M, n] bf16 in;  q_out [M, n] INT8 out;  s_out [M] or [M, ceil(n / 128)] fp32 out
+ * n a positive multiple of 8; block 0 or 128. */
+CODA_API coda_status_t coda_quant_q8(const coda_bf16* x, int64_t M, int64_t n, int block,
+                                     int8_t* q_out, float* s_out, cudaStream_t stream);
+
+/* The values that codes stand for, rounded once: x_out = bf16(code * scale).  Arguments as in
+ * coda_quant_q8.  Codes may be anything in [-128, 127]. */
+CODA_API coda_status_t coda_dequant_q8(const int8_t* q, const float* s, int64_t M, int64_t n,
+                                       int block, coda_bf16* x_out, cudaStream_t stream);
+
+/* The residual's addition and the RMS norm with an output in 8 bits, one scale per token:
+ *   h = x + z,   r = 1 / sqrt(mean_j h^2 + eps),   norm = r * h * gamma
+ *   -> h_out = bf16(h), q_out and s_out = the codes and the scale of norm
+ * h enters the norm unrounded, in fp32.  A row's sum of squares has to stay below FLT_MAX, as in
+ * coda_fwd.  A row of zeros gives codes 0 and, with eps > 0, scale 0 (NaN with eps = 0).
+ *   x [M, d] bf16 in;  z [M, d] bf16 in, may be NULL (h = x);  gamma [d] bf16 in;
+ *   h_out [M, d] bf16 out, may be NULL (not wanted);  q_out [M, d] INT8, s_out [M] fp32 out
+ * d a positive multiple of 8; eps >= 0, finite. */
+CODA_API coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* z,
+                                           const coda_bf16* gamma, float eps, int64_t M, int64_t d,
+                                           coda_bf16* h_out, int8_t* q_out, float* s_out,
+                                           cudaStream_t stream);
+
+/* Matrix product of INT8 codes with a scale per token and per channel, and optionally the
+ * residual's addition:
+ *   y[m, n] = bf16(a_s[m] * w_s[n] * sum_k a_q[m, k] * W_q[k, n] + z[m, n])
+ *   a_q [M, K] INT8, a_s [M] fp32;  W_q [K, N] INT8 ([in, out]), w_s [N] fp32;
+ *   z [M, N] bf16, may be NULL;  y_out [M, N] bf16 out
+ * K and N positive multiples of 16; codes may be anything in [-128, 127].  Sums are fp32 sums of
+ * exact products: exact while they stay below 2^24.  A NaN scale makes its row or column NaN.
+ * workspace: at least coda_matmul_q8_workspace_bytes(M, K, N). */
+CODA_API size_t coda_matmul_q8_workspace_bytes(int64_t M, int64_t K, int64_t N);
+CODA_API coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* W_q,
+                                      const float* w_s, const coda_bf16* z, int64_t M, int64_t K,
+                                      int64_t N, coda_bf16* y_out, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream);
+
+/* coda_bwd_swiglu_dgrad from an 8-bit checkpoint of the pre-activation y = [g | u]:
+ *   y_q [M, N1] INT8 codes, y_s [M, ceil(N1 / 128)] fp32 scales (coda_quant_q8 with block = 128)
+ * take y's place, and a_out ([M, N1/2] bf16, may be NULL) receives a = silu(g) * u recomputed
+ * from the checkpoint (the operand of W2's weight gradient), so that neither y nor a has to be kept
+ * from the forward: 1.03 bytes per pre-activation value instead of 3.  dy, s and dh are the
+ * gradients at the checkpoint's values of y.  N1 must be a multiple of 32 and Dout of 8; everything
+ * else, the workspace (coda_bwd_swiglu_dgrad_workspace_bytes) included, as coda_bwd_swiglu_dgrad. */
+CODA_API coda_status_t coda_bwd_swiglu_dgrad_q8(const coda_bf16* dout, const coda_bf16* W2,
+                                                const int8_t* y_q, const float* y_s,
+                                                const coda_bf16* W1, const coda_bf16* h,
+                                                const float* r, const coda_bf16* gamma, int64_t M,
+                                                int64_t d, int64_t N1, int64_t Dout,
+                                                coda_bf16* dy_out, float* s_out, coda_bf16* dh_out,
+                                                coda_bf16* a_out, void* workspace,
+                                                size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream`, then reports and clears the library's device-side
  * status word: CODA_OK, CODA_ERR_DEVICE_TIMEOUT if a bounded wait in any
  * kernel of this library ran out since the last call (raw code 0x100 | which

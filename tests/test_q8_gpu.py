@@ -1,0 +1,553 @@
+"""The 8-bit operators on the GPU against their definitions in 64 bits.
+
+Tolerances, derived from the arithmetic (u = 2^-24 is fp32's unit roundoff, 2^-8 bf16's):
+  codes   v * 127 / amax is formed with at most five fp32 roundings, so before the rounding to
+          an integer it is off by less than 127 * 6 u < 1e-4: |code - exact| <= 0.5 + 1e-4.
+  scales  amax / 127 of at most three roundings (4 u); the norm's also carries
+          1 / sqrt(mean h^2 + eps): sums of at most 4 * 8 + 10 terms in a row (block of threads) or
+          of d / 1024 + 10 terms (a row read twice), halved by the root, and rsqrt's 2 ulp.
+  values  bf16(code * scale) by the same two roundings as the same product in torch: equal.
+  product sums of exact products, exact below 2^24 and else off by one truncation (2 u) of the
+          running sum per 16 values of k; three fp32 roundings; one to bf16.
+  bwd     dy and a: fp32 sums as above, then up to ten fp32 roundings of factors of size 1 + |g|,
+          one to bf16.  s: the same before bf16, and a sum of N1 terms.  dh: the rounding of dy to
+          bf16 before the second product and of dh after it, each at most 2^-8 / sqrt(3) of the
+          value in the root mean square over many values: 3.2e-3 of the norm together.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U, UB = 2.0 ** -24, 2.0 ** -8
+BLOCK = 128
+
+
+@pytest.fixture(scope="module")
+def B():
+    import __graft_entry__ as g
+
+    g.build()
+    from gemm_epilogue_fusion_gemm0_gb300 import binding
+
+    torch.cuda.set_device(0)
+    return binding
+
+
+def clean(B):
+    st, detail = B.coda_get_device_status()
+    assert st == B.CODA_OK, (B.status_string(st), hex(detail))
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(seed, *shape, std=1.0, mean=0.0):
+    return (torch.randn(*shape, device="cuda", generator=gen(seed)) * std + mean)
+
+
+def bf(t):
+    return t.to(torch.bfloat16)
+
+
+def codes(seed, *shape, lo=-128, hi=127):
+    return torch.randint(lo, hi + 1, shape, device="cuda", dtype=torch.int8, generator=gen(seed))
+
+
+def padded(v, width):
+    """[M, n] -> [M, blocks, width] with zeros past n."""
+    return torch.nn.functional.pad(v, (0, -v.shape[1] % width)).view(v.shape[0], -1, width)
+
+
+def check_codes(q, s, v, block, scale_factor=None, rel=4 * U):
+    """q, s against the definition for the exact values v (64 bits); scale_factor [M]: what the
+    scales carry beside amax / 127."""
+    width = block or v.shape[1]
+    cut = padded(v, width)
+    amax = cut.abs().amax(2)
+    exact = cut * torch.where(amax > 0, 127.0 / amax, torch.zeros_like(amax))[:, :, None]
+    exact = exact.reshape(v.shape[0], -1)[:, :v.shape[1]]
+    assert (q.double() - exact).abs().max().item() <= 0.5 + 1e-4
+    want = amax / 127.0
+    if scale_factor is not None:
+        want = want * scale_factor[:, None]
+    got = s.double().view(want.shape)
+    assert ((got - want).abs() <= rel * want).all(), ((got - want).abs() / want).max()
+
+
+# ------------------------------------------------------------------ quantise and load again
+ROWS = [(1, 8), (3, 24), (257, 128), (5, 136), (9, 1024), (4, 1032), (33, 2056), (2, 4096),
+        (1, 28672), (3, 32768), (2, 32776), (700, 1000)]
+
+
+@pytest.mark.parametrize("block", [0, BLOCK])
+@pytest.mark.parametrize("M,n", ROWS)
+def test_quant_and_dequant(B, M, n, block):
+    x = bf(randn(M * 7 + n, M, n, std=3.0))
+    if M > 2:
+        x[1] = 0  # a padded row
+    q, s = B.coda_quant_q8(x, block=block)
+    check_codes(q, s, x.double(), block)
+    got = B.coda_dequant_q8(q, s, block=block)
+    wide = s.repeat_interleave(BLOCK, 1)[:, :n] if block else s[:, None]
+    assert torch.equal(got, bf(q.float() * wide))
+    # half a step each, and the rounding of the value to bf16
+    assert ((got.double() - x.double()).abs() <= (0.5 + 1e-4) * wide.double() + UB * x.double().abs()).all()
+    clean(B)
+
+
+@pytest.mark.parametrize("block", [0, BLOCK])
+def test_quant_of_extreme_values(B, block):
+    x = torch.zeros(8, 256, device="cuda", dtype=torch.bfloat16)
+    x[0] = 2.0 ** -133  # bf16's smallest: 127 / amax is not a float
+    x[1] = torch.linspace(-1, 1, 256, device="cuda").to(torch.bfloat16) * 2.0 ** -126
+    x[2] = 3.0e38
+    x[3, 5] = float("inf")
+    x[4, 7] = float("nan")
+    x[5, 9] = -1.0
+    x[6, 200] = float("-inf")
+    q, s = B.coda_quant_q8(x, block=block)
+    s2 = s.view(8, -1)
+    fine = [0, 1, 2, 5, 7]
+    exact = torch.round(x.double() / padded(x.double(), block or 256).abs().amax(2).clamp_min(1e-300)
+                        .repeat_interleave(block or 256, 1) * 127)
+    assert torch.equal(q[fine].double(), exact[fine])
+    assert torch.isfinite(s2[fine]).all() and (s2[7] == 0).all()
+    assert torch.isnan(s2[[3, 4], 0]).all() and torch.isnan(s2[6, -1])
+    if block:  # the other block of the row is untouched
+        assert (s2[[3, 4], 1] == 0).all() and s2[6, 0] == 0
+    back = B.coda_dequant_q8(q, s, block=block)
+    assert torch.isnan(back[3, 5]) and torch.isnan(back[4, 7]) and torch.isnan(back[6, 200])
+    clean(B)
+
+
+def test_dequant_takes_every_code(B):
+    q = torch.arange(-128, 128, device="cuda", dtype=torch.int8).view(1, 256).repeat(3, 1)
+    s = torch.tensor([1.0, 0.37, -2.0], device="cuda")
+    assert torch.equal(B.coda_dequant_q8(q, s), bf(q.float() * s[:, None]))
+
+
+# ------------------------------------------------------------------ norm
+@pytest.mark.parametrize("with_z", [False, True])
+@pytest.mark.parametrize("M,d", ROWS)
+def test_add_rmsnorm(B, M, d, with_z):
+    eps = 1e-5
+    x, z = bf(randn(M + d, M, d, std=2.0)), (bf(randn(M + d + 1, M, d)) if with_z else None)
+    gamma = bf(randn(d, d, std=0.3, mean=1.0))
+    if M > 2:
+        x[2] = 0
+        if with_z:
+            z[2] = 0
+    h, q, s = B.coda_add_rmsnorm_q8(x, gamma, eps, z=z)
+    v = x.double() + (z.double() if with_z else 0.0)
+    if with_z:
+        assert torch.equal(h, bf(x.float() + z.float()))
+    else:
+        assert h is x
+    r = 1.0 / torch.sqrt((v * v).mean(1) + eps)
+    terms = 42 if d <= 32768 else d / 1024 + 10
+    check_codes(q, s, v * gamma.double(), 0, scale_factor=r, rel=(terms / 2 + 12) * U)
+    if M > 2:
+        assert not q[2].any() and s[2] == 0
+    clean(B)
+
+
+def test_add_rmsnorm_eps_and_nonfinite(B):
+    x = bf(randn(3, 6, 512))
+    gamma = bf(randn(4, 512, std=0.3, mean=1.0))
+    x[1, 17], x[2, 400], x[3, 0] = float("nan"), float("inf"), float("-inf")
+    for eps in (0.0, 1e-5, 0.5):
+        _, q, s = B.coda_add_rmsnorm_q8(x, gamma, eps)
+        assert torch.isnan(s[1:4]).all()
+        v = x[[0, 4, 5]].double()
+        check_codes(q[[0, 4, 5]], s[[0, 4, 5]], v * gamma.double(), 0,
+                    scale_factor=1.0 / torch.sqrt((v * v).mean(1) + eps), rel=33 * U)
+    gamma[100] = float("nan")  # a NaN weight reaches every row
+    assert torch.isnan(B.coda_add_rmsnorm_q8(x, gamma, 1e-5)[2]).all()
+    clean(B)
+
+
+# ------------------------------------------------------------------ product
+PRODUCT = [(1, 16, 16), (1, 4096, 1024), (2, 48, 32), (7, 80, 144), (8, 512, 256), (9, 2064, 400),
+           (17, 1024, 272), (24, 4096, 512), (32, 144, 4096), (33, 272, 512), (48, 4096, 256),
+           (64, 640, 1296), (65, 1040, 784), (100, 64, 128), (128, 512, 512), (129, 2048, 256),
+           (200, 336, 1040), (256, 1024, 512), (257, 128, 384), (333, 4096, 784), (511, 160, 512),
+           (512, 528, 272), (513, 1024, 528), (1000, 784, 1040), (2049, 512, 784)]
+
+
+def product_ref(a_q, a_s, W_q, w_s, z):
+    t = (a_q.double() @ W_q.double()) * a_s.double()[:, None] * w_s.double()
+    return t, t + (z.double() if z is not None else 0.0)
+
+
+def check_product(y, a_q, a_s, W_q, w_s, z):
+    K = a_q.shape[1]
+    t, ref = product_ref(a_q, a_s, W_q, w_s, z)
+    mag = (a_q.double().abs() @ W_q.double().abs())
+    run = torch.where(mag < 2 ** 24, torch.zeros_like(mag), mag * (2 * U * (K / 16 + 1)))
+    tol = UB * ref.abs() + run * a_s.double().abs()[:, None] * w_s.double().abs() * (1 + UB)
+    tol = tol + 4 * U * (t.abs() + ref.abs())
+    bad = (y.double() - ref).abs() > tol
+    assert not bad.any(), (int(bad.sum()), (y.double() - ref).abs().max().item())
+
+
+@pytest.fixture(params=[0, 1], ids=["cta1", "cta2"])
+def mode(request, B):
+    old = B.coda_get_mma_mode()
+    B.coda_set_mma_mode(request.param)
+    yield request.param
+    B.coda_set_mma_mode(old)
+
+
+def product_inputs(M, K, N, with_z, seed=0):
+    a_q, W_q = codes(seed + 1, M, K), codes(seed + 2, K, N)
+    a_s = torch.rand(M, device="cuda", generator=gen(seed + 3)) + 0.01
+    w_s = torch.rand(N, device="cuda", generator=gen(seed + 4)) / K
+    return a_q, a_s, W_q, w_s, bf(randn(seed + 5, M, N)) if with_z else None
+
+
+@pytest.mark.parametrize("with_z", [False, True])
+@pytest.mark.parametrize("M,K,N", PRODUCT)
+def test_product(B, mode, M, K, N, with_z):
+    t = product_inputs(M, K, N, with_z, seed=M + K + N)
+    check_product(B.coda_matmul_q8(*t[:4], z=t[4]), *t)
+    clean(B)
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 200, 700])
+def test_product_of_extreme_codes(B, M):
+    """Every code at the range's end: the largest sums, positive and alternating."""
+    K, N = 2048, 256
+    a_q = torch.full((M, K), -128, device="cuda", dtype=torch.int8)
+    W_q = torch.full((K, N), -128, device="cuda", dtype=torch.int8)
+    W_q[::2, 1::2] = 127
+    a_q[:, 1024:] = 127
+    a_s = torch.full((M,), 2.0 ** -6, device="cuda")
+    w_s = torch.full((N,), 2.0 ** -9, device="cuda")
+    check_product(B.coda_matmul_q8(a_q, a_s, W_q, w_s), a_q, a_s, W_q, w_s, None)
+    # one-hot rows pick single rows of W: every code of W is read as it stands
+    a_q = torch.zeros(M, K, device="cuda", dtype=torch.int8)
+    at = (torch.arange(M, device="cuda") * 37 + 5) % K
+    a_q[torch.arange(M, device="cuda"), at] = 1
+    W_q = codes(77, K, N)
+    one = torch.ones(M, device="cuda")
+    assert torch.equal(B.coda_matmul_q8(a_q, one, W_q, torch.ones(N, device="cuda")), bf(W_q[at].float()))
+    clean(B)
+
+
+@pytest.mark.parametrize("M", [1, 20, 150, 600])
+def test_product_scales_zero_and_nan(B, M):
+    a_q, a_s, W_q, w_s, z = product_inputs(M, 256, 272, True, seed=9)
+    a_s[0] = 0.0
+    w_s[3] = float("nan")
+    if M > 1:
+        a_s[1] = float("nan")
+    y = B.coda_matmul_q8(a_q, a_s, W_q, w_s, z=z)
+    assert torch.isnan(y[:, 3]).all()
+    rest = [c for c in range(272) if c != 3]
+    assert torch.equal(y[0, rest], z[0, rest])
+    if M > 1:
+        assert torch.isnan(y[1]).all()
+        assert torch.isfinite(y[2:][:, rest]).all()
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 2048), (24, 1024, 512), (300, 512, 1040)])
+def test_product_is_the_same_every_time(B, M, K, N):
+    t = product_inputs(M, K, N, True, seed=4)
+    first = B.coda_matmul_q8(*t[:4], z=t[4])
+    for _ in range(3):
+        assert torch.equal(first, B.coda_matmul_q8(*t[:4], z=t[4]))
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 512, 272), (30, 512, 272), (200, 512, 272), (300, 272, 784),
+                                   (2000, 512, 272)])
+def test_product_writes_its_output_alone(B, M, K, N):
+    """Guard bytes around the output and the workspace stay as they were; the workspace's
+    contents before the call do not matter."""
+    t = product_inputs(M, K, N, True, seed=5)
+    want = B.coda_matmul_q8(*t[:4], z=t[4])
+    need = B.coda_matmul_q8_workspace_bytes(M, K, N)
+    pad = torch.full((M * N + 512,), -7.0, device="cuda", dtype=torch.bfloat16)
+    wbuf = torch.full((need + 512,), 0xA5, device="cuda", dtype=torch.uint8)
+    y = pad[256:256 + M * N].view(M, N)
+    got = B.coda_matmul_q8(*t[:4], z=t[4], y=y, ws=wbuf[256:256 + need])
+    assert torch.equal(got, want)
+    assert (pad[:256] == -7).all() and (pad[256 + M * N:] == -7).all()
+    assert (wbuf[:256] == 0xA5).all() and (wbuf[256 + need:] == 0xA5).all()
+
+
+# ------------------------------------------------------------------ backward from a checkpoint
+BWD = [(1, 8, 32, 8), (5, 64, 96, 24), (128, 256, 512, 256), (77, 264, 1376, 520),
+       (300, 328, 800, 264), (640, 512, 1536, 512), (257, 136, 1120, 72)]
+
+
+def bwd_inputs(M, d, N1, Dout, seed=0):
+    t = {"dout": bf(randn(seed + 1, M, Dout, std=0.1)),
+         "W2": bf(randn(seed + 2, N1 // 2, Dout, std=(2.0 / N1) ** 0.5)),
+         "y_q": codes(seed + 3, M, N1),
+         "y_s": torch.rand(M, -(-N1 // BLOCK), device="cuda", generator=gen(seed + 4)) * 0.03 + 0.01,
+         "W1": bf(randn(seed + 5, d, N1, std=d ** -0.5)),
+         "h": bf(randn(seed + 6, M, d, std=1.5)), "gamma": bf(randn(seed + 7, d, std=0.3, mean=1.0))}
+    t["r"] = (t["h"].float().square().mean(1) + 1e-5).rsqrt()
+    return t
+
+
+def bwd_ref(t):
+    f = {k: v.double() for k, v in t.items()}
+    N1 = f["y_q"].shape[1]
+    y = f["y_q"] * f["y_s"].repeat_interleave(BLOCK, 1)[:, :N1]
+    g, u = y[:, :N1 // 2], y[:, N1 // 2:]
+    da = f["dout"] @ f["W2"].T
+    sig = torch.sigmoid(g)
+    dy = torch.cat([da * u * sig * (1 + g * (1 - sig)), da * g * sig], 1)
+    s = (dy * y).sum(1)
+    r = f["r"][:, None]
+    dh = r * f["gamma"] * (dy @ f["W1"].T) - r * r * s[:, None] / f["h"].shape[1] * f["h"]
+    # what one rounding of each factor can do: |da| bounded by the sum of the products' sizes
+    mag = f["dout"].abs() @ f["W2"].abs().T
+    Dout = f["dout"].shape[1]
+    size = torch.cat([u.abs() * sig * (1 + g.abs()), g.abs() * sig], 1)
+    da_off = 2 * U * (Dout / 16 + 1) * torch.cat([mag, mag], 1)
+    off = size * (da_off + 16 * U * (1 + torch.cat([g, g], 1).abs()) * torch.cat([da, da], 1).abs())
+    # the logistic is 0 where exp(-g) passes 2^126 (the quotient's largest divisor): off by at most
+    # 2^-126, as is every product and rounding below the smallest normal number of fp32 and bf16
+    low = 2.0 ** -126
+    off = off + low * (1 + torch.cat([u.abs() * (1 + g.abs()), g.abs()], 1) * torch.cat([da, da], 1).abs())
+    s_off = (off * y.abs()).sum(1) + U * (N1 / 64 + 20) * (dy * y).abs().sum(1)
+    return {"dy": dy, "s": s, "dh": dh, "a": g * sig * u, "dy_off": off, "s_off": s_off,
+            "a_off": 16 * U * (1 + g.abs()) * (g * sig * u).abs() + low * (1 + (g * u).abs())}
+
+
+def check_bwd(out, ref):
+    dy, s, dh = out[:3]
+    assert ((dy.double() - ref["dy"]).abs() <= UB * ref["dy"].abs() + 1.01 * ref["dy_off"]).all()
+    assert ((s.double() - ref["s"]).abs() <= ref["s_off"]).all()
+    err = (dh.double() - ref["dh"]).norm() / ref["dh"].norm()
+    assert err <= 4e-3, err
+    # element by element: eight times the root mean square of what the roundings of dy leave
+    rms = ref["dh"].square().mean().sqrt()
+    assert ((dh.double() - ref["dh"]).abs() <= UB * ref["dh"].abs() + 8 * 2.3e-3 * rms).all()
+    if len(out) > 3:
+        assert ((out[3].double() - ref["a"]).abs() <= UB * ref["a"].abs() + 1.01 * ref["a_off"]).all()
+
+
+@pytest.mark.parametrize("want_a", [False, True])
+@pytest.mark.parametrize("M,d,N1,Dout", BWD)
+def test_bwd_from_checkpoint(B, mode, M, d, N1, Dout, want_a):
+    t = bwd_inputs(M, d, N1, Dout, seed=M)
+    out = B.coda_bwd_swiglu_dgrad_q8(*(t[k] for k in ("dout", "W2", "y_q", "y_s", "W1", "h", "r", "gamma")),
+                                     want_a=want_a)
+    assert len(out) == (4 if want_a else 3)
+    check_bwd(out, bwd_ref(t))
+    clean(B)
+
+
+def test_bwd_gradient_against_differences(B):
+    """dy against central differences, in 64 bits, of the loss sum(dout * (swiglu(y) @ W2)) at the
+    checkpoint's values y."""
+    t = bwd_inputs(3, 16, 64, 24, seed=21)
+    dy = B.coda_bwd_swiglu_dgrad_q8(*(t[k] for k in ("dout", "W2", "y_q", "y_s", "W1", "h", "r", "gamma")))[0]
+    y = (t["y_q"].double() * t["y_s"].double().repeat_interleave(BLOCK, 1)[:, :64]).cpu()
+    W2, dout = t["W2"].double().cpu(), t["dout"].double().cpu()
+
+    def loss(v):
+        g, u = v[:, :32], v[:, 32:]
+        return (dout * ((g * torch.sigmoid(g) * u) @ W2)).sum(1)
+
+    step = 1e-5
+    off = bwd_ref(t)["dy_off"].cpu()
+    for j in range(64):
+        e = torch.zeros_like(y)
+        e[:, j] = step
+        want = (loss(y + e) - loss(y - e)) / (2 * step)
+        # a central difference is off by step^2 / 6 times the third derivative (below 100 here)
+        assert ((dy[:, j].double().cpu() - want).abs() <= UB * want.abs() + 1.01 * off[:, j] + 2e-8).all()
+
+
+def test_bwd_agrees_with_the_bf16_form(B, mode):
+    """Codes that are small integers and power-of-two scales give y exactly in bf16: the two
+    entry points then compute the same gradients from the same values."""
+    M, d, N1, Dout = 300, 328, 1088, 264
+    t = bwd_inputs(M, d, N1, Dout, seed=33)
+    t["y_q"] = codes(3, M, N1, lo=-100, hi=100)
+    t["y_s"] = 2.0 ** torch.randint(-7, -4, t["y_s"].shape, device="cuda", generator=gen(8)).float()
+    y = bf(t["y_q"].float() * t["y_s"].repeat_interleave(BLOCK, 1)[:, :N1])
+    q8 = B.coda_bwd_swiglu_dgrad_q8(*(t[k] for k in ("dout", "W2", "y_q", "y_s", "W1", "h", "r", "gamma")))
+    b16 = B.coda_bwd_swiglu_dgrad(t["dout"], t["W2"], y, t["W1"], t["h"], t["r"], t["gamma"])
+    for got, want in zip(q8, b16):
+        assert torch.equal(got, want)
+
+
+def test_bwd_saturated_gates(B):
+    """Gates far out on both sides: exp overflows on one, the logistic rounds to 1 on the other."""
+    M, d, N1, Dout = 20, 64, 512, 64
+    t = bwd_inputs(M, d, N1, Dout, seed=2)
+    t["y_s"][:, 0], t["y_s"][:, 1] = 2.0, 0.5
+    out = B.coda_bwd_swiglu_dgrad_q8(*(t[k] for k in ("dout", "W2", "y_q", "y_s", "W1", "h", "r", "gamma")),
+                                     want_a=True)
+    check_bwd(out, bwd_ref(t))
+
+
+# ------------------------------------------------------------------ together
+def test_int8_chain(B):
+    """The chain in INT8 as a server runs it: quantise, product with the residual, norm, product.
+    Each step is held to its own definition on the step before's outputs, the whole to the chain in
+    64 bits: every quantised operand is off by at most half a step, amax / 254 of its row, uniformly
+    spread (amax / 254 / sqrt(3) in the root mean square), which a row's norm of size
+    rms * sqrt(K) passes on to a product in proportion."""
+    for M in (1, 3, 33, 300):
+        d, N1, eps = 512, 1024, 1e-5
+        x, z = bf(randn(1, M, d)), bf(randn(2, M, d))
+        W0, W1 = bf(randn(3, d, d, std=d ** -0.5)), bf(randn(4, d, N1, std=d ** -0.5))
+        gamma = bf(randn(5, d, std=0.1, mean=1.0))
+        W0_q, w0_s = (t.contiguous() for t in B.coda_quant_q8(W0.t().contiguous()))
+        W1_q, w1_s = (t.contiguous() for t in B.coda_quant_q8(W1.t().contiguous()))
+        W0_q, W1_q = W0_q.t().contiguous(), W1_q.t().contiguous()
+        x_q, x_s = B.coda_quant_q8(x)
+        h = B.coda_matmul_q8(x_q, x_s, W0_q, w0_s, z=z)
+        _, n_q, n_s = B.coda_add_rmsnorm_q8(h, gamma, eps)
+        y = B.coda_matmul_q8(n_q, n_s, W1_q, w1_s)
+        clean(B)
+        check_product(h, x_q, x_s, W0_q, w0_s, z)
+        check_product(y, n_q, n_s, W1_q, w1_s, None)
+        hd = x.double() @ W0.double() + z.double()
+        norm = hd / torch.sqrt((hd * hd).mean(1, keepdim=True) + eps) * gamma.double()
+        ref = norm @ W1.double()
+        # four quantised operands with amax below 4.5 of their root mean square: 4.5 / 254 / sqrt(3)
+        # each, h's bf16 and y's: sqrt(4 * 0.0103^2 + 2 * 0.0023^2) = 0.021, a quarter more for M = 1
+        assert ((y.double() - ref).norm() / ref.norm()).item() <= 0.026
+
+
+def test_training_step_from_checkpoint(B):
+    """Forward with its pre-activation saved in 8 bits, y and a dropped, backward from the
+    checkpoint with a recomputed; the residual stream's checkpoint loaded for the full backward."""
+    M, d, N1, Dout, eps = 200, 256, 1024, 256, 1e-5
+    x, z = bf(randn(1, M, d)), bf(randn(2, M, d))
+    W0, W1 = bf(randn(3, d, d, std=d ** -0.5)), bf(randn(4, d, N1, std=d ** -0.5))
+    W2, dout = bf(randn(6, N1 // 2, Dout, std=(2 / N1) ** 0.5)), bf(randn(7, M, Dout, std=0.1))
+    gamma = bf(randn(5, d, std=0.1, mean=1.0))
+    h, r, a, y = B.coda_fwd_swiglu(x, W0, z, gamma, W1, eps, want_y=True)
+    y_q, y_s = B.coda_quant_q8(y, block=BLOCK)
+    h_q, h_s = B.coda_quant_q8(h, block=BLOCK)
+    dy, s, dh, a2 = B.coda_bwd_swiglu_dgrad_q8(dout, W2, y_q, y_s, W1, h, r, gamma, want_a=True)
+    t = {"dout": dout, "W2": W2, "y_q": y_q, "y_s": y_s, "W1": W1, "h": h, "gamma": gamma, "r": r}
+    check_bwd((dy, s, dh, a2), bwd_ref(t))
+    # against the gradients at the values before the checkpoint: half a step of 1/127 of a block's
+    # largest (at most 4.5 of its root mean square), uniformly spread, through factors of size one
+    dy0, s0, dh0 = B.coda_bwd_swiglu_dgrad(dout, W2, y, W1, h, r, gamma)
+    for got, want in ((dy, dy0), (dh, dh0), (a2, a)):
+        assert ((got.double() - want.double()).norm() / want.double().norm()).item() <= 0.03
+    g0 = B.coda_bwd(dy0, x, W0, W1, h, r, gamma)
+    g1 = B.coda_bwd(dy, x, W0, W1, B.coda_dequant_q8(h_q, h_s, block=BLOCK), r, gamma)
+    for k in g0:
+        assert ((g1[k].double() - g0[k].double()).norm() / g0[k].double().norm()).item() <= 0.05, k
+    clean(B)
+
+
+# ------------------------------------------------------------------ streams, graphs, devices
+def _all_ops(B, t, p, stream=None):
+    q, s = B.coda_quant_q8(t["h"], block=BLOCK, stream=stream)
+    x = B.coda_dequant_q8(q, s, block=BLOCK, stream=stream)
+    h, nq, ns = B.coda_add_rmsnorm_q8(t["h"], t["gamma"], 1e-5, z=x, stream=stream)
+    y = B.coda_matmul_q8(*p[:4], z=p[4], stream=stream)
+    b = B.coda_bwd_swiglu_dgrad_q8(*(t[k] for k in ("dout", "W2", "y_q", "y_s", "W1", "h", "r", "gamma")),
+                                   want_a=True, stream=stream)
+    return [q, s, x, h, nq, ns, y, *b]
+
+
+@pytest.mark.parametrize("M", [1, 24, 150, 400])
+def test_on_another_stream_and_from_a_graph(B, M):
+    t, p = bwd_inputs(M, 264, 608, 136, seed=1), product_inputs(M, 528, 272, True, seed=2)
+    want = _all_ops(B, t, p)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = _all_ops(B, t, p, stream=side)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _all_ops(B, t, p)
+    for seed in (3, 4):  # replayed on other inputs
+        t2, p2 = bwd_inputs(M, 264, 608, 136, seed=seed), product_inputs(M, 528, 272, True, seed=seed)
+        for k in t:
+            t[k].copy_(t2[k])
+        for a, b in zip(p, p2):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, _all_ops(B, t2, p2)):
+            assert torch.equal(a, b)
+    clean(B)
+
+
+@pytest.mark.parametrize("M", [2, 130])
+def test_two_streams_at_once(B, M):
+    """The same product on two streams, each with a workspace of its own, back to back."""
+    shapes = (M, 2048, 1024)
+    p = [product_inputs(*shapes, True, seed=i) for i in (1, 2)]
+    want = [B.coda_matmul_q8(*t[:4], z=t[4]) for t in p]
+    need = B.coda_matmul_q8_workspace_bytes(*shapes)
+    ws = [B.workspace(need, "cuda") for _ in p]
+    ys = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in p]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, t in enumerate(p):
+            B.coda_matmul_q8(*t[:4], z=t[4], y=ys[i], ws=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for a, b in zip(ys, want):
+        assert torch.equal(a, b)
+
+
+def test_binding_refusals(B):
+    x = bf(randn(1, 8, 64))
+    q, s = B.coda_quant_q8(x)
+    with pytest.raises(ValueError):
+        B.coda_quant_q8(bf(randn(1, 64, 8)).t())  # not contiguous
+    with pytest.raises(TypeError):
+        B.coda_quant_q8(x.float())
+    with pytest.raises(ValueError):
+        B.coda_dequant_q8(q, s, block=BLOCK)  # scales of another shape
+    with pytest.raises(B.CodaError):
+        B.coda_quant_q8(bf(randn(1, 4, 12)))
+    W = codes(1, 64, 32)
+    ws = torch.ones(32, device="cuda")
+    with pytest.raises(ValueError):
+        B.coda_matmul_q8(q, s, codes(1, 48, 32), ws)  # K differs
+    with pytest.raises(ValueError):
+        B.coda_matmul_q8(q, s, W, ws[:16])
+    with pytest.raises(TypeError):
+        B.coda_matmul_q8(q.to(torch.uint8), s, W, ws)
+    with pytest.raises(B.CodaError):
+        B.coda_matmul_q8(q, s, W, ws, ws=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    empty = B.coda_matmul_q8(q[:0], s[:0], W, ws)
+    assert empty.shape == (0, 32)
+    assert B.coda_add_rmsnorm_q8(x[:0], x[0], 1e-5)[1].shape == (0, 64)
+
+
+def test_long_offsets(B):
+    """More than 2^31 values in one tensor: offsets that pass 32 bits."""
+    M, n = 262152, 8320
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    x = torch.zeros(M, n, device="cuda", dtype=torch.bfloat16)
+    tail = bf(randn(5, 16, n))
+    x[-16:] = tail
+    for block in (0, BLOCK):
+        q, s = B.coda_quant_q8(x, block=block)
+        check_codes(q[-16:], s[-16:], tail.double(), block)
+        assert not q[:64].any()
+        back = B.coda_dequant_q8(q, s, block=block)
+        assert torch.equal(back[-16:], B.coda_dequant_q8(q[-16:].clone(), s[-16:].clone(), block=block))
+        del q, s, back
+    gamma = torch.ones(n, device="cuda", dtype=torch.bfloat16)
+    h, q, s = B.coda_add_rmsnorm_q8(x, gamma, 1e-5, z=x)
+    h2, q2, s2 = B.coda_add_rmsnorm_q8(tail, gamma, 1e-5, z=tail)
+    assert torch.equal(h[-16:], h2) and torch.equal(q[-16:], q2) and torch.equal(s[-16:], s2)
+    clean(B)
