@@ -140,6 +140,12 @@ def _dev(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> int:
     return t.data_ptr()
 
 
+# The current stream's raw handle without building a torch.cuda.Stream object (2 us of a call's
+# host time on Grace); the public route where this torch does not have it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Call:
     """Marshalling for one call: every tensor must be a contiguous CUDA tensor
     of the stated dtype and shape on the device of the call's first tensor,
@@ -147,10 +153,17 @@ class _Call:
     current device, so a tensor on another one would hand the kernels a
     pointer they cannot use)."""
 
+    __slots__ = ("where", "device", "index")
+
     def __init__(self, where: str, device: torch.device):
-        self.where, self.device = where, torch.device(device)
+        self.where, self.device = where, device
+        self.index = device.index if device.type == "cuda" else None
 
     def t(self, t, dtype, shape, name) -> int:
+        # the common case in few steps; anything else is told apart (and raised) below
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                and t.is_contiguous() and t.get_device() == self.index):
+            return t.data_ptr()
         p = _dev(t, dtype, shape, name)
         if t.device != self.device:
             raise ValueError(f"{self.where}: {name} is on {t.device}, the call's first tensor on "
@@ -163,17 +176,20 @@ class _Call:
     def ws(self, ws) -> tuple:
         if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
             raise TypeError(f"{self.where}: the workspace must be a contiguous CUDA tensor")
-        if ws.device != self.device:
+        if ws.get_device() != self.index:
             raise ValueError(f"{self.where}: the workspace is on {ws.device}, the call's first "
                              f"tensor on {self.device}")
         return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def run(self, fn, *args, stream=None) -> None:
-        if self.device.index == torch.cuda.current_device():
-            _check(fn(*args, _stream_ptr(stream, self.device)), self.where)
-            return
-        with torch.cuda.device(self.device):
-            _check(fn(*args, _stream_ptr(stream, self.device)), self.where)
+        if self.index == torch.cuda.current_device():
+            st = fn(*args, _raw_stream(self.index) if stream is None
+                    else _stream_ptr(stream, self.device))
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(*args, _stream_ptr(stream, self.device))
+        if st != CODA_OK:
+            raise CodaError(st, self.where)
 
 
 # --------------------------------------------------------------------------- sizes
