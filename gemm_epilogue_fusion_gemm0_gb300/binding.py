@@ -406,18 +406,20 @@ def coda_matmul_q8_workspace_bytes(M: int, K: int, N: int) -> int:
 
 def coda_matmul_q8(a_q, a_s, W_q, w_s, z=None, y=None, ws=None, stream=None):
     """INT8 product y = a_s * w_s * (a_q @ W_q) (+ z), a scale per token (a_s [M]) and per channel
-    (w_s [N]); W_q [K, N]; returns y (bf16)."""
+    (w_s [N]); W_q [K, N]; returns y (bf16).  No workspace is needed (or looked at) where
+    coda_matmul_q8_workspace_bytes is 0."""
     M, K = a_q.shape
     N = W_q.shape[1]
     dev = a_q.device
     bf, f32, i8 = torch.bfloat16, torch.float32, torch.int8
     y = torch.empty((M, N), dtype=bf, device=dev) if y is None else y
-    if ws is None:
-        ws = workspace(coda_matmul_q8_workspace_bytes(M, K, N), dev)
     c = _Call("coda_matmul_q8", dev)
+    need = _lib.coda_matmul_q8_workspace_bytes(M, K, N)
+    if need and ws is None:
+        ws = workspace(need, dev)
     c.run(_lib.coda_matmul_q8, c.t(a_q, i8, (M, K), "a_q"), c.t(a_s, f32, (M,), "a_s"),
           c.t(W_q, i8, (K, N), "W_q"), c.t(w_s, f32, (N,), "w_s"), c.opt(z, bf, (M, N), "z"),
-          M, K, N, c.t(y, bf, (M, N), "y"), *c.ws(ws), stream=stream)
+          M, K, N, c.t(y, bf, (M, N), "y"), *(c.ws(ws) if need else (None, 0)), stream=stream)
     return y
 
 

@@ -13,6 +13,8 @@
 #include <atomic>
 #include <chrono>
 #include <cmath>
+#include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -27,6 +29,8 @@
 #include "epilogues.cuh"
 #include "gemm_pair.cuh"
 #include "q8.cuh"
+#include "q8_mid.cuh"
+#include "q8_small.cuh"
 
 namespace coda {
 
@@ -156,6 +160,11 @@ static auto* const kSwigluBwdQ8 = &gemm_epilogue_kernel<EpiSwiGLUBackwardQ8, fal
 static auto* const kPairSwigluBwdQ8 = &gemm_pair_epilogue_kernel<EpiSwiGLUBackwardQ8, false>;
 static auto* const kProductQ8 = &gemm_epilogue_kernel<EpiTokenChannelScale, true>;
 static auto* const kPairProductQ8 = &gemm_pair_epilogue_kernel<EpiTokenChannelScale, true>;
+static auto* const kProductSmall1 = &product_q8_small_kernel<1>;  // groups of 8 tokens
+static auto* const kProductSmall2 = &product_q8_small_kernel<2>;
+static auto* const kProductSmall4 = &product_q8_small_kernel<4>;
+static auto* const kProductMid = &product_q8_mid_kernel<false>;
+static auto* const kProductNarrow = &product_q8_mid_kernel<true>;
 static auto* const kDgradGivenS = &gemm_epilogue_kernel<EpiRmsNormBackwardGivenS, false>;
 static auto* const kPairDgradGivenS = &gemm_pair_epilogue_kernel<EpiRmsNormBackwardGivenS, false>;
 
@@ -229,6 +238,7 @@ struct DevState {
   int sms = 0;
   int max_pairs = 0;  // co-resident clusters of two for the CTA-pair kernels
   void* noalloc_scratch = nullptr;  // device address of g_noalloc_dgrad_scratch on this device
+  int mid_clusters[2][3] = {};  // co-resident clusters of 2, 4, 8 of the mid-size product; narrow
 };
 
 std::mutex g_mu;
@@ -284,7 +294,8 @@ uint64_t next_salt() {
 // the library's device code on this device, the static scratch array of the
 // no-allocation entry point included) and looks up the device address of that
 // array, so that whichever entry point runs first on a device does both.
-coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_scratch = nullptr) {
+coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_scratch = nullptr,
+                           const int (**mid_clusters)[3] = nullptr) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
@@ -350,6 +361,16 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
                                  kProductQ8Smem) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kPairProductQ8, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kPairProductQ8Smem) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kProductSmall1, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SmallSmem<1>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kProductSmall2, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SmallSmem<2>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kProductSmall4, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 SmallSmem<4>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kProductMid, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 MidShape<false>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(kProductNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 MidShape<true>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kDgradGivenS, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kDgradGivenSSmem) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kPairDgradGivenS, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -364,6 +385,25 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
           s.max_pairs = std::min(clusters, count / 2);
         else
           ok = false;
+      }
+      for (int i = 0; ok && i < 3; ++i) {  // a cluster stays in one GPC: fewer than the SMs hold
+        cudaLaunchAttribute attr = {};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2u << i;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(count) >> (i + 1) << (i + 1));
+        cfg.blockDim = dim3(kMidThreads);
+        cfg.dynamicSmemBytes = MidShape<false>::kBytes;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        ok = cudaOccupancyMaxActiveClusters(&n, kProductMid, &cfg) == cudaSuccess && n > 0;
+        s.mid_clusters[0][i] = n;
+        // Two narrow blocks share an SM (112 pairs of 32 tokens ran in one wave, 30 us, where one
+        // block per SM takes two, 39 us); the occupancy query, which knows no tensor memory,
+        // answers one.
+        s.mid_clusters[1][i] = 2 * n;
       }
       if (g_encode == nullptr) {
         void* fn = nullptr;
@@ -395,6 +435,7 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
   *sms = s.sms;
   if (max_pairs) *max_pairs = s.max_pairs;
   if (noalloc_scratch) *noalloc_scratch = s.noalloc_scratch;
+  if (mid_clusters) *mid_clusters = s.mid_clusters;  // fixed once set
   return s.status;
 }
 
@@ -411,30 +452,31 @@ bool tmap_2d(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D tensor map over a row-major [outer, inner] matrix of 1-byte (FP8) codes,
-// 128-byte swizzle.
+// 2-D tensor map over a row-major [outer, inner] matrix of 1-byte (FP8, INT8) codes,
+// 128-byte swizzle by default.
 bool tmap_2d_u8(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer,
-                uint32_t box_inner, uint32_t box_outer) {
+                uint32_t box_inner, uint32_t box_outer,
+                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {inner};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename... ExpT, typename... ActT>
-cudaError_t launch(void (*kernel)(ExpT...), int grid, int block, size_t smem, cudaStream_t stream,
-                   bool cooperative, ActT&&... args) {
+cudaError_t launch_cluster(void (*kernel)(ExpT...), int grid, int block, size_t smem,
+                           cudaStream_t stream, bool cooperative, int cluster, ActT&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   // programmatic dependent launch for every kernel (griddep_wait in ptx.cuh)
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[3];
   int na = 0;
   attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[na].val.programmaticStreamSerializationAllowed = 1;
@@ -444,9 +486,22 @@ cudaError_t launch(void (*kernel)(ExpT...), int grid, int block, size_t smem, cu
     attr[na].val.cooperative = 1;
     ++na;
   }
+  if (cluster > 1) {  // blocks per cluster, for the kernels that do not fix it themselves
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = cluster;
+    attr[na].val.clusterDim.y = attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
   cfg.attrs = attr;
   cfg.numAttrs = na;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<ActT>(args)...);
+}
+
+template <typename... ExpT, typename... ActT>
+cudaError_t launch(void (*kernel)(ExpT...), int grid, int block, size_t smem, cudaStream_t stream,
+                   bool cooperative, ActT&&... args) {
+  return launch_cluster(kernel, grid, block, smem, stream, cooperative, 1,
+                        std::forward<ActT>(args)...);
 }
 
 coda_status_t check_common(int64_t M, int64_t d, int64_t N1) {
@@ -919,6 +974,121 @@ coda_status_t check_product(int64_t M, int64_t K, int64_t N) {
   // 16-byte rows of one-byte codes
   if (K % 16 != 0 || N % 16 != 0 || M > lim || K > lim || N > lim) return CODA_ERR_UNSUPPORTED_SHAPE;
   return CODA_OK;
+}
+
+// Blocks along K (a cluster) of the few-token product: as many as one wave of `slots`
+// blocks holds.  A wave more costs more than the idle slots (N = 28672, K = 4096, one token:
+// 224 blocks 25 us, 448 in two waves 28 us, 896 33 us; N = 4096: 32 blocks 12 us, 256 7 us).
+int small_split(int64_t K, int64_t N, int slots) {
+  const int64_t tiles = cdiv(N, kSmallChannels), steps = cdiv(K, kSmallStep);
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= slots && steps >= 2 * s * kSmallWarps) s *= 2;
+  return s;
+}
+
+cudaError_t launch_product_small(const SmallQ8Params& p, const uint8_t* a_q, const uint8_t* W_q,
+                                 int sms, cudaStream_t stream) {
+  const int groups = p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4;
+  const int split = small_split(p.K, p.N, groups <= 2 ? 2 * sms : sms);
+  CUtensorMap mW, mA;
+  if (!tmap_2d_u8(&mW, W_q, p.N, p.K, kSmallChannels, kSmallStep) ||
+      !tmap_2d_u8(&mA, a_q, p.K, p.M, kSmallStep, 8 * groups, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  const int64_t grid = cdiv(p.N, kSmallChannels) * split;
+  auto* const kernel = groups == 1 ? kProductSmall1 : groups == 2 ? kProductSmall2 : kProductSmall4;
+  const uint32_t smem = groups == 1   ? SmallSmem<1>::kBytes
+                        : groups == 2 ? SmallSmem<2>::kBytes
+                                      : SmallSmem<4>::kBytes;
+  return launch_cluster(kernel, static_cast<int>(grid), 32 * kSmallWarps, smem, stream, false, split,
+                        mW, mA, p, split, g_timeout_ns.load());
+}
+
+// The INT8 product's three kernels.
+//   few tokens (q8_small.cuh)    up to 16 tokens, and up to 32 while W is small: measured with 32
+//                                tokens, W of 17 MB 10.1 us against 12.2 for the mid-size kernel, 59 MB
+//                                20.9 against 19.6
+//   mid-size (q8_mid.cuh)        up to kMidSure tokens, and beyond while its estimate is the lower one
+//   whole GEMM                   a and W widened to bf16 in the workspace first
+constexpr int64_t kMidSure = 1024;  // 1024 x 4096 x 14336: 86 us against 100
+
+bool product_small(int64_t M, int64_t K, int64_t N) {
+  return M <= 16 || (M <= kSmallMaxTokens && K * N < (int64_t(3) << 24));
+}
+
+// Time of the whole-GEMM form: widening at 6.2 bytes per ps (1 read, 2 written per code), waves
+// of 256 x 256 tiles at 333 ns per 64 rows of K, about 7 us of launches and ends.
+double product_gemm_ns(int64_t M, int64_t K, int64_t N, int pairs) {
+  return 3.0 * (static_cast<double>(M) * K + static_cast<double>(K) * N) / 6200.0 +
+         333.0 * static_cast<double>(cdiv(cdiv(M, kPairBM) * cdiv(N, kBN), pairs) * cdiv(K, kBK)) +
+         7000.0;
+}
+
+// Tokens per CTA pair, pairs along K and blocks per SM of the mid-size product: those with the
+// least estimated time, waves of clusters times a cluster's.  Measured on GB300: a step of 64 rows
+// takes 1.33 ns per token and at least 200 ns (q8_mid.cuh; two blocks on an SM 186 ns each, their
+// share of HBM), a pair's start and its sums' way out about 3 us and 10 ns per token, a split's
+// exchange 2 us and 10 ns per token more.
+struct MidPlan {
+  int tokens, split;
+  bool narrow;
+  double ns;
+};
+
+MidPlan plan_mid(int64_t M, int64_t K, int64_t N, const int (*clusters)[3]) {
+  const int64_t ct = cdiv(N, 2 * kMidChannels), nk = cdiv(K, kMidK);
+  MidPlan best = {0, 1, false, 1e30};
+  const int64_t mt0 = cdiv(M, kMidMaxTokens);
+  for (int64_t mt = mt0; mt <= mt0 + 3; ++mt) {
+    int64_t tokens = cdiv(cdiv(M, mt), 16) * 16;
+    if (tokens > 256) tokens = cdiv(tokens, 32) * 32;
+    const double t = static_cast<double>(tokens);
+    for (int i = 0, s = 1; s <= kMidMaxSplit; ++i, s *= 2) {
+      if (s > 1 && nk < 4 * s) break;
+      const int64_t tiles = ct * cdiv(M, tokens);
+      for (int narrow = 0; narrow < 2; ++narrow) {
+        // a narrow block alone on its SM is a wide one with shorter rings
+        if (narrow && (tokens > MidShape<true>::kTokens || tiles <= clusters[0][i])) break;
+        const double step = narrow ? 2.0 * std::max(1.33 * t, 186.0) : std::max(1.33 * t, 200.0);
+        const double pair = static_cast<double>(cdiv(nk, s)) * step + 3000.0 + 10.0 * t +
+                            (s > 1 ? 2000.0 + 10.0 * t : 0.0);
+        const double ns = static_cast<double>(cdiv(tiles, clusters[narrow][i])) * pair;
+        if (ns < 0.98 * best.ns) best = {static_cast<int>(tokens), s, narrow != 0, ns};
+      }
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t* W_q, void* x16,
+                               const MidPlan& plan, cudaStream_t stream) {
+  p.tokens = plan.tokens;
+  p.split = plan.split;
+  p.parts = p.tokens > 256 ? 2 : 1;
+  // The rings: as many of the tokens' stages as tensor memory has slots for, W's ring the rest.
+  const int x_stage = p.tokens * kMidK;  // bytes of a CTA's half
+  const int slots =
+      std::min(kMidMaxSlots, (static_cast<int>(plan.narrow ? MidShape<true>::kCols
+                                                           : MidShape<false>::kCols) -
+                              (p.tokens + 31) / 32 * 32) / 32);
+  p.pairs_slots = slots / 2;
+  const uint32_t rings = plan.narrow ? MidShape<true>::kRings : MidShape<false>::kRings;
+  p.pairs_w = std::min<int>(kMidMaxStages,
+                            (rings - 2 * p.pairs_slots * x_stage) / kMidWBytes) / 2;
+  CUtensorMap mW, mX;
+  if (!tmap_2d_u8(&mW, W_q, p.N, p.K, kMidChannels, kMidK) ||
+      !tmap_2d(&mX, x16, p.K, p.M, kMidK, p.tokens / p.parts / 2))
+    return cudaErrorInvalidValue;
+  const size_t n16 = static_cast<size_t>(p.M) * p.K / 16;
+  cudaError_t e = launch(q8_to_f16_kernel, static_cast<int>(cdiv(n16, 256)), 256, 0, stream, false,
+                         a_q, static_cast<uint4*>(x16), n16);
+  if (e != cudaSuccess) return e;
+  after_launch(0, stream);
+  const int64_t grid = cdiv(p.N, 2 * kMidChannels) * cdiv(p.M, p.tokens) * 2 * p.split;
+  e = launch_cluster(plan.narrow ? kProductNarrow : kProductMid, static_cast<int>(grid), kMidThreads,
+                     plan.narrow ? MidShape<true>::kBytes : MidShape<false>::kBytes, stream, false,
+                     2 * p.split, mW, mX, p, g_timeout_ns.load());
+  if (e == cudaSuccess) after_launch(1, stream);
+  return e;
 }
 
 }  // namespace
@@ -1526,9 +1696,11 @@ coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* z, const 
   return CODA_OK;
 }
 
-// [slot | a as bf16 integers | W as bf16 integers | split-tail region]
+// Nothing for few tokens; [slot | a as fp16 integers] up to kMidSure; then
+// [slot | a as bf16 (or fp16) integers | W as bf16 integers | split-tail region]
 size_t coda_matmul_q8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (check_product(M, K, N) != CODA_OK || M == 0) return 0;
+  if (check_product(M, K, N) != CODA_OK || product_small(M, K, N)) return 0;
+  if (M <= kMidSure) return kSlotBytes + align256(static_cast<size_t>(M) * K * 2);
   return kSlotBytes + align256(static_cast<size_t>(M) * K * 2) +
          align256(static_cast<size_t>(K) * N * 2) + sk_region_bytes(cdiv(M, kPairBM) * cdiv(N, kBN));
 }
@@ -1544,17 +1716,56 @@ coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* 
   const void* ptrs[] = {a_q, a_s, W_q, w_s, z, y_out};  // z may be null
   for (const void* p : ptrs)
     if (!aligned16(p)) return CODA_ERR_MISALIGNED;
-  if (workspace == nullptr || workspace_bytes < coda_matmul_q8_workspace_bytes(M, K, N))
+  const size_t need = coda_matmul_q8_workspace_bytes(M, K, N);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return CODA_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned16(workspace)) return CODA_ERR_MISALIGNED;
   int sms = 0, max_pairs = 0;
-  st = device_setup(&sms, &max_pairs);
+  const int (*clusters)[3] = nullptr;
+  st = device_setup(&sms, &max_pairs, nullptr, &clusters);
   if (st != CODA_OK) return st;
   const bool pair = g_mma_mode.load() == 1;
   const uint64_t tmo = g_timeout_ns.load();
   const int Mi = static_cast<int>(M), Ki = static_cast<int>(K), Ni = static_cast<int>(N);
 
+  if (product_small(M, K, N)) {
+    SmallQ8Params sp = {};
+    sp.a_s = a_s;
+    sp.w_s = w_s;
+    sp.z = reinterpret_cast<const __nv_bfloat16*>(z);
+    sp.y = reinterpret_cast<__nv_bfloat16*>(y_out);
+    sp.M = Mi;
+    sp.K = Ki;
+    sp.N = Ni;
+    if (launch_product_small(sp, reinterpret_cast<const uint8_t*>(a_q),
+                             reinterpret_cast<const uint8_t*>(W_q), sms, stream) != cudaSuccess) {
+      cudaGetLastError();
+      return CODA_ERR_LAUNCH;
+    }
+    after_launch(0, stream);
+    return CODA_OK;
+  }
   char* wsb = static_cast<char*>(workspace);
+  // the mid-size form also widens the tokens: 3 us and their bytes
+  const MidPlan plan = plan_mid(M, K, N, clusters);
+  if (M <= kMidSure || plan.ns + 3000.0 + 3.0 * static_cast<double>(M) * K / 6200.0 <
+                           product_gemm_ns(M, K, N, max_pairs)) {
+    MidQ8Params mp = {};
+    mp.a_s = a_s;
+    mp.w_s = w_s;
+    mp.z = reinterpret_cast<const __nv_bfloat16*>(z);
+    mp.y = reinterpret_cast<__nv_bfloat16*>(y_out);
+    mp.M = Mi;
+    mp.K = Ki;
+    mp.N = Ni;
+    if (launch_product_mid(mp, reinterpret_cast<const uint8_t*>(a_q),
+                           reinterpret_cast<const uint8_t*>(W_q), wsb + kSlotBytes, plan,
+                           stream) != cudaSuccess) {
+      cudaGetLastError();
+      return CODA_ERR_LAUNCH;
+    }
+    return CODA_OK;
+  }
   __nv_bfloat16* a = reinterpret_cast<__nv_bfloat16*>(wsb + kSlotBytes);
   __nv_bfloat16* W =
       reinterpret_cast<__nv_bfloat16*>(wsb + kSlotBytes + align256(static_cast<size_t>(M) * K * 2));

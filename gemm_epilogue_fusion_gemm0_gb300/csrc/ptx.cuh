@@ -93,6 +93,7 @@ enum WaitSite : uint32_t {
   kSiteSelftestFlag = 8,
   kSiteSplitTail = 9,  // owner of a split tile waiting for its partial
   kSitePieces = 10,    // owner of a tile cut into K pieces waiting for the pieces' partials
+  kSitePairTmem = 11,  // the CTAs of a pair were given different tensor memory (not a wait)
 };
 
 struct WaitCtl {
@@ -254,6 +255,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
+}
+
+// Brings a tile into L2 (no shared memory, no completion): the same box start rules.
+__device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
 }
 
 // ---------------------------------------------------------------------------

@@ -44,7 +44,8 @@
  *    reported later by coda_get_device_status().
  *  - Every kernel is launched with programmatic stream serialisation: it may
  *    begin its prologue while the kernel before it in `stream` is finishing,
- *    and it reads no memory before that kernel has completed.  Stream order is
+ *    and it reads no memory before that kernel has completed (the INT8 product
+ *    asks L2, where every write is seen, for the first bytes of its weights).  Stream order is
  *    kept as for ordinary launches, whatever kernel precedes it.
  *  - Numerics: bf16 operands, fp32 accumulation in tensor memory, fp32
  *    epilogue arithmetic, bf16 round-to-nearest-even stores.
@@ -341,7 +342,8 @@ CODA_API coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* 
  *   z [M, N] bf16, may be NULL;  y_out [M, N] bf16 out
  * K and N positive multiples of 16; codes may be anything in [-128, 127].  Sums are fp32 sums of
  * exact products: exact while they stay below 2^24.  A NaN scale makes its row or column NaN.
- * workspace: at least coda_matmul_q8_workspace_bytes(M, K, N). */
+ * workspace: at least coda_matmul_q8_workspace_bytes(M, K, N); NULL will do where that is 0
+ * (few tokens). */
 CODA_API size_t coda_matmul_q8_workspace_bytes(int64_t M, int64_t K, int64_t N);
 CODA_API coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* W_q,
                                       const float* w_s, const coda_bf16* z, int64_t M, int64_t K,

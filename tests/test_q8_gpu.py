@@ -177,7 +177,10 @@ PRODUCT = [(1, 16, 16), (1, 4096, 1024), (2, 48, 32), (7, 80, 144), (8, 512, 256
            (17, 1024, 272), (24, 4096, 512), (32, 144, 4096), (33, 272, 512), (48, 4096, 256),
            (64, 640, 1296), (65, 1040, 784), (100, 64, 128), (128, 512, 512), (129, 2048, 256),
            (200, 336, 1040), (256, 1024, 512), (257, 128, 384), (333, 4096, 784), (511, 160, 512),
-           (512, 528, 272), (513, 1024, 528), (1000, 784, 1040), (2049, 512, 784)]
+           (512, 528, 272), (513, 1024, 528), (1000, 784, 1040), (2049, 512, 784),
+           # more tiles than one wave holds: two blocks per SM, several waves, small W and large
+           (20, 208, 20496), (40, 256, 20496), (130, 192, 20480), (300, 80, 39936), (24, 8192, 8192),
+           (1100, 2048, 528), (1300, 4096, 1040)]
 
 
 def product_ref(a_q, a_s, W_q, w_s, z):
@@ -271,7 +274,7 @@ def test_product_writes_its_output_alone(B, M, K, N):
     contents before the call do not matter."""
     t = product_inputs(M, K, N, True, seed=5)
     want = B.coda_matmul_q8(*t[:4], z=t[4])
-    need = B.coda_matmul_q8_workspace_bytes(M, K, N)
+    need = B.coda_matmul_q8_workspace_bytes(M, K, N)  # 0 for few tokens
     pad = torch.full((M * N + 512,), -7.0, device="cuda", dtype=torch.bfloat16)
     wbuf = torch.full((need + 512,), 0xA5, device="cuda", dtype=torch.uint8)
     y = pad[256:256 + M * N].view(M, N)
@@ -492,7 +495,7 @@ def test_two_streams_at_once(B, M):
     shapes = (M, 2048, 1024)
     p = [product_inputs(*shapes, True, seed=i) for i in (1, 2)]
     want = [B.coda_matmul_q8(*t[:4], z=t[4]) for t in p]
-    need = B.coda_matmul_q8_workspace_bytes(*shapes)
+    need = max(B.coda_matmul_q8_workspace_bytes(*shapes), 16)
     ws = [B.workspace(need, "cuda") for _ in p]
     ys = [torch.empty_like(w) for w in want]
     streams = [torch.cuda.Stream() for _ in p]
@@ -525,7 +528,8 @@ def test_binding_refusals(B):
     with pytest.raises(TypeError):
         B.coda_matmul_q8(q.to(torch.uint8), s, W, ws)
     with pytest.raises(B.CodaError):
-        B.coda_matmul_q8(q, s, W, ws, ws=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        big = B.coda_quant_q8(bf(randn(2, 64, 64)))
+        B.coda_matmul_q8(*big, W, ws, ws=torch.empty(8, dtype=torch.uint8, device="cuda"))
     empty = B.coda_matmul_q8(q[:0], s[:0], W, ws)
     assert empty.shape == (0, 32)
     assert B.coda_add_rmsnorm_q8(x[:0], x[0], 1e-5)[1].shape == (0, 64)
