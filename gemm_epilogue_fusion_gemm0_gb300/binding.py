@@ -173,6 +173,13 @@ class _Call:
     def opt(self, t, dtype, shape, name):
         return None if t is None else self.t(t, dtype, shape, name)
 
+    def out(self, t, dtype, shape, name) -> tuple:
+        """An output and its address: `t` checked, or allocated (and then in need of no check)."""
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+            return t, t.data_ptr()
+        return t, self.t(t, dtype, shape, name)
+
     def ws(self, ws) -> tuple:
         if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
             raise TypeError(f"{self.where}: the workspace must be a contiguous CUDA tensor")
@@ -355,49 +362,48 @@ def _q8_scales(M: int, n: int, block: int) -> tuple:
 def coda_quant_q8(x, block=0, q=None, s=None, stream=None):
     """INT8 codes and scales of x [M, n]; a scale per row (block=0) or per row and 128
     columns (block=128, a checkpoint).  Returns (q, s)."""
-    M, n = x.shape
-    dev = x.device
+    shape = M, n = x.shape
     if block not in (0, 128):
         raise ValueError(f"block must be 0 (a scale per row) or 128, got {block}")
-    q = torch.empty((M, n), dtype=torch.int8, device=dev) if q is None else q
-    s = torch.empty(_q8_scales(M, n, block), dtype=torch.float32, device=dev) if s is None else s
-    c = _Call("coda_quant_q8", dev)
-    c.run(_lib.coda_quant_q8, c.t(x, torch.bfloat16, (M, n), "x"), M, n, block,
-          c.t(q, torch.int8, (M, n), "q"), c.t(s, torch.float32, _q8_scales(M, n, block), "s"),
-          stream=stream)
+    c = _Call("coda_quant_q8", x.device)
+    xp = c.t(x, torch.bfloat16, shape, "x")
+    q, qp = c.out(q, torch.int8, shape, "q")
+    s, sp = c.out(s, torch.float32, _q8_scales(M, n, block), "s")
+    c.run(_lib.coda_quant_q8, xp, M, n, block, qp, sp, stream=stream)
     return q, s
 
 
 def coda_dequant_q8(q, s, block=0, x=None, stream=None):
     """The values of codes q with scales s (as coda_quant_q8 gives them) in bf16; returns x."""
-    M, n = q.shape
+    shape = M, n = q.shape
+    c = _Call("coda_dequant_q8", q.device)
     if block not in (0, 128):
         raise ValueError(f"block must be 0 (a scale per row) or 128, got {block}")
-    x = torch.empty((M, n), dtype=torch.bfloat16, device=q.device) if x is None else x
-    c = _Call("coda_dequant_q8", q.device)
-    c.run(_lib.coda_dequant_q8, c.t(q, torch.int8, (M, n), "q"),
-          c.t(s, torch.float32, _q8_scales(M, n, block), "s"), M, n, block,
-          c.t(x, torch.bfloat16, (M, n), "x"), stream=stream)
+    qp = c.t(q, torch.int8, shape, "q")
+    sp = c.t(s, torch.float32, _q8_scales(M, n, block), "s")
+    x, xp = c.out(x, torch.bfloat16, shape, "x")
+    c.run(_lib.coda_dequant_q8, qp, sp, M, n, block, xp, stream=stream)
     return x
 
 
 def coda_add_rmsnorm_q8(x, gamma, eps, z=None, h=None, q=None, s=None, stream=None):
     """Residual addition h = x + z and RMS norm with INT8 codes and a scale per token; returns
     (h, q, s).  Without z no h is written and x itself is returned in its place."""
-    M, d = x.shape
-    dev = x.device
-    bf = torch.bfloat16
+    shape = M, d = x.shape
     if z is None and h is not None:
         raise ValueError("h is an output of the residual's addition: it needs z")
-    if z is not None and h is None:
-        h = torch.empty((M, d), dtype=bf, device=dev)
-    q = torch.empty((M, d), dtype=torch.int8, device=dev) if q is None else q
-    s = torch.empty((M,), dtype=torch.float32, device=dev) if s is None else s
-    c = _Call("coda_add_rmsnorm_q8", dev)
-    c.run(_lib.coda_add_rmsnorm_q8, c.t(x, bf, (M, d), "x"), c.opt(z, bf, (M, d), "z"),
-          c.t(gamma, bf, (d,), "gamma"), float(eps), M, d, c.opt(h, bf, (M, d), "h"),
-          c.t(q, torch.int8, (M, d), "q"), c.t(s, torch.float32, (M,), "s"), stream=stream)
-    return (x if z is None else h), q, s
+    c = _Call("coda_add_rmsnorm_q8", x.device)
+    bf = torch.bfloat16
+    xp, gp = c.t(x, bf, shape, "x"), c.t(gamma, bf, (d,), "gamma")
+    if z is None:
+        h, hp, zp = x, None, None
+    else:
+        zp = c.t(z, bf, shape, "z")
+        h, hp = c.out(h, bf, shape, "h")
+    q, qp = c.out(q, torch.int8, shape, "q")
+    s, sp = c.out(s, torch.float32, (M,), "s")
+    c.run(_lib.coda_add_rmsnorm_q8, xp, zp, gp, float(eps), M, d, hp, qp, sp, stream=stream)
+    return h, q, s
 
 
 def coda_matmul_q8_workspace_bytes(M: int, K: int, N: int) -> int:
@@ -410,16 +416,21 @@ def coda_matmul_q8(a_q, a_s, W_q, w_s, z=None, y=None, ws=None, stream=None):
     coda_matmul_q8_workspace_bytes is 0."""
     M, K = a_q.shape
     N = W_q.shape[1]
-    dev = a_q.device
+    c = _Call("coda_matmul_q8", a_q.device)
     bf, f32, i8 = torch.bfloat16, torch.float32, torch.int8
-    y = torch.empty((M, N), dtype=bf, device=dev) if y is None else y
-    c = _Call("coda_matmul_q8", dev)
+    ap, asp = c.t(a_q, i8, (M, K), "a_q"), c.t(a_s, f32, (M,), "a_s")
+    wp, wsp = c.t(W_q, i8, (K, N), "W_q"), c.t(w_s, f32, (N,), "w_s")
+    zp = None if z is None else c.t(z, bf, (M, N), "z")
+    y, yp = c.out(y, bf, (M, N), "y")
     need = _lib.coda_matmul_q8_workspace_bytes(M, K, N)
-    if need and ws is None:
-        ws = workspace(need, dev)
-    c.run(_lib.coda_matmul_q8, c.t(a_q, i8, (M, K), "a_q"), c.t(a_s, f32, (M,), "a_s"),
-          c.t(W_q, i8, (K, N), "W_q"), c.t(w_s, f32, (N,), "w_s"), c.opt(z, bf, (M, N), "z"),
-          M, K, N, c.t(y, bf, (M, N), "y"), *(c.ws(ws) if need else (None, 0)), stream=stream)
+    if not need:
+        wk, wkb = None, 0
+    elif ws is None:  # named, so that it lives until the call is enqueued
+        ws = torch.empty(need, dtype=torch.uint8, device=c.device)
+        wk, wkb = ws.data_ptr(), need
+    else:
+        wk, wkb = c.ws(ws)
+    c.run(_lib.coda_matmul_q8, ap, asp, wp, wsp, zp, M, K, N, yp, wk, wkb, stream=stream)
     return y
 
 
@@ -432,23 +443,22 @@ def coda_bwd_swiglu_dgrad_q8(dout, W2, y_q, y_s, W1, h, r, gamma, dy=None, s=Non
     half = W2.shape[0]
     N1 = 2 * half
     d = W1.shape[0]
-    dev = dout.device
+    c = _Call("coda_bwd_swiglu_dgrad_q8", dout.device)
     bf, f32 = torch.bfloat16, torch.float32
-    dy = torch.empty((M, N1), dtype=bf, device=dev) if dy is None else dy
-    s = torch.empty((M,), dtype=f32, device=dev) if s is None else s
-    dh = torch.empty((M, d), dtype=bf, device=dev) if dh is None else dh
-    if want_a and a is None:
-        a = torch.empty((M, half), dtype=bf, device=dev)
+    ins = (c.t(dout, bf, (M, Dout), "dout"), c.t(W2, bf, (half, Dout), "W2"),
+           c.t(y_q, torch.int8, (M, N1), "y_q"), c.t(y_s, f32, _q8_scales(M, N1, 128), "y_s"),
+           c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"), c.t(r, f32, (M,), "r"),
+           c.t(gamma, bf, (d,), "gamma"))
+    dy, dyp = c.out(dy, bf, (M, N1), "dy")
+    s, sp = c.out(s, f32, (M,), "s")
+    dh, dhp = c.out(dh, bf, (M, d), "dh")
+    ap = None
+    if want_a or a is not None:
+        a, ap = c.out(a, bf, (M, half), "a")
     if ws is None:
-        ws = workspace(coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout), dev)
-    c = _Call("coda_bwd_swiglu_dgrad_q8", dev)
-    c.run(_lib.coda_bwd_swiglu_dgrad_q8,
-          c.t(dout, bf, (M, Dout), "dout"), c.t(W2, bf, (half, Dout), "W2"),
-          c.t(y_q, torch.int8, (M, N1), "y_q"), c.t(y_s, f32, _q8_scales(M, N1, 128), "y_s"),
-          c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"), c.t(r, f32, (M,), "r"),
-          c.t(gamma, bf, (d,), "gamma"), M, d, N1, Dout, c.t(dy, bf, (M, N1), "dy"),
-          c.t(s, f32, (M,), "s"), c.t(dh, bf, (M, d), "dh"), c.opt(a, bf, (M, half), "a"),
-          *c.ws(ws), stream=stream)
+        ws = workspace(coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout), c.device)
+    c.run(_lib.coda_bwd_swiglu_dgrad_q8, *ins, M, d, N1, Dout, dyp, sp, dhp, ap, *c.ws(ws),
+          stream=stream)
     return (dy, s, dh, a) if a is not None else (dy, s, dh)
 
 

@@ -939,11 +939,15 @@ ColPlan plan_dgrad_cols(int64_t mt, int64_t d, int64_t K, int npairs) {
 // ---------------------------------------------------------------------------
 // 8-bit codes with scales (q8.cuh)
 // ---------------------------------------------------------------------------
+// No tensor of the 8-bit operators has more values than this (several times what a device
+// holds), so that byte counts and grids stay far from overflowing.
+bool fits(int64_t rows, int64_t cols) { return cols <= (int64_t(1) << 40) / std::max<int64_t>(rows, 1); }
+
 // M rows of n values; n a positive multiple of 8
 coda_status_t check_rows(int64_t M, int64_t n) {
   if (M < 0 || n <= 0) return CODA_ERR_INVALID_ARG;
   const int64_t lim = (int64_t(1) << 31) - 256;
-  if (n % 8 != 0 || M > lim || n > lim) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (n % 8 != 0 || M > lim || n > lim || !fits(M, n)) return CODA_ERR_UNSUPPORTED_SHAPE;
   return CODA_OK;
 }
 
@@ -972,7 +976,9 @@ coda_status_t check_product(int64_t M, int64_t K, int64_t N) {
   if (M < 0 || K <= 0 || N <= 0) return CODA_ERR_INVALID_ARG;
   const int64_t lim = (int64_t(1) << 31) - 256;
   // 16-byte rows of one-byte codes
-  if (K % 16 != 0 || N % 16 != 0 || M > lim || K > lim || N > lim) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (K % 16 != 0 || N % 16 != 0 || M > lim || K > lim || N > lim || !fits(M, K) || !fits(K, N) ||
+      !fits(M, N))
+    return CODA_ERR_UNSUPPORTED_SHAPE;
   return CODA_OK;
 }
 

@@ -406,61 +406,77 @@ struct EpiSwiGLUBackwardQ8 : EpiDefaultCols {
       }
     }
     float ss = 0.f;
+    const uint32_t lane = threadIdx.x & 31u;
+    // The next chunk's codes are in flight while the current one is worked on (four 16-byte
+    // registers; the bf16 form would need twice as many).
+    const size_t rbase = static_cast<size_t>(wr.row0) * q_pitch;
+    const Span q_span = span(p.y_q, c.M, q_pitch);
+    uint4 gf[Stage32::kGroups], uf[Stage32::kGroups];
+    const auto fetch = [&](int j0) {
+      const int valid = valid_bytes(j0, c.nend, 1);
+      Stage32::fetch(gf, p.y_q + rbase + j0, q_pitch, wr.rows, valid, q_span);
+      Stage32::fetch(uf, p.y_q + rbase + half + j0, q_pitch, wr.rows, valid, q_span);
+    };
+    fetch(jh);
 #pragma unroll 1
     for (int ch = 0; ch < kHalfChunks; ++ch) {
       const int col = c.half * kHalfCols + ch * 32;
       const int j0 = c.n0 + col;
-      const int valid = valid_bytes(j0, c.nend, 1);
-      const size_t row_off = static_cast<size_t>(wr.row0) * q_pitch + j0;
-      Stage32::load(buf0, p.y_q + row_off, q_pitch, wr.rows, valid, span(p.y_q, c.M, q_pitch));
-      Stage32::load(buf1, p.y_q + row_off + half, q_pitch, wr.rows, valid,
-                    span(p.y_q, c.M, q_pitch));
+      const int valid = valid_bytes(j0, c.nend, 2);
+      const size_t row_off = rbase + j0;
+      Stage32::deposit(buf0, gf);
+      Stage32::deposit(buf1, uf);
+      if (ch + 1 < kHalfChunks) fetch(j0 + 32);
       uint32_t v[32];
       tmem_ld32(c.taddr + col, v);
       tmem_ld_wait(v);
       mask_chunk(v, j0, c.nend);
       __syncwarp();
-      uint32_t gq[8], uq[8], dgw[16], duw[16], aw[16];
+      uint32_t gq[8], uq[8], aw[16];
       Stage32::get(buf0, gq);
       Stage32::get(buf1, uq);
-      __syncwarp();  // a put below writes where other lanes' codes were
+      __syncwarp();  // the stores below write where other lanes' codes were
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        float gv[4], uv[4], dgv[4], duv[4], av[4];
-        q8_unpack4(gq[w], gv);
-        q8_unpack4(uq[w], uv);
+      for (int g8 = 0; g8 < 4; ++g8) {  // 8 columns: one 16-byte group of a staged row
+        uint32_t dgw[4], duw[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float da = __uint_as_float(v[4 * w + k]);
-          const float g = sg * gv[k];
-          const float u = (j0 + 4 * w + k < u_next ? su0 : su1) * uv[k];
-          const float sig = __fdividef(1.0f, 1.0f + __expf(-g));
-          dgv[k] = da * u * sig * (1.0f + g * (1.0f - sig));
-          duv[k] = da * g * sig;
-          av[k] = g * sig * u;
-          ss = fmaf(dgv[k], g, ss);  // da is zero past the last row and column
-          ss = fmaf(duv[k], u, ss);
+        for (int w = 2 * g8; w < 2 * g8 + 2; ++w) {
+          float gv[4], uv[4], dgv[4], duv[4], av[4];
+          q8_unpack4(gq[w], gv);
+          q8_unpack4(uq[w], uv);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float da = __uint_as_float(v[4 * w + k]);
+            const float g = sg * gv[k];
+            const float u = (j0 + 4 * w + k < u_next ? su0 : su1) * uv[k];
+            const float sig = __fdividef(1.0f, 1.0f + __expf(-g));
+            dgv[k] = da * u * sig * (1.0f + g * (1.0f - sig));
+            duv[k] = da * g * sig;
+            av[k] = g * sig * u;
+            ss = fmaf(dgv[k], g, ss);  // da is zero past the last row and column
+            ss = fmaf(duv[k], u, ss);
+          }
+          const int o = 2 * (w - 2 * g8);
+          dgw[o] = pack_bf16x2(dgv[0], dgv[1]);
+          dgw[o + 1] = pack_bf16x2(dgv[2], dgv[3]);
+          duw[o] = pack_bf16x2(duv[0], duv[1]);
+          duw[o + 1] = pack_bf16x2(duv[2], duv[3]);
+          aw[2 * w] = pack_bf16x2(av[0], av[1]);
+          aw[2 * w + 1] = pack_bf16x2(av[2], av[3]);
         }
-        dgw[2 * w] = pack_bf16x2(dgv[0], dgv[1]);
-        dgw[2 * w + 1] = pack_bf16x2(dgv[2], dgv[3]);
-        duw[2 * w] = pack_bf16x2(duv[0], duv[1]);
-        duw[2 * w + 1] = pack_bf16x2(duv[2], duv[3]);
-        aw[2 * w] = pack_bf16x2(av[0], av[1]);
-        aw[2 * w + 1] = pack_bf16x2(av[2], av[3]);
+        st_shared_v4(Stage64::at(buf0, lane, g8), dgw[0], dgw[1], dgw[2], dgw[3]);
+        st_shared_v4(Stage64::at(buf1, lane, g8), duw[0], duw[1], duw[2], duw[3]);
       }
-      Stage64::put(buf0, dgw);
-      Stage64::put(buf1, duw);
       __syncwarp();
-      Stage64::flush(buf0, p.dy_out + row_off, pitch, wr.rows, 2 * valid,
-                     span(p.dy_out, c.M, pitch));
-      Stage64::flush(buf1, p.dy_out + row_off + half, pitch, wr.rows, 2 * valid,
+      Stage64::flush(buf0, p.dy_out + row_off, pitch, wr.rows, valid, span(p.dy_out, c.M, pitch));
+      Stage64::flush(buf1, p.dy_out + row_off + half, pitch, wr.rows, valid,
                      span(p.dy_out, c.M, pitch));
       __syncwarp();
       if (p.a_out != nullptr) {
         Stage64::put(buf0, aw);
         __syncwarp();
         Stage64::flush(buf0, p.a_out + static_cast<size_t>(wr.row0) * half + j0, a_pitch, wr.rows,
-                       2 * valid, span(p.a_out, c.M, a_pitch));
+                       valid, span(p.a_out, c.M, a_pitch));
         __syncwarp();
       }
     }

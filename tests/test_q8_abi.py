@@ -70,6 +70,18 @@ def test_rows(B, name):
     assert call(B, M=0, p=[None] * count) == B.CODA_OK  # empty batch: no-op
 
 
+def test_sizes_that_overflow_are_refused(B):
+    """Within the limit of each size, but with more values than any device holds."""
+    lim = (1 << 31) - 256
+    assert _quant(B, M=lim, n=lim // 8 * 8) == B.CODA_ERR_UNSUPPORTED_SHAPE
+    assert _dequant(B, M=lim, n=lim // 8 * 8, block=128) == B.CODA_ERR_UNSUPPORTED_SHAPE
+    assert _norm(B, M=lim, d=lim // 8 * 8) == B.CODA_ERR_UNSUPPORTED_SHAPE
+    top = lim // 16 * 16
+    for M, K, N in ((1, top, top), (lim, top, 16), (lim, 16, top)):
+        assert _product(B, M=M, K=K, N=N) == B.CODA_ERR_UNSUPPORTED_SHAPE
+        assert B.coda_matmul_q8_workspace_bytes(M, K, N) == 0
+
+
 @pytest.mark.parametrize("call", [_quant, _dequant], ids=["quant", "dequant"])
 def test_quantiser_shapes(B, call):
     assert call(B, n=0) == B.CODA_ERR_INVALID_ARG

@@ -180,7 +180,7 @@ PRODUCT = [(1, 16, 16), (1, 4096, 1024), (2, 48, 32), (7, 80, 144), (8, 512, 256
            (512, 528, 272), (513, 1024, 528), (1000, 784, 1040), (2049, 512, 784),
            # more tiles than one wave holds: two blocks per SM, several waves, small W and large
            (20, 208, 20496), (40, 256, 20496), (130, 192, 20480), (300, 80, 39936), (24, 8192, 8192),
-           (1100, 2048, 528), (1300, 4096, 1040)]
+           (1100, 2048, 528), (1300, 4096, 1040), (40, 16, 16), (70, 48, 32), (1025, 16, 48)]
 
 
 def product_ref(a_q, a_s, W_q, w_s, z):
