@@ -232,6 +232,8 @@ constexpr int kMaxDevices = 64;
 constexpr int kGroupM = 16;     // 128-row blocks per L2 group (single-CTA tiles)
 constexpr int kPairGroupM = 8;  // 256-row blocks per L2 group (CTA-pair tiles)
 
+constexpr int kRingSmem = 220 * 1024;  // of an SM, for the rings of its blocks
+
 struct DevState {
   bool init = false;
   coda_status_t status = CODA_OK;
@@ -361,6 +363,11 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
                                  kProductQ8Smem) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kPairProductQ8, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kPairProductQ8Smem) == cudaSuccess;
+      for (auto* ring : {&row_q8_ring_kernel<false, false, false>, &row_q8_ring_kernel<true, false, false>,
+                         &row_q8_ring_kernel<true, false, true>, &row_q8_ring_kernel<true, true, false>,
+                         &row_q8_ring_kernel<true, true, true>})
+        ok &= cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem) ==
+              cudaSuccess;
       ok &= cudaFuncSetAttribute(kProductSmall1, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  SmallSmem<1>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kProductSmall2, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -468,10 +475,10 @@ bool tmap_2d_u8(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t oute
 }
 
 template <typename... ExpT, typename... ActT>
-cudaError_t launch_cluster(void (*kernel)(ExpT...), int grid, int block, size_t smem,
+cudaError_t launch_cluster(void (*kernel)(ExpT...), dim3 grid, int block, size_t smem,
                            cudaStream_t stream, bool cooperative, int cluster, ActT&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -498,7 +505,7 @@ cudaError_t launch_cluster(void (*kernel)(ExpT...), int grid, int block, size_t 
 }
 
 template <typename... ExpT, typename... ActT>
-cudaError_t launch(void (*kernel)(ExpT...), int grid, int block, size_t smem, cudaStream_t stream,
+cudaError_t launch(void (*kernel)(ExpT...), dim3 grid, int block, size_t smem, cudaStream_t stream,
                    bool cooperative, ActT&&... args) {
   return launch_cluster(kernel, grid, block, smem, stream, cooperative, 1,
                         std::forward<ActT>(args)...);
@@ -954,22 +961,43 @@ coda_status_t check_rows(int64_t M, int64_t n) {
 // One scale per row: a warp per row up to 1024 columns, a block of up to 1024
 // threads holding 4 vectors of 8 values each up to 32768, a block that reads the
 // row twice beyond.
-template <bool kNorm, bool kRes>
-cudaError_t launch_row_q8(const RowQ8Params& p, cudaStream_t stream) {
+template <bool kNorm, bool kRes, bool kH>
+cudaError_t launch_row_q8(const RowQ8Params& p, int sms, cudaStream_t stream) {
   const int nvec = p.d / 8;
+  if (nvec <= 32)
+    return launch(&row_q8_kernel<kNorm, kRes, kH, 1, true>, static_cast<int>(cdiv(p.M, 8)), 256, 0, stream,
+                  false, p);
   if (nvec <= 32 * kRowQ8Vec)
-    return launch(&row_q8_kernel<kNorm, kRes, kRowQ8Vec, true>, static_cast<int>(cdiv(p.M, 8)), 256,
+    return launch(&row_q8_kernel<kNorm, kRes, kH, kRowQ8Vec, true>, static_cast<int>(cdiv(p.M, 8)), 256,
                   0, stream, false, p);
-  if (nvec <= 1024 * kRowQ8Vec)
-    return launch(&row_q8_kernel<kNorm, kRes, kRowQ8Vec, false>, p.M,
-                  static_cast<int>(cdiv(nvec, 32 * kRowQ8Vec)) * 32, 0, stream, false, p);
-  return launch(&row_q8_kernel<kNorm, kRes, 0, false>, p.M, 1024, 0, stream, false, p);
+  const int threads = static_cast<int>(cdiv(nvec, 32 * kRowQ8Vec)) * 32;
+  if (threads > 512 && threads <= 1024) {
+    // Rows of more than 16384 columns leave one or two blocks to an SM: walked by blocks that stay,
+    // where two rows fit and there are at least four for each block (8192 x 28672, norm without a
+    // residual 113 us against 182, quantiser 118 against 133; at 8192 x 8192 it is the other way
+    // around, 82 us against 74 with a residual).
+    const int stage = (kRes ? 4 : 2) * p.d;
+    const int room = kRingSmem - static_cast<int>(row_ring_bytes(p.d, kNorm, kRes, 0));
+    const int stages = std::min(kRingMaxStages, room / stage);
+    if (stages >= 2 && p.M >= 4 * static_cast<int64_t>(sms))
+      return launch(&row_q8_ring_kernel<kNorm, kRes, kH>, sms, threads,
+                    row_ring_bytes(p.d, kNorm, kRes, stages), stream, false, p, stages,
+                    g_timeout_ns.load());
+  }
+  if (threads <= 1024)
+    return launch(&row_q8_kernel<kNorm, kRes, kH, kRowQ8Vec, false>, p.M, threads, 0, stream, false, p);
+  return launch(&row_q8_kernel<kNorm, kRes, kH, 0, false>, p.M, 1024, 0, stream, false, p);
 }
 
-// Thread blocks of the kernels that walk a row's blocks of 128 columns; 0: too many.
-int q8_block_grid(int64_t M, int64_t n) {
-  const int64_t grid = cdiv(M * cdiv(n, kQ8Block), kQ8UnitsPerCta);
-  return grid <= 0x7fffffff ? static_cast<int>(grid) : 0;
+// Grid of the kernels on blocks of 128 columns: x over rows, y over a row's blocks.
+// `lanes` of them share a block of 128 columns.
+bool q8_block_grid(int64_t M, int64_t n, int lanes, dim3* grid) {
+  const int64_t nb = cdiv(n, kQ8Block);
+  const int lg = q8_span_log2(static_cast<int>(std::min<int64_t>(nb, 16)));
+  const int64_t gx = cdiv(M, kQ8Passes * ((256 / lanes) >> lg)), gy = cdiv(nb, int64_t(1) << lg);
+  if (gx > 0x7fffffff || gy > 65535) return false;
+  *grid = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  return true;
 }
 
 coda_status_t check_product(int64_t M, int64_t K, int64_t N) {
@@ -1616,8 +1644,8 @@ coda_status_t coda_quant_q8(const coda_bf16* x, int64_t M, int64_t n, int block,
   if (M == 0) return CODA_OK;
   if (!x || !q_out || !s_out) return CODA_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q_out) || !aligned16(s_out)) return CODA_ERR_MISALIGNED;
-  const int grid = q8_block_grid(M, n);
-  if (grid == 0) return CODA_ERR_UNSUPPORTED_SHAPE;
+  dim3 grid;
+  if (!q8_block_grid(M, n, kQ8QuantLanes, &grid)) return CODA_ERR_UNSUPPORTED_SHAPE;
   int sms = 0;
   st = device_setup(&sms);
   if (st != CODA_OK) return st;
@@ -1629,7 +1657,7 @@ coda_status_t coda_quant_q8(const coda_bf16* x, int64_t M, int64_t n, int block,
     p.s_out = s_out;
     p.M = static_cast<int>(M);
     p.d = static_cast<int>(n);
-    e = launch_row_q8<false, false>(p, stream);
+    e = launch_row_q8<false, false, false>(p, sms, stream);
   } else {
     e = launch(block_q8_kernel, grid, 256, 0, stream, false,
                reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<uint8_t*>(q_out), s_out,
@@ -1651,8 +1679,8 @@ coda_status_t coda_dequant_q8(const int8_t* q, const float* s, int64_t M, int64_
   if (M == 0) return CODA_OK;
   if (!q || !s || !x_out) return CODA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(s) || !aligned16(x_out)) return CODA_ERR_MISALIGNED;
-  const int grid = q8_block_grid(M, n);
-  if (grid == 0) return CODA_ERR_UNSUPPORTED_SHAPE;
+  dim3 grid;
+  if (!q8_block_grid(M, n, kQ8DequantLanes, &grid)) return CODA_ERR_UNSUPPORTED_SHAPE;
   int sms = 0;
   st = device_setup(&sms);
   if (st != CODA_OK) return st;
@@ -1693,7 +1721,10 @@ coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* z, const 
   p.eps = eps;
   p.M = static_cast<int>(M);
   p.d = static_cast<int>(d);
-  const cudaError_t e = z ? launch_row_q8<true, true>(p, stream) : launch_row_q8<true, false>(p, stream);
+  const cudaError_t e = z ? (h_out ? launch_row_q8<true, true, true>(p, sms, stream)
+                                   : launch_row_q8<true, true, false>(p, sms, stream))
+                          : (h_out ? launch_row_q8<true, false, true>(p, sms, stream)
+                                   : launch_row_q8<true, false, false>(p, sms, stream));
   if (e != cudaSuccess) {
     cudaGetLastError();
     return CODA_ERR_LAUNCH;

@@ -257,6 +257,27 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Untiled bulk copy to shared memory: both addresses 16-byte aligned, bytes a multiple of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// The last of `count` copies into a ring of `stages` barriers have landed (bounded): before a
+// block that gave up may exit.
+__device__ __forceinline__ void land_copies(uint32_t bar_full, int count, int stages,
+                                            uint64_t timeout_ns) {
+  for (int i = max(0, count - stages); i < count; ++i) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar_full + 8u * (i % stages), static_cast<uint32_t>(i / stages) & 1u) &&
+           globaltimer_ns() - t0 < timeout_ns) {
+    }
+  }
+}
+
 // Brings a tile into L2 (no shared memory, no completion): the same box start rules.
 __device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap* map, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(

@@ -190,17 +190,6 @@ struct RingPos {
   }
 };
 
-// Let the copies that a producer has issued land before the block can exit.
-__device__ __forceinline__ void land_copies(uint32_t bar_full, int count, int stages,
-                                            uint64_t timeout_ns) {
-  for (int i = max(0, count - stages); i < count; ++i) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar_full + 8u * (i % stages), static_cast<uint32_t>(i / stages) & 1u) &&
-           globaltimer_ns() - t0 < timeout_ns) {
-    }
-  }
-}
-
 template <bool kNarrow>
 __global__ void __launch_bounds__(kMidThreads, kNarrow ? 2 : 1)
     product_q8_mid_kernel(const __grid_constant__ CUtensorMap tmW,

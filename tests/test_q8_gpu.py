@@ -82,7 +82,9 @@ def check_codes(q, s, v, block, scale_factor=None, rel=4 * U):
 
 # ------------------------------------------------------------------ quantise and load again
 ROWS = [(1, 8), (3, 24), (257, 128), (5, 136), (9, 1024), (4, 1032), (33, 2056), (2, 4096),
-        (1, 28672), (3, 32768), (2, 32776), (700, 1000)]
+        (1, 28672), (3, 32768), (2, 32776), (700, 1000),
+        # enough rows for blocks that walk them
+        (7000, 1032), (5003, 2064), (2501, 4104), (2000, 8200), (1300, 16384)]
 
 
 @pytest.mark.parametrize("block", [0, BLOCK])
