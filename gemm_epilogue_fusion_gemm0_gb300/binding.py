@@ -153,10 +153,12 @@ class _Call:
     current device, so a tensor on another one would hand the kernels a
     pointer they cannot use)."""
 
-    __slots__ = ("where", "device", "index")
+    __slots__ = ("where", "device", "index", "own")
 
-    def __init__(self, where: str, device: torch.device):
+    def __init__(self, where: str, device: torch.device, stream=None):
         self.where, self.device = where, device
+        # tensors allocated for a call on a stream of its own
+        self.own = None if stream is None else []
         self.index = device.index if device.type == "cuda" else None
 
     def t(self, t, dtype, shape, name) -> int:
@@ -177,8 +179,20 @@ class _Call:
         """An output and its address: `t` checked, or allocated (and then in need of no check)."""
         if t is None:
             t = torch.empty(shape, dtype=dtype, device=self.device)
+            if self.own is not None:
+                self.own.append(t)
             return t, t.data_ptr()
         return t, self.t(t, dtype, shape, name)
+
+    def scratch(self, ws, need: int) -> tuple:
+        """Address and size of the workspace: `ws` checked, or `need` bytes allocated."""
+        if ws is None:
+            # kept until the call is enqueued: freed memory is reused in stream order
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            if self.own is not None:
+                self.own.append(ws)
+            return ws, ws.data_ptr(), need
+        return (ws, *self.ws(ws))
 
     def ws(self, ws) -> tuple:
         if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
@@ -189,6 +203,13 @@ class _Call:
         return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def run(self, fn, *args, stream=None) -> None:
+        if self.own:
+            # allocated for the current stream, used on another one: not to be handed out again
+            # before that one is done with them
+            user = (stream if hasattr(stream, "cuda_stream")
+                    else torch.cuda.ExternalStream(int(stream), device=self.device))
+            for t in self.own:
+                t.record_stream(user)
         if self.index == torch.cuda.current_device():
             st = fn(*args, _raw_stream(self.index) if stream is None
                     else _stream_ptr(stream, self.device))
@@ -365,7 +386,7 @@ def coda_quant_q8(x, block=0, q=None, s=None, stream=None):
     shape = M, n = x.shape
     if block not in (0, 128):
         raise ValueError(f"block must be 0 (a scale per row) or 128, got {block}")
-    c = _Call("coda_quant_q8", x.device)
+    c = _Call("coda_quant_q8", x.device, stream)
     xp = c.t(x, torch.bfloat16, shape, "x")
     q, qp = c.out(q, torch.int8, shape, "q")
     s, sp = c.out(s, torch.float32, _q8_scales(M, n, block), "s")
@@ -376,7 +397,7 @@ def coda_quant_q8(x, block=0, q=None, s=None, stream=None):
 def coda_dequant_q8(q, s, block=0, x=None, stream=None):
     """The values of codes q with scales s (as coda_quant_q8 gives them) in bf16; returns x."""
     shape = M, n = q.shape
-    c = _Call("coda_dequant_q8", q.device)
+    c = _Call("coda_dequant_q8", q.device, stream)
     if block not in (0, 128):
         raise ValueError(f"block must be 0 (a scale per row) or 128, got {block}")
     qp = c.t(q, torch.int8, shape, "q")
@@ -392,7 +413,7 @@ def coda_add_rmsnorm_q8(x, gamma, eps, z=None, h=None, q=None, s=None, stream=No
     shape = M, d = x.shape
     if z is None and h is not None:
         raise ValueError("h is an output of the residual's addition: it needs z")
-    c = _Call("coda_add_rmsnorm_q8", x.device)
+    c = _Call("coda_add_rmsnorm_q8", x.device, stream)
     bf = torch.bfloat16
     xp, gp = c.t(x, bf, shape, "x"), c.t(gamma, bf, (d,), "gamma")
     if z is None:
@@ -416,20 +437,14 @@ def coda_matmul_q8(a_q, a_s, W_q, w_s, z=None, y=None, ws=None, stream=None):
     coda_matmul_q8_workspace_bytes is 0."""
     M, K = a_q.shape
     N = W_q.shape[1]
-    c = _Call("coda_matmul_q8", a_q.device)
+    c = _Call("coda_matmul_q8", a_q.device, stream)
     bf, f32, i8 = torch.bfloat16, torch.float32, torch.int8
     ap, asp = c.t(a_q, i8, (M, K), "a_q"), c.t(a_s, f32, (M,), "a_s")
     wp, wsp = c.t(W_q, i8, (K, N), "W_q"), c.t(w_s, f32, (N,), "w_s")
     zp = None if z is None else c.t(z, bf, (M, N), "z")
     y, yp = c.out(y, bf, (M, N), "y")
     need = _lib.coda_matmul_q8_workspace_bytes(M, K, N)
-    if not need:
-        wk, wkb = None, 0
-    elif ws is None:  # named, so that it lives until the call is enqueued
-        ws = torch.empty(need, dtype=torch.uint8, device=c.device)
-        wk, wkb = ws.data_ptr(), need
-    else:
-        wk, wkb = c.ws(ws)
+    ws, wk, wkb = c.scratch(ws, need) if need else (None, None, 0)
     c.run(_lib.coda_matmul_q8, ap, asp, wp, wsp, zp, M, K, N, yp, wk, wkb, stream=stream)
     return y
 
@@ -443,7 +458,7 @@ def coda_bwd_swiglu_dgrad_q8(dout, W2, y_q, y_s, W1, h, r, gamma, dy=None, s=Non
     half = W2.shape[0]
     N1 = 2 * half
     d = W1.shape[0]
-    c = _Call("coda_bwd_swiglu_dgrad_q8", dout.device)
+    c = _Call("coda_bwd_swiglu_dgrad_q8", dout.device, stream)
     bf, f32 = torch.bfloat16, torch.float32
     ins = (c.t(dout, bf, (M, Dout), "dout"), c.t(W2, bf, (half, Dout), "W2"),
            c.t(y_q, torch.int8, (M, N1), "y_q"), c.t(y_s, f32, _q8_scales(M, N1, 128), "y_s"),
@@ -455,9 +470,9 @@ def coda_bwd_swiglu_dgrad_q8(dout, W2, y_q, y_s, W1, h, r, gamma, dy=None, s=Non
     ap = None
     if want_a or a is not None:
         a, ap = c.out(a, bf, (M, half), "a")
-    if ws is None:
-        ws = workspace(coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout), c.device)
-    c.run(_lib.coda_bwd_swiglu_dgrad_q8, *ins, M, d, N1, Dout, dyp, sp, dhp, ap, *c.ws(ws),
+    need = max(_lib.coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout), 16)
+    ws, wk, wkb = c.scratch(ws, need)
+    c.run(_lib.coda_bwd_swiglu_dgrad_q8, *ins, M, d, N1, Dout, dyp, sp, dhp, ap, wk, wkb,
           stream=stream)
     return (dy, s, dh, a) if a is not None else (dy, s, dh)
 

@@ -31,14 +31,20 @@ __device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
 // What a group of values with the given amax is multiplied by to give codes: 127 / amax.
 // Outside of 2^-100 .. 2^100 that quotient or its reciprocal leaves fp32's normal range, so the
 // values are brought near one first (`pre`, a power of two: exact), which hardly any group needs.
-// The approximate reciprocal is off by 1 ulp at most, a code's argument by 127 * 3 * 2^-24.
+// A row's quotient is rounded once; for a block of 128 values that costs as much as the rest, and
+// the approximate reciprocal (1 ulp) puts a code's argument off by 127 * 3 * 2^-24 at most.
 struct Q8Factors {
   float pre, inv;
-  __device__ __forceinline__ explicit Q8Factors(float amax) {
+  __device__ __forceinline__ explicit Q8Factors(float amax, bool approximate = false) {
     pre = amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.0f;
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax * pre));
-    inv = amax > 0.f && amax <= 3.402823466e38f ? 127.0f * r : 0.f;
+    if (approximate) {
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax * pre));
+      r *= 127.0f;
+    } else {
+      r = __fdiv_rn(127.0f, amax * pre);
+    }
+    inv = amax > 0.f && amax <= 3.402823466e38f ? r : 0.f;
   }
   template <int kV>
   __device__ __forceinline__ void prepare(float (&u)[kV][8]) const {
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(256) block_q8_kernel(const __nv_bfloat16* __re
 #pragma unroll
     for (int o = kQ8QuantLanes / 2; o > 0; o >>= 1)
       amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const Q8Factors f(amax);
+    const Q8Factors f(amax, true);
     if (pl.row(i) < M) {
       uint8_t* dst = q + pl.row(i) * n + pl.col;
       float u[2][8];

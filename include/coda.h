@@ -293,8 +293,9 @@ CODA_API coda_status_t coda_bwd(const coda_bf16* dy, const coda_bf16* x, const c
  *
  * A value v is held as code * scale.  Over the values that share a scale,
  *   scale = amax / 127,   code = rint(v * 127 / amax),   amax = max |v|,
- * code in [-127, 127], ties to even; amax = 0 gives code 0 and scale 0.  A value
- * is then off by at most amax / 254.  Values that share a scale with an infinity
+ * code in [-127, 127]; amax = 0 gives code 0 and scale 0.  A value is then off by
+ * at most amax / 254 (and a few parts in 10^7: v * 127 / amax is formed in fp32, so
+ * that a value so near to half way between two codes may get either).  Values that share a scale with an infinity
  * or a NaN get the scale NaN (the codes are then unspecified), so that it is not
  * lost in whatever the codes are used for.  A scale belongs to a row (block = 0,
  * scales [M]: one per token) or to 128 columns of a row (block = 128, scales
@@ -313,7 +314,7 @@ CODA_API coda_status_t coda_bwd(const coda_bf16* dy, const coda_bf16* x, const c
 
 /* Codes and scales of a tensor.
  *   x [M, n] bf16 in;  q_out [M, n] INT8 out;  s_out [M] or [M, ceil(n / 128)] fp32 out
- * n a positive multiple of 8; block 0 or 128. */
+ * n a positive multiple of 8, at most 2^27 - 2^11 (here and in coda_dequant_q8); block 0 or 128. */
 CODA_API coda_status_t coda_quant_q8(const coda_bf16* x, int64_t M, int64_t n, int block,
                                      int8_t* q_out, float* s_out, cudaStream_t stream);
 
@@ -490,7 +491,8 @@ CODA_API coda_status_t coda_fwd_unfused(const coda_bf16* x, const coda_bf16* W0,
  * time each launch on the launching stream.  coda_fwd, coda_fwd_swiglu,
  * coda_fwd_unfused, coda_fwd_fp8 and coda_bwd_swiglu_dgrad launch 3 kernels
  * (2 for the forwards with the folded row reduction), coda_bwd 5,
- * coda_bwd_dgrad 1.  The events are caller-owned; pass NULL to stop.
+ * coda_bwd_dgrad 1, coda_bwd_swiglu_dgrad_q8 3, coda_matmul_q8 1 to 3 and the
+ * other 8-bit operators 1.  The events are caller-owned; pass NULL to stop.
  * Process-wide setting, not thread-safe; no effect on results.
  */
 CODA_API void coda_set_launch_events(cudaEvent_t* events, int n);

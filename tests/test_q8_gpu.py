@@ -491,6 +491,32 @@ def test_on_another_stream_and_from_a_graph(B, M):
     clean(B)
 
 
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_memory_of_a_call_on_another_stream_is_not_handed_out(B, raw):
+    """Outputs and workspace that a call allocates while its work waits on another stream: what
+    is allocated next on the current stream, of the same sizes, must not get their memory."""
+    side = torch.cuda.Stream()
+    p = product_inputs(200, 2048, 512, False, seed=6)
+    t = bwd_inputs(64, 128, 512, 128, seed=7)
+    args = [t[k] for k in ("dout", "W2", "y_q", "y_s", "W1", "h", "r", "gamma")]
+    want = B.coda_matmul_q8(*p[:4])
+    want_b = B.coda_bwd_swiglu_dgrad_q8(*args, want_a=True)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+    handle = side.cuda_stream if raw else side
+    got = B.coda_matmul_q8(*p[:4], stream=handle)
+    got_b = B.coda_bwd_swiglu_dgrad_q8(*args, want_a=True, stream=handle)
+    need = B.coda_matmul_q8_workspace_bytes(200, 2048, 512)
+    need_b = B.coda_bwd_swiglu_dgrad_workspace_bytes(64, 128, 512, 128)
+    other = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF) for n in (need, need_b) * 3]
+    side.synchronize()
+    assert torch.equal(got, want)
+    for a, b in zip(got_b, want_b):
+        assert torch.equal(a, b)
+    assert all((o == 0xFF).all() for o in other)
+
+
 @pytest.mark.parametrize("M", [2, 130])
 def test_two_streams_at_once(B, M):
     """The same product on two streams, each with a workspace of its own, back to back."""
