@@ -583,3 +583,31 @@ def test_long_offsets(B):
     h2, q2, s2 = B.coda_add_rmsnorm_q8(tail, gamma, 1e-5, z=tail)
     assert torch.equal(h[-16:], h2) and torch.equal(q[-16:], q2) and torch.equal(s[-16:], s2)
     clean(B)
+
+
+@pytest.mark.parametrize("M,K,N", [(8, 65536, 36864), (64, 65536, 36864), (70000, 32, 32768)])
+def test_long_offsets_of_products(B, M, K, N):
+    """More than 2^31 codes of W, or more than 2^31 outputs."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    a_q, a_s, W_q, w_s, _ = product_inputs(M, K, N, False, seed=3)
+    y = B.coda_matmul_q8(a_q, a_s, W_q, w_s)
+    rows = [0, M // 2, M - 1]
+    for at in (0, N - 64):
+        cols = slice(at, at + 64)
+        check_product(y[rows][:, cols], a_q[rows], a_s[rows], W_q[:, cols].contiguous(), w_s[cols], None)
+    clean(B)
+
+
+def test_long_offsets_of_the_backward(B):
+    """More than 2^31 codes of the checkpoint and values of dy."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    M, d, N1, Dout = 80000, 64, 28672, 64
+    t = bwd_inputs(M, d, N1, Dout, seed=5)
+    keys = ("dout", "W2", "y_q", "y_s", "W1", "h", "r", "gamma")
+    dy, s, dh, a = B.coda_bwd_swiglu_dgrad_q8(*(t[k] for k in keys), want_a=True)
+    rows = torch.tensor([0, 40001, M - 2, M - 1], device="cuda")
+    few = {k: (t[k] if k in ("W1", "W2", "gamma") else t[k][rows]) for k in keys}
+    check_bwd((dy[rows], s[rows], dh[rows], a[rows]), bwd_ref(few))
+    clean(B)
