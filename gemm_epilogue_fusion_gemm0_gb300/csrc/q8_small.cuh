@@ -108,7 +108,10 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kGroups <= 2 ? 2 : 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // (from one lane: known to be the same in the whole warp, which keeps a copy's operands uniform)
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const bool issuer = elect_one();
   const int g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % split;
   const int n0 = static_cast<int>(blockIdx.x) / split * kSmallChannels;
@@ -149,11 +152,11 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kGroups <= 2 ? 2 : 1)
   int issued = min(count, kStagesS);
   // While the kernel before this one finishes, the ring's first boxes of W are brought
   // into L2 (the point of coherence: nothing is read into this kernel yet).
-  if (lane == 0)
+  if (issuer)
     for (int i = 0; i < issued; ++i)
       tma_prefetch_l2_2d(&tmW, n0, (first + i * stride) * kSmallStep);
   griddep_wait();
-  if (lane == 0)
+  if (issuer)
     for (int i = 0; i < issued; ++i) issue(i);
 
   float acc[8][kGroups][4];
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kGroups <= 2 ? 2 : 1)
     }
     __syncwarp();  // every lane has its part of the stage
     if (issued < count) {
-      if (lane == 0) issue(issued);
+      if (issuer) issue(issued);
       ++issued;
     }
 #pragma unroll
