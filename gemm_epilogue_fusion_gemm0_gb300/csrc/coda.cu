@@ -400,7 +400,7 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(count) >> (i + 1) << (i + 1));
-        cfg.blockDim = dim3(kMidThreads);
+        cfg.blockDim = dim3(mid_threads(false));
         cfg.dynamicSmemBytes = MidShape<false>::kBytes;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
@@ -1043,7 +1043,7 @@ cudaError_t launch_product_small(const SmallQ8Params& p, const uint8_t* a_q, con
 //                                20.9 against 19.6
 //   mid-size (q8_mid.cuh)        up to kMidSure tokens, and beyond while its estimate is the lower one
 //   whole GEMM                   a and W widened to bf16 in the workspace first
-constexpr int64_t kMidSure = 1024;  // 1024 x 4096 x 14336: 86 us against 100
+constexpr int64_t kMidSure = 1024;  // 1024 x 4096 x 14336: 88 us against 100
 
 bool product_small(int64_t M, int64_t K, int64_t N) {
   return M <= 16 || (M <= kSmallMaxTokens && K * N < (int64_t(3) << 24));
@@ -1059,8 +1059,9 @@ double product_gemm_ns(int64_t M, int64_t K, int64_t N, int pairs) {
 
 // Tokens per CTA pair, pairs along K and blocks per SM of the mid-size product: those with the
 // least estimated time, waves of clusters times a cluster's.  Measured on GB300: a step of 64 rows
-// takes 1.33 ns per token and at least 200 ns (q8_mid.cuh; two blocks on an SM 186 ns each, their
-// share of HBM), a pair's start and its sums' way out about 3 us and 10 ns per token, a split's
+// takes 1.33 ns per token (the tensor cores), below about 300 tokens 235 ns and 0.53 ns per token
+// (the way from a stage to a slot), two blocks on an SM 364 ns and 1.09 ns per token for both; a
+// pair's start and its sums' way out about 3 us and 10 ns per token, a split's
 // exchange 2 us and 10 ns per token more.
 struct MidPlan {
   int tokens, split;
@@ -1082,7 +1083,7 @@ MidPlan plan_mid(int64_t M, int64_t K, int64_t N, const int (*clusters)[3]) {
       for (int narrow = 0; narrow < 2; ++narrow) {
         // a narrow block alone on its SM is a wide one with shorter rings
         if (narrow && (tokens > MidShape<true>::kTokens || tiles <= clusters[0][i])) break;
-        const double step = narrow ? 2.0 * std::max(1.33 * t, 186.0) : std::max(1.33 * t, 200.0);
+        const double step = narrow ? 364.0 + 1.09 * t : std::max(1.33 * t, 235.0 + 0.53 * t);
         const double pair = static_cast<double>(cdiv(nk, s)) * step + 3000.0 + 10.0 * t +
                             (s > 1 ? 2000.0 + 10.0 * t : 0.0);
         const double ns = static_cast<double>(cdiv(tiles, clusters[narrow][i])) * pair;
@@ -1093,35 +1094,30 @@ MidPlan plan_mid(int64_t M, int64_t K, int64_t N, const int (*clusters)[3]) {
   return best;
 }
 
-cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t* W_q, void* x16,
+cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t* W_q,
                                const MidPlan& plan, cudaStream_t stream) {
   p.tokens = plan.tokens;
   p.split = plan.split;
   p.parts = p.tokens > 256 ? 2 : 1;
-  // The rings: as many of the tokens' stages as tensor memory has slots for, W's ring the rest.
-  const int x_stage = p.tokens * kMidK;  // bytes of a CTA's half
-  const int slots =
-      std::min(kMidMaxSlots, (static_cast<int>(plan.narrow ? MidShape<true>::kCols
-                                                           : MidShape<false>::kCols) -
-                              (p.tokens + 31) / 32 * 32) / 32);
-  p.pairs_slots = slots / 2;
-  const uint32_t rings = plan.narrow ? MidShape<true>::kRings : MidShape<false>::kRings;
-  p.pairs_w = std::min<int>(kMidMaxStages,
-                            (rings - 2 * p.pairs_slots * x_stage) / kMidWBytes) / 2;
+  p.tok_warps = std::min(plan.narrow ? 2 : 4, static_cast<int>(cdiv(p.tokens, 64)));
+  // As many slots as tensor memory holds and as leave six stages; the stages have the rest.
+  const int rings = static_cast<int>(plan.narrow ? MidShape<true>::kRings : MidShape<false>::kRings);
+  const int cols = static_cast<int>(plan.narrow ? MidShape<true>::kCols : MidShape<false>::kCols);
+  const int stage = static_cast<int>(mid_stage_bytes(p.tokens));
+  const int slot = static_cast<int>(mid_slot_bytes(p.tokens));
+  p.pairs_slots = std::min({kMidMaxSlots, (cols - (p.tokens + 31) / 32 * 32) / 32,
+                            (rings - 6 * stage) / slot}) / 2;
+  p.pairs_stages = std::min(kMidMaxStages, (rings - 2 * p.pairs_slots * slot) / stage) / 2;
   CUtensorMap mW, mX;
   if (!tmap_2d_u8(&mW, W_q, p.N, p.K, kMidChannels, kMidK) ||
-      !tmap_2d(&mX, x16, p.K, p.M, kMidK, p.tokens / p.parts / 2))
+      !tmap_2d_u8(&mX, a_q, p.K, p.M, kMidK, p.tokens / p.parts / 2, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  const size_t n16 = static_cast<size_t>(p.M) * p.K / 16;
-  cudaError_t e = launch(q8_to_f16_kernel, static_cast<int>(cdiv(n16, 256)), 256, 0, stream, false,
-                         a_q, static_cast<uint4*>(x16), n16);
-  if (e != cudaSuccess) return e;
-  after_launch(0, stream);
   const int64_t grid = cdiv(p.N, 2 * kMidChannels) * cdiv(p.M, p.tokens) * 2 * p.split;
-  e = launch_cluster(plan.narrow ? kProductNarrow : kProductMid, static_cast<int>(grid), kMidThreads,
-                     plan.narrow ? MidShape<true>::kBytes : MidShape<false>::kBytes, stream, false,
-                     2 * p.split, mW, mX, p, g_timeout_ns.load());
-  if (e == cudaSuccess) after_launch(1, stream);
+  const cudaError_t e = launch_cluster(
+      plan.narrow ? kProductNarrow : kProductMid, static_cast<int>(grid), mid_threads(plan.narrow),
+      plan.narrow ? MidShape<true>::kBytes : MidShape<false>::kBytes, stream, false, 2 * p.split, mW, mX,
+      p, g_timeout_ns.load());
+  if (e == cudaSuccess) after_launch(0, stream);
   return e;
 }
 
@@ -1733,11 +1729,10 @@ coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* z, const 
   return CODA_OK;
 }
 
-// Nothing for few tokens; [slot | a as fp16 integers] up to kMidSure; then
-// [slot | a as bf16 (or fp16) integers | W as bf16 integers | split-tail region]
+// Nothing up to kMidSure tokens; then
+// [slot | a as bf16 integers | W as bf16 integers | split-tail region]
 size_t coda_matmul_q8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-  if (check_product(M, K, N) != CODA_OK || product_small(M, K, N)) return 0;
-  if (M <= kMidSure) return kSlotBytes + align256(static_cast<size_t>(M) * K * 2);
+  if (check_product(M, K, N) != CODA_OK || M <= kMidSure) return 0;
   return kSlotBytes + align256(static_cast<size_t>(M) * K * 2) +
          align256(static_cast<size_t>(K) * N * 2) + sk_region_bytes(cdiv(M, kPairBM) * cdiv(N, kBN));
 }
@@ -1783,10 +1778,8 @@ coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* 
     return CODA_OK;
   }
   char* wsb = static_cast<char*>(workspace);
-  // the mid-size form also widens the tokens: 3 us and their bytes
   const MidPlan plan = plan_mid(M, K, N, clusters);
-  if (M <= kMidSure || plan.ns + 3000.0 + 3.0 * static_cast<double>(M) * K / 6200.0 <
-                           product_gemm_ns(M, K, N, max_pairs)) {
+  if (M <= kMidSure || plan.ns < product_gemm_ns(M, K, N, max_pairs)) {
     MidQ8Params mp = {};
     mp.a_s = a_s;
     mp.w_s = w_s;
@@ -1796,8 +1789,7 @@ coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* 
     mp.K = Ki;
     mp.N = Ni;
     if (launch_product_mid(mp, reinterpret_cast<const uint8_t*>(a_q),
-                           reinterpret_cast<const uint8_t*>(W_q), wsb + kSlotBytes, plan,
-                           stream) != cudaSuccess) {
+                           reinterpret_cast<const uint8_t*>(W_q), plan, stream) != cudaSuccess) {
       cudaGetLastError();
       return CODA_ERR_LAUNCH;
     }

@@ -13,30 +13,37 @@
 // CTA, and up to 384 tokens, half of which each CTA holds for both.  Shared memory then sees a
 // code of W twice (TMA in, read out) and not the 16-bit form at all: with the operand in shared
 // memory instead it would be written and read there too, three times the traffic.  256 tokens
-// take 48 KB of it per step of 64 rows and 512 cycles of products; on single CTAs, each with all
-// the tokens, they took 80 KB, and shared memory's 128 bytes per cycle were the bound (1024 x
-// 4096 x 14336: 86 us).
+// take 64 KB of it per step of 64 rows (W 16, the tokens' codes 16, widened 32), as long at 128
+// bytes a cycle as their products, 512 cycles.  Single CTAs, each with all the tokens, would
+// move half as much again.
 //
-// The tokens' codes are few: a pass of their own widens them to fp16 in the workspace.
+// The tokens' codes are widened by other warps from shared memory to shared memory, in every
+// block that uses them.  A pass of their own before the product spared shared memory that work,
+// but was a second launch and a workspace, 5 us of host time: 38 x 112 x 4960 as called 28 us
+// with it and 20 without, captured 64 x 4096 x 14336 20.2 us and 19.0, 333 tokens of it 36.3 and
+// 35.0, 1024 tokens 84.7 and 88.5, 128 x 4096 x 28672 33.4 and 37.3.
 //
-// Block = 352 threads; one block per SM, or two where a pair has at most 128 tokens and there are
+// One block of 576 threads per SM, or two of 448 where a pair has at most 128 tokens and there is
 // more than one wave of them (kNarrow: half the tensor memory and shared memory); in each CTA:
-//   warp 0      TMA producer of W: a ring of stages of 128 channels x 64 rows, INT8 (8 KB)
+//   warp 0      TMA producer: a ring of stages of W (128 channels x 64 rows, 8 KB) and of this
+//               CTA's half of the tokens (x 64 codes), INT8
 //   warp 1      allocates tensor memory; in CTA 0 one thread issues tcgen05.mma (M = 256, N =
-//               tokens, K = 16; two of them above 256 tokens) from operand slots of 32 columns
-//   warps 2..9  widen their quadrant's 32 channels of a stage of W into a slot (two sets of
-//               four warps take the stages in turn) and give W's stage back at once; after
-//               the last stage they are the epilogue.  W's ring and the slots are even in
-//               number, so that a stage and a slot always belong to the same set: a set that
-//               met one in the next round while the other set still owed it the round
-//               before could not tell the two by the parity of its barrier.
-//   warp 10     TMA producer of this CTA's half of the tokens x 64, fp16, a stage per slot
-// A slot and the tokens' stage of the same K form one step for the issuing thread: the eight
-// warps of both CTAs and the TMA arrive on CTA 0's `ready` barrier of the slot and one commit
-// frees both in both CTAs.  That thread is what few tokens wait for: a step takes it about 420
-// cycles (64 tokens' products take 128; W's 8 KB are 350 cycles of an SM's share of HBM).  It was
-// 630 with one lane in a branch of its own, where descriptors are not warp-uniform, and 700
-// with a barrier and a commit each for the slot and the tokens.
+//               tokens, K = 16; two of them above 256 tokens) from slots: 32 columns of tensor
+//               memory (W) and a swizzled tile of shared memory (the tokens)
+//   warps 2..9  widen their quadrant's 32 channels of a stage of W into a slot, two sets of
+//               four warps taking the stages in turn; after the last stage they are the epilogue
+//   warps 10..  widen a stage's tokens into a slot, two sets in turn of as many warps as have
+//               four chunks of 16 codes per lane (64 tokens each, at most four; two in kNarrow):
+//               with 256 tokens four took 28.6 us and two 31.5, with 128 two 23.2 and one 27.6,
+//               with 64 one 18.9 and two 19.1 (K = 4096, N = 14336)
+// Stages and slots are even in number, so that each always belongs to the same sets: a set that
+// met one in the next round while the other set still owed it the round before could not
+// tell the two by the parity of its barrier.
+// All warps of both CTAs that fill a slot arrive on CTA 0's `ready` barrier of it and one
+// commit frees it in both CTAs.  The issuing thread is what few tokens wait for: a step takes it
+// about 400 cycles (64 tokens' products take 128; W's 8 KB are 350 cycles of an SM's share of
+// HBM).  It was 630 with one lane in a branch of its own, where descriptors are not
+// warp-uniform.
 //
 // Widening: a code becomes fp16 by its bits, 0x6400 | (code + 128) = 1024 + 128 + code, and a
 // packed subtraction of 1152 leaves it exactly.  A thread (g = lane / 4, t = lane % 4) reads
@@ -44,7 +51,8 @@
 // operands in the store's 16-lane x 256-bit form: channel 4 g + b goes to lane g + 8 b.
 // For t >= 2 the rows are read as 2, 3, 0, 1, which with the 128-byte swizzle gives every
 // read 32 banks; the k order that follows (k 8..15 of each 16 as 10 11 8 9 14 15 12 13) is
-// the same in the tokens' fp16 form, and a sum does not mind.
+// the same in the tokens' fp16 form, and a sum does not mind.  A lane widens 16 codes of a token
+// at a time (16 bytes in, two swizzled 16-byte groups out), free of bank conflicts both ways.
 //
 // Small N leaves SMs idle, so a cluster of up to four pairs may share a tile along K.  The
 // fp32 sums go to shared memory as [token][channel] and each CTA adds and writes its share of
@@ -59,11 +67,11 @@ constexpr int kMidChannels = 128;
 constexpr int kMidK = 64;  // rows of W per stage
 constexpr uint32_t kMidWBytes = kMidK * kMidChannels;  // 8 KB
 
-constexpr int kMidThreads = 352;
+__host__ __device__ constexpr int mid_threads(bool narrow) { return narrow ? 448 : 576; }
 constexpr int kMidMaxTokens = 384;     // per CTA pair
-constexpr int kMidMaxStages = 12;      // of W's ring (per CTA)
+constexpr int kMidMaxStages = 12;      // of the ring of codes (per CTA)
 constexpr int kMidMaxSplit = 4;        // CTA pairs per tile along K
-constexpr int kMidMaxSlots = 8;        // of the widened W, and stages of the tokens
+constexpr int kMidMaxSlots = 8;        // of widened codes
 
 // kNarrow: at most 128 tokens per pair and room for two blocks on an SM.
 template <bool kNarrow>
@@ -87,30 +95,18 @@ struct MidQ8Params {
   int tokens;  // per CTA pair: a multiple of 16, of 32 above 256
   int parts;   // instructions of tokens / parts tokens per 16 rows of K: 2 above 256, else 1
   int split;   // CTA pairs per tile along K (the cluster)
-  int pairs_w;      // pairs of stages of W's ring, at most kMidMaxStages / 2
-  int pairs_slots;  // pairs of slots and of the tokens' stages, at most kMidMaxSlots / 2
+  int pairs_stages;  // pairs of stages of codes, at most kMidMaxStages / 2
+  int tok_warps;     // warps that widen a stage's tokens
+  int pairs_slots;   // pairs of slots, at most kMidMaxSlots / 2
 };
 
-// The tokens' codes in fp16, in the k order of the widened W: 16 codes per thread.  Unlike the
-// other kernels it lets the next one start only after its own wait, so that whatever came
-// before both has completed by then and the product may read W while this pass runs.
-__global__ void __launch_bounds__(256) q8_to_f16_kernel(const uint8_t* __restrict__ q,
-                                                        uint4* __restrict__ x, size_t n16) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n16) return;
-  const uint4 c = __ldg(reinterpret_cast<const uint4*>(q) + i);
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t v = w[k] ^ 0x80808080u;
-    o[2 * k] = q8_less_1152(__byte_perm(v, 0x64646464u, 0x4140));
-    o[2 * k + 1] = q8_less_1152(__byte_perm(v, 0x64646464u, 0x4342));
-  }
-  x[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
-  x[2 * i + 1] = make_uint4(o[5], o[4], o[7], o[6]);
+// Bytes of a stage of codes (W's, then the half of the tokens; whole swizzle atoms) and of a slot's
+// tile of tokens.
+__host__ __device__ constexpr uint32_t mid_stage_bytes(int tokens) {
+  return kMidWBytes + (static_cast<uint32_t>(tokens / 2 * kMidK) + 1023u) / 1024u * 1024u;
+}
+__host__ __device__ constexpr uint32_t mid_slot_bytes(int tokens) {
+  return static_cast<uint32_t>(tokens / 2 * kMidK * 2);
 }
 
 // 16 lanes x 32 columns of tensor memory: thread (g, t) writes columns 8 i + 2 t, 8 i + 2 t + 1
@@ -150,6 +146,17 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
                : "memory");
 }
 
+// Arrive on a barrier of either CTA; what this CTA's threads wrote to their own shared memory and
+// fenced for the async proxy is the tensor cores' to read.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Generic writes of this thread to shared memory become visible to the async proxy.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -180,20 +187,21 @@ struct RingPos {
 };
 
 template <bool kNarrow>
-__global__ void __launch_bounds__(kMidThreads, kNarrow ? 2 : 1)
+__global__ void __launch_bounds__(mid_threads(kNarrow), kNarrow ? 2 : 1)
     product_q8_mid_kernel(const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmX, const MidQ8Params p,
                           uint64_t timeout_ns) {
+  constexpr int kMidThreads = mid_threads(kNarrow);
   constexpr uint32_t kMidRings = MidShape<kNarrow>::kRings, kMidCols = MidShape<kNarrow>::kCols;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
-  // barriers: W full | W empty | slot ready | slot free | done, then the TMEM address holder
-  // and the abort flag
-  const uint32_t bar_wfull = base + kMidRings;
-  const uint32_t bar_wempty = bar_wfull + 8u * kMidMaxStages;
-  const uint32_t bar_ready = bar_wempty + 8u * kMidMaxStages;
+  // barriers: stage full | stage empty | slot ready | slot free | done, then the TMEM address
+  // holder and the abort flag
+  const uint32_t bar_full = base + kMidRings;
+  const uint32_t bar_empty = bar_full + 8u * kMidMaxStages;
+  const uint32_t bar_ready = bar_empty + 8u * kMidMaxStages;
   const uint32_t bar_free = bar_ready + 8u * kMidMaxSlots;
   const uint32_t bar_done = bar_free + 8u * kMidMaxSlots;
   constexpr uint32_t kAfterBars = kMidRings + 8 * (2 * kMidMaxStages + 2 * kMidMaxSlots + 1);
@@ -205,11 +213,11 @@ __global__ void __launch_bounds__(kMidThreads, kNarrow ? 2 : 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
     for (int s = 0; s < kMidMaxStages; ++s) {
-      mbar_init(bar_wfull + 8u * s, 1);
-      mbar_init(bar_wempty + 8u * s, 4);  // the four warps that read the stage
+      mbar_init(bar_full + 8u * s, 1);
+      mbar_init(bar_empty + 8u * s, 4 + p.tok_warps);  // the warps that read the stage
     }
     for (int s = 0; s < kMidMaxSlots; ++s) {
-      mbar_init(bar_ready + 8u * s, 9);  // four warps of each CTA, the tokens' producer (with the bytes)
+      mbar_init(bar_ready + 8u * s, 2 * (4 + p.tok_warps));  // the same warps, of both CTAs
       mbar_init(bar_free + 8u * s, 1);
     }
     mbar_init(bar_done, 1);
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(kMidThreads, kNarrow ? 2 : 1)
   const int n0 = tile / mt * (2 * kMidChannels) + static_cast<int>(half) * kMidChannels;
   const int m0 = tile % mt * p.tokens;
   // its stages of K: kb0 .. kb0 + nkb - 1
-  const int stages_w = 2 * p.pairs_w, slots = 2 * p.pairs_slots;
+  const int stages = 2 * p.pairs_stages, slots = 2 * p.pairs_slots;
   const int nk = (p.K + kMidK - 1) / kMidK;
   const int kb0 = static_cast<int>(static_cast<long long>(nk) * rank / p.split);
   int nkb = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / p.split) - kb0;
@@ -253,68 +261,50 @@ __global__ void __launch_bounds__(kMidThreads, kNarrow ? 2 : 1)
     }
   }
 
-  // The kernel before this one is the pass that widens the tokens, which starts this one after
-  // its own wait: everything before it has completed, and only the tokens' producer waits here.
-  const uint32_t x_bytes = static_cast<uint32_t>(p.tokens) * kMidK;  // this CTA's half, 2 bytes each
-  const uint32_t sX = base + static_cast<uint32_t>(stages_w) * kMidWBytes;
-
   const int n_mma = p.tokens / p.parts;  // tokens of one instruction
+  const uint32_t stage_bytes = mid_stage_bytes(p.tokens), slot_bytes = mid_slot_bytes(p.tokens);
+  const uint32_t sX = base + static_cast<uint32_t>(stages) * stage_bytes;  // the slots' tokens
+  const bool issuer = elect_one();
+  // While the kernel before this one finishes, the ring's first boxes of W are brought into L2
+  // (the point of coherence: nothing is read into this kernel yet).
+  if (warp == 0 && issuer)
+    for (int i = 0; i < min(nkb, stages); ++i) tma_prefetch_l2_2d(&tmW, n0, (kb0 + i) * kMidK);
+  griddep_wait();
+
   if (warp == 0) {
-    // ------------------------------------------------------------ producer of W
-    const bool issuer = elect_one();
-    RingPos r(0, stages_w);
-    int i = 0;
-    for (; i < nkb; ++i, r.step(1)) {
-      if (!__all_sync(0xffffffffu,
-                      bounded_wait(bar_wempty + 8u * r.s, r.ph ^ 1u, wc, kSiteProducerEmpty)))
-        break;
-      if (!checked(tma_start_ok(n0, (kb0 + i) * kMidK, p.N, p.K, 1), kChkTmaB)) {
-        *wc.abort_flag = 1u;
-        break;
-      }
-      if (issuer) {
-        mbar_arrive_expect_tx(bar_wfull + 8u * r.s, kMidWBytes);
-        tma_load_2d(base + r.s * kMidWBytes, &tmW, bar_wfull + 8u * r.s, n0, (kb0 + i) * kMidK);
-      }
-      __syncwarp();
-    }
-    if (i < nkb) land_copies(bar_wfull, i, stages_w, timeout_ns);
-    __syncwarp();
-  } else if (warp == 10) {
-    // ------------------------------------------------------------ producer of the tokens
-    const bool issuer = elect_one();
-    const uint32_t ready0 = mapa_shared(bar_ready, lead);
+    // ------------------------------------------------------------ producer
     const int box = n_mma / 2, row = m0 + static_cast<int>(half) * box;
-    griddep_wait();
-    RingPos r(0, slots);
+    const uint32_t bytes = kMidWBytes + static_cast<uint32_t>(p.tokens / 2 * kMidK);
+    RingPos r(0, stages);
     int i = 0;
     for (; i < nkb; ++i, r.step(1)) {
       if (!__all_sync(0xffffffffu,
-                      bounded_wait(bar_free + 8u * r.s, r.ph ^ 1u, wc, kSiteProducerEmpty)))
+                      bounded_wait(bar_empty + 8u * r.s, r.ph ^ 1u, wc, kSiteProducerEmpty)))
         break;
-      if (!checked(tma_start_ok((kb0 + i) * kMidK, m0, p.K, p.M, 2), kChkTmaA)) {
+      const int k = (kb0 + i) * kMidK;
+      if (!checked(tma_start_ok(n0, k, p.N, p.K, 1), kChkTmaB) ||
+          !checked(tma_start_ok(k, m0, p.K, p.M, 1), kChkTmaA)) {
         *wc.abort_flag = 1u;
         break;
       }
       if (issuer) {
-        const uint32_t ready = ready0 + 8u * r.s, dst = sX + r.s * x_bytes;
-        if (half == 0) mbar_arrive_expect_tx(bar_ready + 8u * r.s, 2u * x_bytes);
+        const uint32_t full = bar_full + 8u * r.s, dst = base + r.s * stage_bytes;
+        mbar_arrive_expect_tx(full, bytes);
+        tma_load_2d(dst, &tmW, full, n0, k);
         // an instruction's tokens: the first half of them in CTA 0, the second in CTA 1
-        tma_load_2d_pair(dst, &tmX, ready, (kb0 + i) * kMidK, row);
+        tma_load_2d(dst + kMidWBytes, &tmX, full, k, row);
         if (p.parts > 1)
-          tma_load_2d_pair(dst + static_cast<uint32_t>(box) * kMidK * 2, &tmX, ready,
-                           (kb0 + i) * kMidK, row + n_mma);
+          tma_load_2d(dst + kMidWBytes + static_cast<uint32_t>(box * kMidK), &tmX, full, k, row + n_mma);
       }
       __syncwarp();
     }
-    if (i < nkb && half == 0) land_copies(bar_ready, i, slots, timeout_ns);
+    land_copies(bar_full, i, stages, timeout_ns);  // also if others gave up
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp walks the steps and one elected thread issues (here and in the producers),
     // so that descriptors and addresses stay warp-uniform.
     if (half == 0) {
-      const bool issuer = elect_one();
       const uint32_t idesc = idesc_f16_f32(2 * kMidChannels, n_mma);
       const uint64_t desc0 = sdesc_sw128(sX, 16, 1024);
       RingPos r(0, slots);
@@ -325,7 +315,7 @@ __global__ void __launch_bounds__(kMidThreads, kNarrow ? 2 : 1)
         tc_fence_after();
         const uint32_t a0 = tmem_slots + 32u * r.s;
         // shared memory ends below 2^18, so the address field (address / 16) takes the sums
-        const uint64_t b0 = desc0 + r.s * x_bytes / 16;
+        const uint64_t b0 = desc0 + r.s * slot_bytes / 16;
         if (issuer) {
 #pragma unroll
           for (int k = 0; k < kMidK / 16; ++k)
@@ -345,8 +335,53 @@ __global__ void __launch_bounds__(kMidThreads, kNarrow ? 2 : 1)
       if (issuer) umma_commit_pair_mc(bar_done, pair_mask);
     }
     __syncwarp();
+  } else if (warp >= 10 + 2 * p.tok_warps) {
+    // nothing to widen
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ widening the tokens
+    const int set = (warp - 10) & 1, first = (warp - 10) / 2 * 32 + lane;
+    const int chunks = p.tokens / 2 * 4;  // 16 codes each, four to a row
+    const uint32_t ready0 = mapa_shared(bar_ready, lead);
+    RingPos r(set, stages), slot(set, slots);
+    for (int i = set; i < nkb; i += 2, r.step(2), slot.step(2)) {
+      if (!__all_sync(0xffffffffu,
+                      bounded_wait(bar_full + 8u * r.s, r.ph, wc, kSiteEpiTmemFull) &&
+                          bounded_wait(bar_free + 8u * slot.s, slot.ph ^ 1u, wc, kSiteMmaTmemEmpty)))
+        break;
+      const uint32_t src = base + r.s * stage_bytes + kMidWBytes, dst = sX + slot.s * slot_bytes;
+      for (int q0 = first; q0 < chunks; q0 += 4 * 32 * p.tok_warps) {  // four reads under way
+        uint4 v[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          v[b] = ld_shared_v4(
+              src + 16u * static_cast<uint32_t>(min(q0 + 32 * p.tok_warps * b, chunks - 1)));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t q = static_cast<uint32_t>(q0 + 32 * p.tok_warps * b);
+          if (q >= static_cast<uint32_t>(chunks)) break;
+          const uint32_t row = q >> 2, c = q & 3u;
+          const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t u = w[k] ^ 0x80808080u;
+            o[2 * k] = q8_less_1152(__byte_perm(u, 0x64646464u, 0x4140));
+            o[2 * k + 1] = q8_less_1152(__byte_perm(u, 0x64646464u, 0x4342));
+          }
+          const uint32_t line = dst + 128u * row;
+          st_shared_v4(line + 16u * ((2u * c) ^ (row & 7u)), o[0], o[1], o[2], o[3]);
+          st_shared_v4(line + 16u * ((2u * c + 1u) ^ (row & 7u)), o[5], o[4], o[7], o[6]);
+        }
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar_empty + 8u * r.s);
+        mbar_arrive_remote(ready0 + 8u * slot.s);
+      }
+    }
   } else {
-    // ------------------------------------------------------------ widening
+    // ------------------------------------------------------------ widening W
     const uint32_t quad = warp & 3;
     const uint32_t g = lane >> 2, t = lane & 3;
     // this thread's word of row r of 16: chunk (2 quad + g / 4) ^ (r % 8), word g % 4
@@ -358,19 +393,19 @@ __global__ void __launch_bounds__(kMidThreads, kNarrow ? 2 : 1)
       at[j] = 128u * r + 16u * (chunk ^ (r & 7u)) + 4u * (g & 3u);
     }
     const int set = (warp - 2) >> 2;  // set 0: even stages, set 1: odd ones
-    RingPos r(set, stages_w), slot(set, slots);
+    RingPos r(set, stages), slot(set, slots);
     for (int i = set; i < nkb; i += 2, r.step(2), slot.step(2)) {
       if (!__all_sync(0xffffffffu,
-                      bounded_wait(bar_wfull + 8u * r.s, r.ph, wc, kSiteEpiTmemFull)))
+                      bounded_wait(bar_full + 8u * r.s, r.ph, wc, kSiteEpiTmemFull)))
         break;
-      const uint32_t src = base + r.s * kMidWBytes;
+      const uint32_t src = base + r.s * stage_bytes;
       uint32_t l[4][4];
 #pragma unroll
       for (uint32_t c = 0; c < 4; ++c)
 #pragma unroll
         for (int j = 0; j < 4; ++j) l[c][j] = ld_shared_u32(src + 2048u * c + at[j]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_wempty + 8u * r.s);
+      if (lane == 0) mbar_arrive(bar_empty + 8u * r.s);
       uint32_t v01[16], v23[16];  // channels 0, 1 (lanes g, g + 8) and 2, 3 (g + 16, g + 24)
 #pragma unroll
       for (uint32_t c = 0; c < 4; ++c)

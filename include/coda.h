@@ -344,7 +344,7 @@ CODA_API coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* 
  * K and N positive multiples of 16; codes may be anything in [-128, 127].  Sums are fp32 sums of
  * exact products: exact while they stay below 2^24.  A NaN scale makes its row or column NaN.
  * workspace: at least coda_matmul_q8_workspace_bytes(M, K, N); NULL will do where that is 0
- * (few tokens). */
+ * (up to 1024 tokens). */
 CODA_API size_t coda_matmul_q8_workspace_bytes(int64_t M, int64_t K, int64_t N);
 CODA_API coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* W_q,
                                       const float* w_s, const coda_bf16* z, int64_t M, int64_t K,

@@ -103,10 +103,10 @@ def test_product_shapes_and_workspace(B):
     assert _product(B, N=-16) == B.CODA_ERR_INVALID_ARG
     for bad in ({"K": 24}, {"N": 40}, {"K": 1 << 31}, {"N": 1 << 31}):
         assert _product(B, **bad) == B.CODA_ERR_UNSUPPORTED_SHAPE
-    for M, K, N in ((1, 16, 16), (16, 8192, 57344), (32, 4096, 4096)):  # few tokens: none
+    for M, K, N in ((1, 16, 16), (32, 8192, 8192), (1024, 4096, 4096)):  # up to 1024 tokens: none
         assert B.coda_matmul_q8_workspace_bytes(M, K, N) == 0
         assert _product(B, M, K, N, ws=FAKE + 4) == B.CODA_ERR_MISALIGNED
-    for M, K, N in ((33, 16, 16), (32, 8192, 8192), (300, 1040, 784), (8192, 4096, 28672)):
+    for M, K, N in ((1025, 16, 16), (2048, 1040, 784), (8192, 4096, 28672)):
         need = B.coda_matmul_q8_workspace_bytes(M, K, N)
         assert need > 0
         assert _product(B, M, K, N, wsb=need - 1) == B.CODA_ERR_WORKSPACE_TOO_SMALL
