@@ -491,7 +491,7 @@ CODA_API coda_status_t coda_fwd_unfused(const coda_bf16* x, const coda_bf16* W0,
  * time each launch on the launching stream.  coda_fwd, coda_fwd_swiglu,
  * coda_fwd_unfused, coda_fwd_fp8 and coda_bwd_swiglu_dgrad launch 3 kernels
  * (2 for the forwards with the folded row reduction), coda_bwd 5,
- * coda_bwd_dgrad 1, coda_bwd_swiglu_dgrad_q8 3, coda_matmul_q8 1 to 3 and the
+ * coda_bwd_dgrad 1, coda_bwd_swiglu_dgrad_q8 3, coda_matmul_q8 1 or 3 and the
  * other 8-bit operators 1.  The events are caller-owned; pass NULL to stop.
  * Process-wide setting, not thread-safe; no effect on results.
  */
