@@ -1043,7 +1043,7 @@ cudaError_t launch_product_small(const SmallQ8Params& p, const uint8_t* a_q, con
 //                                20.9 against 19.6
 //   mid-size (q8_mid.cuh)        up to kMidSure tokens, and beyond while its estimate is the lower one
 //   whole GEMM                   a and W widened to bf16 in the workspace first
-constexpr int64_t kMidSure = 1024;  // 1024 x 4096 x 14336: 88 us against 100
+constexpr int64_t kMidSure = 1024;  // 1025 x 4096 x 14336: 89 us against 114
 
 bool product_small(int64_t M, int64_t K, int64_t N) {
   return M <= 16 || (M <= kSmallMaxTokens && K * N < (int64_t(3) << 24));

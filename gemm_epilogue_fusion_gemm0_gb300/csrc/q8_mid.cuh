@@ -15,13 +15,13 @@
 // memory instead it would be written and read there too, three times the traffic.  256 tokens
 // take 64 KB of it per step of 64 rows (W 16, the tokens' codes 16, widened 32), as long at 128
 // bytes a cycle as their products, 512 cycles.  Single CTAs, each with all the tokens, would
-// move half as much again.
+// move 112 KB.
 //
 // The tokens' codes are widened by other warps from shared memory to shared memory, in every
 // block that uses them.  A pass of their own before the product spared shared memory that work,
 // but was a second launch and a workspace, 5 us of host time: 38 x 112 x 4960 as called 28 us
 // with it and 20 without, captured 64 x 4096 x 14336 20.2 us and 19.0, 333 tokens of it 36.3 and
-// 35.0, 1024 tokens 84.7 and 88.5, 128 x 4096 x 28672 33.4 and 37.3.
+// 35.0, 1024 tokens 84.7 and 88.5, 128 x 4096 x 28672 33.4 and 37.3 (the way out as it was then).
 //
 // One block of 576 threads per SM, or two of 448 where a pair has at most 128 tokens and there is
 // more than one wave of them (kNarrow: half the tensor memory and shared memory); in each CTA:
@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(mid_threads(kNarrow), kNarrow ? 2 : 1)
         // an instruction's tokens: the first half of them in CTA 0, the second in CTA 1
         tma_load_2d(dst + kMidWBytes, &tmX, full, k, row);
         if (p.parts > 1)
-          tma_load_2d(dst + kMidWBytes + static_cast<uint32_t>(box * kMidK), &tmX, full, k, row + n_mma);
+          tma_load_2d(dst + kMidWBytes + static_cast<uint32_t>(box * kMidK), &tmX, full, k,
+                      row + n_mma);
       }
       __syncwarp();
     }
@@ -464,49 +465,71 @@ __global__ void __launch_bounds__(mid_threads(kNarrow), kNarrow ? 2 : 1)
     }
     __syncwarp();
   }
+  // A thread keeps its 8 channels and takes every (threads / 16)-th of this block's tokens, which
+  // are rank, rank + split, ...  What it reads for two tokens is under way together (1024 x
+  // 4096 x 14336, three waves: 82.5 us, one token at a time 87; four at a time no faster).
+  static_assert(kMidThreads % (kMidChannels / 8) == 0, "a thread keeps its channels");
+  constexpr int kU = 2, kStride = kMidThreads / (kMidChannels / 8);
+  const int c8 = static_cast<int>(threadIdx.x) % (kMidChannels / 8) * 8, n = n0 + c8;
+  float ws[8] = {};
+  if (n < p.N) {
+    const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.w_s + n));
+    const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.w_s + n + 4));
+    ws[0] = w0.x, ws[1] = w0.y, ws[2] = w0.z, ws[3] = w0.w;
+    ws[4] = w1.x, ws[5] = w1.y, ws[6] = w1.z, ws[7] = w1.w;
+  }
   cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, kMidCols);
 
-  // This block's tokens of the tile: rank, rank + split, ...; a unit is 8 channels of a token.
   const int tokens = min(p.tokens, p.M - m0);
-  const int mine = tokens > rank ? (tokens - rank + p.split - 1) / p.split : 0;
-  for (int u = threadIdx.x; u < mine * (kMidChannels / 8); u += kMidThreads) {
-    const int tok = rank + u / (kMidChannels / 8) * p.split;
-    const int c8 = u % (kMidChannels / 8) * 8;
-    const int n = n0 + c8, m = m0 + tok;
-    if (n >= p.N) continue;
-    const uint32_t at = base + 4u * (tok * kMidChannels + c8);
-    float4 part[kMidMaxSplit][2];
+  const int mine = n < p.N && tokens > rank ? (tokens - rank + p.split - 1) / p.split : 0;
+  // the eight lanes that read shared memory together take different halves of their 32 bytes
+  const uint32_t hi = (lane >> 2) & 1;
+  for (int i0 = static_cast<int>(threadIdx.x) / (kMidChannels / 8); i0 < mine; i0 += kU * kStride) {
+    float as[kU], v[kU][8] = {};
+    Chunk8 z[kU];
 #pragma unroll
-    for (int r = 0; r < kMidMaxSplit; ++r) {
-      if (r < p.split) {
-        const uint32_t peer = mapa_shared(at, 2u * static_cast<uint32_t>(r) + half);
-        part[r][0] = ld_cluster_f4(peer);
-        part[r][1] = ld_cluster_f4(peer + 16u);
-      } else {
-        part[r][0] = part[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < kU; ++u) {
+      const bool in = i0 + u * kStride < mine;
+      const int m = m0 + rank + (i0 + u * kStride) * p.split;
+      as[u] = in ? __ldg(p.a_s + m) : 0.f;
+      if (in && p.z != nullptr) z[u] = ldg8(p.z + static_cast<size_t>(m) * p.N + n);
+    }
+#pragma unroll 1
+    for (int r = 0; r < p.split; ++r) {
+      const uint32_t peer = mapa_shared(base, 2u * static_cast<uint32_t>(r) + half);
+      float4 a[kU], b[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int tok = rank + (i0 + u * kStride) * p.split;
+        const uint32_t at = peer + 4u * static_cast<uint32_t>(tok * kMidChannels + c8);
+        a[u] = b[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + u * kStride < mine) {
+          a[u] = ld_cluster_f4(at + 16u * hi);
+          b[u] = ld_cluster_f4(at + 16u - 16u * hi);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const float4 lo4 = hi ? b[u] : a[u], hi4 = hi ? a[u] : b[u];
+        v[u][0] += lo4.x, v[u][1] += lo4.y, v[u][2] += lo4.z, v[u][3] += lo4.w;
+        v[u][4] += hi4.x, v[u][5] += hi4.y, v[u][6] += hi4.z, v[u][7] += hi4.w;
       }
     }
-    float v[8] = {};
 #pragma unroll
-    for (int r = 0; r < kMidMaxSplit; ++r) {
-      v[0] += part[r][0].x, v[1] += part[r][0].y, v[2] += part[r][0].z, v[3] += part[r][0].w;
-      v[4] += part[r][1].x, v[5] += part[r][1].y, v[6] += part[r][1].z, v[7] += part[r][1].w;
+    for (int u = 0; u < kU; ++u) {
+      if (i0 + u * kStride >= mine) break;
+      const int m = m0 + rank + (i0 + u * kStride) * p.split;
+      float zv[8] = {};
+      if (p.z != nullptr) unpack8(z[u], zv);
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = pack_bf16x2(fmaf(as[u] * v[u][2 * e], ws[2 * e], zv[2 * e]),
+                           fmaf(as[u] * v[u][2 * e + 1], ws[2 * e + 1], zv[2 * e + 1]));
+      stg8(p.y + static_cast<size_t>(m) * p.N + n, o);
     }
-    const float as = __ldg(p.a_s + m);
-    const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.w_s + n));
-    const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.w_s + n + 4));
-    const float ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-    const size_t off = static_cast<size_t>(m) * p.N + n;
-    float zv[8] = {};
-    if (p.z != nullptr) unpack8(ldg8(p.z + off), zv);
-    uint32_t o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o[e] = pack_bf16x2(fmaf(as * v[2 * e], ws[2 * e], zv[2 * e]),
-                         fmaf(as * v[2 * e + 1], ws[2 * e + 1], zv[2 * e + 1]));
-    stg8(p.y + off, o);
   }
   cluster_sync_all();  // no block leaves while another reads its shared memory or its barriers
 }
