@@ -182,7 +182,12 @@ PRODUCT = [(1, 16, 16), (1, 4096, 1024), (2, 48, 32), (7, 80, 144), (8, 512, 256
            (512, 528, 272), (513, 1024, 528), (1000, 784, 1040), (2049, 512, 784),
            # more tiles than one wave holds: two blocks per SM, several waves, small W and large
            (20, 208, 20496), (40, 256, 20496), (130, 192, 20480), (300, 80, 39936), (24, 8192, 8192),
-           (1100, 2048, 528), (1300, 4096, 1040), (40, 16, 16), (70, 48, 32), (1025, 16, 48)]
+           (1100, 2048, 528), (1300, 4096, 1040), (40, 16, 16), (70, 48, 32), (1025, 16, 48),
+           # every share of a token tile among the warps that widen it
+           (144, 192, 272), (190, 192, 19728), (380, 144, 19712), (100, 320, 39952),
+           # the whole GEMM: short K and many columns, odd sizes, a last wave cut along K
+           (1025, 80, 39952), (2500, 144, 20496), (6000, 528, 1040), (3001, 1024, 4112),
+           (8192, 4096, 1024)]
 
 
 def product_ref(a_q, a_s, W_q, w_s, z):
@@ -270,7 +275,7 @@ def test_product_is_the_same_every_time(B, M, K, N):
 
 
 @pytest.mark.parametrize("M,K,N", [(1, 512, 272), (30, 512, 272), (200, 512, 272), (300, 272, 784),
-                                   (2000, 512, 272)])
+                                   (2000, 512, 272), (3001, 1024, 4112)])
 def test_product_writes_its_output_alone(B, M, K, N):
     """Guard bytes around the output and the workspace stay as they were; the workspace's
     contents before the call do not matter."""
@@ -496,7 +501,7 @@ def test_memory_of_a_call_on_another_stream_is_not_handed_out(B, raw):
     """Outputs and workspace that a call allocates while its work waits on another stream: what
     is allocated next on the current stream, of the same sizes, must not get their memory."""
     side = torch.cuda.Stream()
-    p = product_inputs(1100, 64, 512, False, seed=6)
+    p = product_inputs(6000, 528, 1040, False, seed=6)
     t = bwd_inputs(64, 128, 512, 128, seed=7)
     args = [t[k] for k in ("dout", "W2", "y_q", "y_s", "W1", "h", "r", "gamma")]
     want = B.coda_matmul_q8(*p[:4])
@@ -507,7 +512,7 @@ def test_memory_of_a_call_on_another_stream_is_not_handed_out(B, raw):
     handle = side.cuda_stream if raw else side
     got = B.coda_matmul_q8(*p[:4], stream=handle)
     got_b = B.coda_bwd_swiglu_dgrad_q8(*args, want_a=True, stream=handle)
-    need = B.coda_matmul_q8_workspace_bytes(1100, 64, 512)
+    need = B.coda_matmul_q8_workspace_bytes(6000, 528, 1040)
     need_b = B.coda_bwd_swiglu_dgrad_workspace_bytes(64, 128, 512, 128)
     other = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF) for n in (need, need_b) * 3]
     side.synchronize()
@@ -533,6 +538,31 @@ def test_two_streams_at_once(B, M):
             B.coda_matmul_q8(*t[:4], z=t[4], y=ys[i], ws=ws[i], stream=streams[i])
     torch.cuda.synchronize()
     for a, b in zip(ys, want):
+        assert torch.equal(a, b)
+
+
+def test_two_blocks_per_sm_beside_other_tensor_work(B):
+    """The form with two blocks on an SM, on two streams, with library products on a third."""
+    p = [product_inputs(40, 512, 24576, True, seed=i) for i in (1, 2)]
+    want = [B.coda_matmul_q8(*t[:4], z=t[4]) for t in p]
+    ys = [torch.empty_like(w) for w in want]
+    m = bf(randn(9, 512, 512))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for i, t in enumerate(p):
+            B.coda_matmul_q8(*t[:4], z=t[4], y=ys[i], stream=streams[i])
+        with torch.cuda.stream(streams[2]):
+            torch.mm(m, m)
+    torch.cuda.synchronize()
+    for a, b in zip(ys, want):
+        assert torch.equal(a, b)
+    clean(B)
+
+
+def test_the_default_stream_by_its_handle(B):
+    x = bf(randn(3, 40, 264))
+    for a, b in zip(B.coda_quant_q8(x, stream=0), B.coda_quant_q8(x)):
         assert torch.equal(a, b)
 
 
