@@ -1038,15 +1038,17 @@ cudaError_t launch_product_small(const SmallQ8Params& p, const uint8_t* a_q, con
 }
 
 // The INT8 product's three kernels.
-//   few tokens (q8_small.cuh)    up to 16 tokens, and up to 32 while W is small: measured with 32
-//                                tokens, W of 17 MB 10.1 us against 12.2 for the mid-size kernel, 59 MB
-//                                20.9 against 19.6
+//   few tokens (q8_small.cuh)    up to 8 tokens; more while W is small, where it starts sooner.  Against
+//                                the mid-size kernel, 16 tokens: W of 17 MB 9.0 us and 10.4, 59 MB 16.5
+//                                and 16.9, 117 MB 29.2 and 27.1; 32 tokens: 17 MB 9.8 and 11.4, 59 MB
+//                                19.3 and 17.5
 //   mid-size (q8_mid.cuh)        up to kMidSure tokens, and beyond while its estimate is the lower one
 //   whole GEMM                   a and W widened to bf16 in the workspace first
 constexpr int64_t kMidSure = 1024;  // 1025 x 4096 x 14336: 89 us against 114
 
 bool product_small(int64_t M, int64_t K, int64_t N) {
-  return M <= 16 || (M <= kSmallMaxTokens && K * N < (int64_t(3) << 24));
+  return M <= 8 || (M <= 16 && K * N < (int64_t(5) << 24)) ||
+         (M <= kSmallMaxTokens && K * N < (int64_t(3) << 24));
 }
 
 // Time of the whole-GEMM form: widening at 6.2 bytes per ps (1 read, 2 written per code), waves
@@ -1058,11 +1060,13 @@ double product_gemm_ns(int64_t M, int64_t K, int64_t N, int pairs) {
 }
 
 // Tokens per CTA pair, pairs along K and blocks per SM of the mid-size product: those with the
-// least estimated time, waves of clusters times a cluster's.  Measured on GB300: a step of 64 rows
-// takes 1.33 ns per token (the tensor cores), below about 300 tokens 235 ns and 0.53 ns per token
-// (the way from a stage to a slot), two blocks on an SM 364 ns and 1.09 ns per token for both; a
-// pair's start and its sums' way out about 3 us and 10 ns per token, a split's
-// exchange 2 us and 10 ns per token more.
+// least estimated time, waves of clusters times a cluster's; more token tiles only where they gain
+// 5 %, as each reads W again.  Fitted to sweeps on GB300 (its picks are 1 % above the best on the
+// average of 40 shapes): a step of 64 rows takes 1.33 ns per token (the tensor cores), below about
+// 300 tokens 235 ns and 0.53 ns per token (the way from a stage to a slot) and no less than with 64,
+// two blocks on an SM 364 ns and 1.09 ns per token for both; a pair's start and its sums'
+// way out 3 us and 5 ns per token, a split's exchange 0.5 us and 10 ns more, of four pairs or
+// with two blocks on an SM 1 us and 25 ns.
 struct MidPlan {
   int tokens, split;
   bool narrow;
@@ -1083,11 +1087,13 @@ MidPlan plan_mid(int64_t M, int64_t K, int64_t N, const int (*clusters)[3]) {
       for (int narrow = 0; narrow < 2; ++narrow) {
         // a narrow block alone on its SM is a wide one with shorter rings
         if (narrow && (tokens > MidShape<true>::kTokens || tiles <= clusters[0][i])) break;
-        const double step = narrow ? 364.0 + 1.09 * t : std::max(1.33 * t, 235.0 + 0.53 * t);
-        const double pair = static_cast<double>(cdiv(nk, s)) * step + 3000.0 + 10.0 * t +
-                            (s > 1 ? 2000.0 + 10.0 * t : 0.0);
+        const double t64 = std::max(t, 64.0);
+        const double step = narrow ? 364.0 + 1.09 * t64 : std::max(1.33 * t, 235.0 + 0.53 * t64);
+        const double exchange =
+            s == 1 ? 0.0 : s == 4 || narrow ? 1000.0 + 25.0 * t : 500.0 + 10.0 * t;
+        const double pair = static_cast<double>(cdiv(nk, s)) * step + 3000.0 + 5.0 * t + exchange;
         const double ns = static_cast<double>(cdiv(tiles, clusters[narrow][i])) * pair;
-        if (ns < 0.98 * best.ns) best = {static_cast<int>(tokens), s, narrow != 0, ns};
+        if (ns < 0.95 * best.ns) best = {static_cast<int>(tokens), s, narrow != 0, ns};
       }
     }
   }
@@ -1779,7 +1785,8 @@ coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* 
   }
   char* wsb = static_cast<char*>(workspace);
   const MidPlan plan = plan_mid(M, K, N, clusters);
-  if (M <= kMidSure || plan.ns < product_gemm_ns(M, K, N, max_pairs)) {
+  // (short K, whose waves the plan takes for some 3 us shorter than they are: 10 % in hand)
+  if (M <= kMidSure || 1.1 * plan.ns < product_gemm_ns(M, K, N, max_pairs)) {
     MidQ8Params mp = {};
     mp.a_s = a_s;
     mp.w_s = w_s;
