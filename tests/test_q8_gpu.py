@@ -250,6 +250,37 @@ def test_product_of_extreme_codes(B, M):
     clean(B)
 
 
+def test_product_with_a_last_wave_cut_along_k(B):
+    """780 tiles on 76 CTA pairs, 64 blocks of K each: the whole GEMM with its split tail, eager and
+    from two graphs that share one workspace."""
+    M, K, N = 5000, 4096, 9984
+    p = product_inputs(M, K, N, True, seed=11)
+    rows = torch.arange(0, M, 23, device="cuda")
+
+    def check(y, t):
+        assert torch.isfinite(y).all()
+        check_product(y[rows], t[0][rows], t[1][rows], t[2], t[3], t[4][rows])
+
+    check(B.coda_matmul_q8(*p[:4], z=p[4]), p)
+    ws = B.workspace(B.coda_matmul_q8_workspace_bytes(M, K, N), "cuda")
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(B.coda_matmul_q8(*p[:4], z=p[4], ws=ws))
+        graphs.append(g)
+    for seed in (12, 13):
+        t = product_inputs(M, K, N, True, seed=seed)
+        for x, y in zip(p, t):
+            x.copy_(y)
+        for g in graphs + graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        check(outs[0], t)
+        check(outs[1], t)
+    clean(B)
+
+
 @pytest.mark.parametrize("M", [1, 20, 150, 600])
 def test_product_scales_zero_and_nan(B, M):
     a_q, a_s, W_q, w_s, z = product_inputs(M, 256, 272, True, seed=9)
