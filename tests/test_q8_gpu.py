@@ -185,7 +185,7 @@ PRODUCT = [(1, 16, 16), (1, 4096, 1024), (2, 48, 32), (7, 80, 144), (8, 512, 256
            (1100, 2048, 528), (1300, 4096, 1040), (40, 16, 16), (70, 48, 32), (1025, 16, 48),
            # every share of a token tile among the warps that widen it
            (12, 4096, 20496), (144, 192, 272), (190, 192, 19728), (380, 144, 19712), (100, 320, 39952),
-           # the whole GEMM: short K and many columns, odd sizes, a last wave cut along K
+           # the whole GEMM: short K and many columns, odd sizes
            (1025, 80, 39952), (2500, 144, 20496), (6000, 528, 1040), (3001, 1024, 4112),
            (8192, 4096, 1024)]
 
