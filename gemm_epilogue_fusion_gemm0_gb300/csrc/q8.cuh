@@ -63,23 +63,20 @@ __device__ __forceinline__ uint32_t pack_bf16x2_2(uint64_t v) {
   return pack_bf16x2(lo, hi);
 }
 
-// What a group of values with the given amax is multiplied by to give codes: 127 / amax.
+// What a group of values with the given amax is multiplied by to give codes: 127 / amax to fp32's
+// half ulp, from the approximate reciprocal and one correction by the exact remainder (an IEEE
+// quotient costs a block of 128 values as much as the rest).
 // Outside of 2^-100 .. 2^100 that quotient or its reciprocal leaves fp32's normal range, so the
 // values are brought near one first (`pre`, a power of two: exact), which hardly any group needs.
-// A row's quotient is rounded once; for a block of 128 values that costs as much as the rest, and
-// the approximate reciprocal (1 ulp) puts a code's argument off by 127 * 3 * 2^-24 at most.
 struct Q8Factors {
   float pre, inv;
-  __device__ __forceinline__ explicit Q8Factors(float amax, bool approximate = false) {
+  __device__ __forceinline__ explicit Q8Factors(float amax) {
     pre = amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.0f;
+    const float a = amax * pre;
     float r;
-    if (approximate) {
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax * pre));
-      r *= 127.0f;
-    } else {
-      r = __fdiv_rn(127.0f, amax * pre);
-    }
-    inv = amax > 0.f && amax <= 3.402823466e38f ? r : 0.f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    const float v = 127.0f * r;
+    inv = amax > 0.f && amax <= 3.402823466e38f ? fmaf(fmaf(-v, a, 127.0f), r, v) : 0.f;
   }
   template <int kV>
   __device__ __forceinline__ void prepare(float (&u)[kV][8]) const {
@@ -92,19 +89,37 @@ struct Q8Factors {
   }
 };
 
+// amax / 127: a product with the rounded 1 / 127, corrected once by its exact remainder
 __device__ __forceinline__ float q8_scale(float amax) {
-  return amax <= 3.402823466e38f ? amax * (1.0f / 127.0f) : __int_as_float(0x7fffffff);
+  const float s = amax * (1.0f / 127.0f);
+  return amax <= 3.402823466e38f ? fmaf(fmaf(-127.0f, s, amax), 1.0f / 127.0f, s)
+                                 : __int_as_float(0x7fffffff);
 }
 
 // Four codes of prepared values: v + 1.5 * 2^23 holds rint(v) (ties to even) in its low mantissa
-// bits as a two's complement number for |v| < 2^22, so the code is the sum's low byte and
-// one fused multiply-add rounds once.
+// bits as a two's complement number for |v| < 2^22, so the code is the sum's low byte.
+//
+// kBf16: u and amax are bf16 numbers, whose codes are often half way between two integers (one in
+// 400 of a bell-shaped tensor in blocks of 128).  The quotient's rounding would put such a code on
+// either side, so the product is first rounded to multiples of 2^-15 (+ 1.5 * 2^8), which half
+// way numbers are and which 127 * 2^-24, the quotient's error, does not leave.  All other
+// codes >= 1/2 are further from half way than half of that step: with 8-bit mantissas a, b and
+// v = a 2^-j, amax = b they are |254 a - (2 k + 1) 2^j b| / (2^(j+1) b) from it, j <= 8, the
+// numerator even for j >= 1 and not 0: 2^-8 / 255 at least.  So a bf16 tensor's codes are the definition's.
+// Other values (the norm's) go the shorter way, one rounding; theirs are off by 127 * 2^-24 and
+// rarely half way.
+template <bool kBf16>
 __device__ __forceinline__ uint32_t q8_pack4(const float* u, const Q8Factors& f) {
+  constexpr float kInt = 12582912.0f, kStep = 384.0f;  // 1.5 * 2^23, 1.5 * 2^8
   uint32_t b[4];
 #pragma unroll
   for (int i = 0; i < 4; i += 2) {
+    const uint64_t v = pack2(u[i], u[i + 1]), inv = pack2(f.inv, f.inv);
     float lo, hi;
-    unpack2(fma2(pack2(u[i], u[i + 1]), pack2(f.inv, f.inv), pack2(12582912.0f, 12582912.0f)), lo, hi);
+    if constexpr (kBf16)
+      unpack2(add2(fma2(v, inv, pack2(kStep, kStep)), pack2(kInt - kStep, kInt - kStep)), lo, hi);
+    else
+      unpack2(fma2(v, inv, pack2(kInt, kInt)), lo, hi);
     b[i] = __float_as_uint(lo);
     b[i + 1] = __float_as_uint(hi);
   }
@@ -210,8 +225,9 @@ __device__ __forceinline__ void row_q8_values(const Chunk8& x, const Chunk8& z, 
   for (int e = 0; e < 8; e += 2) amax = max3_abs_nan(amax, u[e], u[e + 1]);
 }
 
+template <bool kBf16>
 __device__ __forceinline__ void q8_store8(uint8_t* q, const float (&u)[8], const Q8Factors& f) {
-  *reinterpret_cast<uint2*>(q) = make_uint2(q8_pack4(u, f), q8_pack4(u + 4, f));
+  *reinterpret_cast<uint2*>(q) = make_uint2(q8_pack4<kBf16>(u, f), q8_pack4<kBf16>(u + 4, f));
 }
 
 // kH: h is stored (h_out is not null)
@@ -295,7 +311,7 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 1024) row_q8_kernel(const Row
     f.prepare(u);
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
-      if (v * nthr <= last) q8_store8(q + 8 * (v * nthr), u[v], f);
+      if (v * nthr <= last) q8_store8<!kNorm>(q + 8 * (v * nthr), u[v], f);
   } else {
     float s2 = 0.f, m2 = 0.f;
     for (int i = 0; i <= last; i += nthr) {
@@ -303,7 +319,7 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 1024) row_q8_kernel(const Row
       row_q8_values<kNorm, kRes, false, kPacked>(ldg8(x + o), kRes ? ldg8(z + o) : kZero,
                                         kNorm ? ldg8(gm + o) : kZero, nullptr, true, u[0], s2, m2);
       f.prepare(u);
-      q8_store8(q + o, u[0], f);
+      q8_store8<!kNorm>(q + o, u[0], f);
     }
   }
 }
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(1024) row_q8_ring_kernel(const RowQ8Params p, 
 #pragma unroll
     for (int v = 0; v < kVec; ++v) {
       const int i = v * nthr + tid;
-      if (i < nvec) q8_store8(p.q_out + base + 8 * static_cast<size_t>(i), u[v], f);
+      if (i < nvec) q8_store8<!kNorm>(p.q_out + base + 8 * static_cast<size_t>(i), u[v], f);
     }
     if (++s == static_cast<uint32_t>(stages)) {
       s = 0;
@@ -495,15 +511,15 @@ __global__ void __launch_bounds__(256) block_q8_kernel(const __nv_bfloat16* __re
 #pragma unroll
     for (int o = kQ8QuantLanes / 2; o > 0; o >>= 1)
       amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const Q8Factors f(amax, true);
+    const Q8Factors f(amax);
     if (pl.row(i) < M) {
       uint8_t* dst = q + pl.row(i) * n + pl.col;
       float u[2][8];
       unpack8(c[i][0], u[0]);
       unpack8(c[i][1], u[1]);
       f.prepare(u);
-      if (pl.in) q8_store8(dst, u[0], f);
-      if (in2) q8_store8(dst + 8, u[1], f);
+      if (pl.in) q8_store8<true>(dst, u[0], f);
+      if (in2) q8_store8<true>(dst + 8, u[1], f);
       if (threadIdx.x % kQ8QuantLanes == 0 && pl.in) s[pl.row(i) * pl.nb + pl.blk] = q8_scale(amax);
     }
   }

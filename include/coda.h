@@ -293,9 +293,11 @@ CODA_API coda_status_t coda_bwd(const coda_bf16* dy, const coda_bf16* x, const c
  *
  * A value v is held as code * scale.  Over the values that share a scale,
  *   scale = amax / 127,   code = rint(v * 127 / amax),   amax = max |v|,
- * code in [-127, 127]; amax = 0 gives code 0 and scale 0.  A value is then off by
- * at most amax / 254 (and a few parts in 10^7: v * 127 / amax is formed in fp32, so
- * that a value so near to half way between two codes may get either).  Values that share a scale with an infinity
+ * code in [-127, 127]; amax = 0 gives code 0 and scale 0.  coda_quant_q8's codes are
+ * these, ties to even, and its scales amax / 127 rounded once.  The norm forms
+ * v * 127 / amax in fp32, so that a value so near to half way between two codes may
+ * get either.  A value is then off by at most amax / 254 (the norm's by a few parts in
+ * 10^7 more).  Values that share a scale with an infinity
  * or a NaN get the scale NaN (the codes are then unspecified), so that it is not
  * lost in whatever the codes are used for.  A scale belongs to a row (block = 0,
  * scales [M]: one per token) or to 128 columns of a row (block = 128, scales
