@@ -3,7 +3,13 @@
 Argument marshalling only: torch tensors are checked for device, dtype and
 contiguity and passed as raw device pointers together with the current CUDA
 stream.  Every step of the computation runs in the library's kernels; if the
-library is missing this module raises at import time.  A process started with
+library is missing this module raises at import time.
+
+With stream= (a torch stream or a raw cudaStream_t handle) a call is enqueued there
+and its outputs and workspace, where they are not given, are that stream's memory.
+As with any work on another stream, the caller orders it behind whatever wrote the
+inputs, keeps them until it is done, and waits for it before reading the outputs.
+  A process started with
 CODA_CHECKED_BUILD=1 loads the checked build (libcoda_checked.so) instead.
 """
 
@@ -153,13 +159,33 @@ class _Call:
     current device, so a tensor on another one would hand the kernels a
     pointer they cannot use)."""
 
-    __slots__ = ("where", "device", "index", "own")
+    __slots__ = ("where", "device", "index", "stream", "user")
 
     def __init__(self, where: str, device: torch.device, stream=None):
         self.where, self.device = where, device
-        # tensors allocated for a call on a stream of its own
-        self.own = None if stream is None else []
         self.index = device.index if device.type == "cuda" else None
+        # the stream asked for, if any, and (once something is allocated) what to allocate it on
+        self.stream, self.user = stream, None
+
+    def empty(self, shape, dtype) -> torch.Tensor:
+        """Memory for this call.  For a call on another stream than the current one it comes from
+        that stream's memory: a block just freed on the current stream may still be in use there,
+        and nothing orders the other stream behind that.  What is done with it on the
+        current stream, before it is freed, is waited for before it is handed out again."""
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        handle = _stream_ptr(self.stream, self.device)
+        if handle == _raw_stream(self.index):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if self.user is None:
+            # 1 is CUDA's handle of the legacy default stream, which torch knows as 0
+            self.user = (self.stream if hasattr(self.stream, "cuda_stream")
+                         else torch.cuda.ExternalStream(0 if handle == 1 else handle,
+                                                        device=self.device))
+        with torch.cuda.stream(self.user):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
 
     def t(self, t, dtype, shape, name) -> int:
         # the common case in few steps; anything else is told apart (and raised) below
@@ -178,19 +204,16 @@ class _Call:
     def out(self, t, dtype, shape, name) -> tuple:
         """An output and its address: `t` checked, or allocated (and then in need of no check)."""
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-            if self.own is not None:
-                self.own.append(t)
+            t = self.empty(shape, dtype)
             return t, t.data_ptr()
         return t, self.t(t, dtype, shape, name)
 
     def scratch(self, ws, need: int) -> tuple:
-        """Address and size of the workspace: `ws` checked, or `need` bytes allocated."""
+        """The workspace, its address and its size: `ws` checked, or `need` bytes allocated (to be
+        kept until the call is enqueued: freed memory is reused in stream order)."""
         if ws is None:
-            # kept until the call is enqueued: freed memory is reused in stream order
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            if self.own is not None:
-                self.own.append(ws)
+            need = max(need, 16)
+            ws = self.empty(need, torch.uint8)
             return ws, ws.data_ptr(), need
         return (ws, *self.ws(ws))
 
@@ -203,13 +226,6 @@ class _Call:
         return ws.data_ptr(), ws.numel() * ws.element_size()
 
     def run(self, fn, *args, stream=None) -> None:
-        if self.own:
-            # allocated for the current stream, used on another one: not to be handed out again
-            # before that one is done with them
-            user = (stream if hasattr(stream, "cuda_stream")
-                    else torch.cuda.ExternalStream(int(stream), device=self.device))
-            for t in self.own:
-                t.record_stream(user)
         if self.index == torch.cuda.current_device():
             st = fn(*args, _raw_stream(self.index) if stream is None
                     else _stream_ptr(stream, self.device))
@@ -242,21 +258,15 @@ def workspace(nbytes: int, device) -> torch.Tensor:
 def _fwd_common(fn, wsfn, x, W0, z, gamma, W1, eps, h, r, y, ws, stream):
     M, d = x.shape
     N1 = W1.shape[1]
-    dev = x.device
-    if h is None:
-        h = torch.empty((M, d), dtype=torch.bfloat16, device=dev)
-    if r is None:
-        r = torch.empty((M,), dtype=torch.float32, device=dev)
-    if y is None:
-        y = torch.empty((M, N1), dtype=torch.bfloat16, device=dev)
-    if ws is None:
-        ws = workspace(wsfn(M, d, N1), dev)
     bf = torch.bfloat16
-    c = _Call(fn.__name__, dev)
-    c.run(fn, c.t(x, bf, (M, d), "x"), c.t(W0, bf, (d, d), "W0"), c.t(z, bf, (M, d), "z"),
-          c.t(gamma, bf, (d,), "gamma"), c.t(W1, bf, (d, N1), "W1"), float(eps), M, d, N1,
-          c.t(h, bf, (M, d), "h"), c.t(r, torch.float32, (M,), "r"), c.t(y, bf, (M, N1), "y"),
-          *c.ws(ws), stream=stream)
+    c = _Call(fn.__name__, x.device, stream)
+    ins = (c.t(x, bf, (M, d), "x"), c.t(W0, bf, (d, d), "W0"), c.t(z, bf, (M, d), "z"),
+           c.t(gamma, bf, (d,), "gamma"), c.t(W1, bf, (d, N1), "W1"))
+    h, hp = c.out(h, bf, (M, d), "h")
+    r, rp = c.out(r, torch.float32, (M,), "r")
+    y, yp = c.out(y, bf, (M, N1), "y")
+    ws, wk, wkb = c.scratch(ws, wsfn(M, d, N1))
+    c.run(fn, *ins, float(eps), M, d, N1, hp, rp, yp, wk, wkb, stream=stream)
     return h, r, y
 
 
@@ -278,21 +288,18 @@ def coda_fwd_swiglu(x, W0, z, gamma, W1, eps, h=None, r=None, a=None, y=None, wa
     Returns (h, r, a) or (h, r, a, y) with want_y=True (pre-activation)."""
     M, d = x.shape
     N1 = W1.shape[1]
-    dev = x.device
     bf = torch.bfloat16
-    h = torch.empty((M, d), dtype=bf, device=dev) if h is None else h
-    r = torch.empty((M,), dtype=torch.float32, device=dev) if r is None else r
-    a = torch.empty((M, N1 // 2), dtype=bf, device=dev) if a is None else a
-    if want_y and y is None:
-        y = torch.empty((M, N1), dtype=bf, device=dev)
-    if ws is None:
-        ws = workspace(coda_fwd_workspace_bytes(M, d, N1), dev)
-    c = _Call("coda_fwd_swiglu", dev)
-    c.run(_lib.coda_fwd_swiglu,
-          c.t(x, bf, (M, d), "x"), c.t(W0, bf, (d, d), "W0"), c.t(z, bf, (M, d), "z"),
-          c.t(gamma, bf, (d,), "gamma"), c.t(W1, bf, (d, N1), "W1"), float(eps), M, d, N1,
-          c.t(h, bf, (M, d), "h"), c.t(r, torch.float32, (M,), "r"), c.opt(y, bf, (M, N1), "y"),
-          c.t(a, bf, (M, N1 // 2), "a"), *c.ws(ws), stream=stream)
+    c = _Call("coda_fwd_swiglu", x.device, stream)
+    ins = (c.t(x, bf, (M, d), "x"), c.t(W0, bf, (d, d), "W0"), c.t(z, bf, (M, d), "z"),
+           c.t(gamma, bf, (d,), "gamma"), c.t(W1, bf, (d, N1), "W1"))
+    h, hp = c.out(h, bf, (M, d), "h")
+    r, rp = c.out(r, torch.float32, (M,), "r")
+    a, ap = c.out(a, bf, (M, N1 // 2), "a")
+    yp = None
+    if want_y or y is not None:
+        y, yp = c.out(y, bf, (M, N1), "y")
+    ws, wk, wkb = c.scratch(ws, coda_fwd_workspace_bytes(M, d, N1))
+    c.run(_lib.coda_fwd_swiglu, *ins, float(eps), M, d, N1, hp, rp, yp, ap, wk, wkb, stream=stream)
     return (h, r, a, y) if y is not None else (h, r, a)
 
 
@@ -306,25 +313,22 @@ def coda_fwd_fp8(x_q, sx, W0_q, sW0, z, gamma, W1_q, sW1, s_hg, eps, h=None, r=N
     per-tensor scales; returns (h, r, y)."""
     M, d = x_q.shape
     N1 = W1_q.shape[1]
-    dev = x_q.device
     bf = torch.bfloat16
-    h = torch.empty((M, d), dtype=bf, device=dev) if h is None else h
-    r = torch.empty((M,), dtype=torch.float32, device=dev) if r is None else r
-    y = torch.empty((M, N1), dtype=bf, device=dev) if y is None else y
-    if ws is None:
-        ws = workspace(coda_fwd_fp8_workspace_bytes(M, d, N1), dev)
-    c = _Call("coda_fwd_fp8", dev)
+    c = _Call("coda_fwd_fp8", x_q.device, stream)
 
     def code(t, shape, name):
         if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
             raise TypeError(f"{name} must hold E4M3 codes (float8_e4m3fn or uint8)")
         return c.t(t, t.dtype, shape, name)
 
-    c.run(_lib.coda_fwd_fp8,
-          code(x_q, (M, d), "x_q"), float(sx), code(W0_q, (d, d), "W0_q"), float(sW0),
-          c.t(z, bf, (M, d), "z"), c.t(gamma, bf, (d,), "gamma"), code(W1_q, (d, N1), "W1_q"),
-          float(sW1), float(s_hg), float(eps), M, d, N1, c.t(h, bf, (M, d), "h"),
-          c.t(r, torch.float32, (M,), "r"), c.t(y, bf, (M, N1), "y"), *c.ws(ws), stream=stream)
+    ins = (code(x_q, (M, d), "x_q"), float(sx), code(W0_q, (d, d), "W0_q"), float(sW0),
+           c.t(z, bf, (M, d), "z"), c.t(gamma, bf, (d,), "gamma"), code(W1_q, (d, N1), "W1_q"),
+           float(sW1), float(s_hg), float(eps))
+    h, hp = c.out(h, bf, (M, d), "h")
+    r, rp = c.out(r, torch.float32, (M,), "r")
+    y, yp = c.out(y, bf, (M, N1), "y")
+    ws, wk, wkb = c.scratch(ws, coda_fwd_fp8_workspace_bytes(M, d, N1))
+    c.run(_lib.coda_fwd_fp8, *ins, M, d, N1, hp, rp, yp, wk, wkb, stream=stream)
     return h, r, y
 
 
@@ -332,16 +336,13 @@ def coda_bwd_dgrad(dy, W1, h, r, gamma, dh=None, ws=None, stream=None):
     """Fused RMSNorm-branch data gradient; returns dh."""
     M, N1 = dy.shape
     d = W1.shape[0]
-    if dh is None:
-        dh = torch.empty((M, d), dtype=torch.bfloat16, device=dy.device)
-    if ws is None:
-        ws = workspace(coda_bwd_dgrad_workspace_bytes(M, d, N1), dy.device)
     bf = torch.bfloat16
-    c = _Call("coda_bwd_dgrad", dy.device)
-    c.run(_lib.coda_bwd_dgrad,
-          c.t(dy, bf, (M, N1), "dy"), c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"),
-          c.t(r, torch.float32, (M,), "r"), c.t(gamma, bf, (d,), "gamma"), M, d, N1,
-          c.t(dh, bf, (M, d), "dh"), *c.ws(ws), stream=stream)
+    c = _Call("coda_bwd_dgrad", dy.device, stream)
+    ins = (c.t(dy, bf, (M, N1), "dy"), c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"),
+           c.t(r, torch.float32, (M,), "r"), c.t(gamma, bf, (d,), "gamma"))
+    dh, dhp = c.out(dh, bf, (M, d), "dh")
+    ws, wk, wkb = c.scratch(ws, coda_bwd_dgrad_workspace_bytes(M, d, N1))
+    c.run(_lib.coda_bwd_dgrad, *ins, M, d, N1, dhp, wk, wkb, stream=stream)
     return dh
 
 
@@ -357,20 +358,16 @@ def coda_bwd_swiglu_dgrad(dout, W2, y, W1, h, r, gamma, dy=None, s=None, dh=None
     half = W2.shape[0]
     N1 = 2 * half
     d = W1.shape[0]
-    dev = dout.device
     bf = torch.bfloat16
-    dy = torch.empty((M, N1), dtype=bf, device=dev) if dy is None else dy
-    s = torch.empty((M,), dtype=torch.float32, device=dev) if s is None else s
-    dh = torch.empty((M, d), dtype=bf, device=dev) if dh is None else dh
-    if ws is None:
-        ws = workspace(coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout), dev)
-    c = _Call("coda_bwd_swiglu_dgrad", dev)
-    c.run(_lib.coda_bwd_swiglu_dgrad,
-          c.t(dout, bf, (M, Dout), "dout"), c.t(W2, bf, (half, Dout), "W2"),
-          c.t(y, bf, (M, N1), "y"), c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"),
-          c.t(r, torch.float32, (M,), "r"), c.t(gamma, bf, (d,), "gamma"), M, d, N1, Dout,
-          c.t(dy, bf, (M, N1), "dy"), c.t(s, torch.float32, (M,), "s"), c.t(dh, bf, (M, d), "dh"),
-          *c.ws(ws), stream=stream)
+    c = _Call("coda_bwd_swiglu_dgrad", dout.device, stream)
+    ins = (c.t(dout, bf, (M, Dout), "dout"), c.t(W2, bf, (half, Dout), "W2"),
+           c.t(y, bf, (M, N1), "y"), c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"),
+           c.t(r, torch.float32, (M,), "r"), c.t(gamma, bf, (d,), "gamma"))
+    dy, dyp = c.out(dy, bf, (M, N1), "dy")
+    s, sp = c.out(s, torch.float32, (M,), "s")
+    dh, dhp = c.out(dh, bf, (M, d), "dh")
+    ws, wk, wkb = c.scratch(ws, coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout))
+    c.run(_lib.coda_bwd_swiglu_dgrad, *ins, M, d, N1, Dout, dyp, sp, dhp, wk, wkb, stream=stream)
     return dy, s, dh
 
 
@@ -470,8 +467,7 @@ def coda_bwd_swiglu_dgrad_q8(dout, W2, y_q, y_s, W1, h, r, gamma, dy=None, s=Non
     ap = None
     if want_a or a is not None:
         a, ap = c.out(a, bf, (M, half), "a")
-    need = max(_lib.coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout), 16)
-    ws, wk, wkb = c.scratch(ws, need)
+    ws, wk, wkb = c.scratch(ws, _lib.coda_bwd_swiglu_dgrad_workspace_bytes(M, d, N1, Dout))
     c.run(_lib.coda_bwd_swiglu_dgrad_q8, *ins, M, d, N1, Dout, dyp, sp, dhp, ap, wk, wkb,
           stream=stream)
     return (dy, s, dh, a) if a is not None else (dy, s, dh)
@@ -485,24 +481,22 @@ def coda_bwd(dy, x, W0, W1, h, r, gamma, dh_res=None, out=None, ws=None, stream=
     """All gradients of the chain; returns dict dh (= dz), dx, dgamma, dW0, dW1."""
     M, N1 = dy.shape
     d = W1.shape[0]
-    dev = dy.device
     bf, f32 = torch.bfloat16, torch.float32
     o = dict(out or {})
-    o.setdefault("dh", torch.empty((M, d), dtype=bf, device=dev))
-    o.setdefault("dx", torch.empty((M, d), dtype=bf, device=dev))
-    o.setdefault("dgamma", torch.empty((d,), dtype=f32, device=dev))
-    o.setdefault("dW0", torch.empty((d, d), dtype=f32, device=dev))
-    o.setdefault("dW1", torch.empty((d, N1), dtype=f32, device=dev))
-    if ws is None:
-        ws = workspace(coda_bwd_workspace_bytes(M, d, N1), dev)
-    c = _Call("coda_bwd", dev)
-    c.run(_lib.coda_bwd,
-          c.t(dy, bf, (M, N1), "dy"), c.t(x, bf, (M, d), "x"), c.t(W0, bf, (d, d), "W0"),
-          c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"), c.t(r, f32, (M,), "r"),
-          c.t(gamma, bf, (d,), "gamma"), c.opt(dh_res, bf, (M, d), "dh_res"),
-          M, d, N1, c.t(o["dh"], bf, (M, d), "dh"), c.t(o["dx"], bf, (M, d), "dx"),
-          c.t(o["dgamma"], f32, (d,), "dgamma"), c.t(o["dW0"], f32, (d, d), "dW0"),
-          c.t(o["dW1"], f32, (d, N1), "dW1"), *c.ws(ws), stream=stream)
+    c = _Call("coda_bwd", dy.device, stream)
+    ins = (c.t(dy, bf, (M, N1), "dy"), c.t(x, bf, (M, d), "x"), c.t(W0, bf, (d, d), "W0"),
+           c.t(W1, bf, (d, N1), "W1"), c.t(h, bf, (M, d), "h"), c.t(r, f32, (M,), "r"),
+           c.t(gamma, bf, (d,), "gamma"), c.opt(dh_res, bf, (M, d), "dh_res"))
+    outs = []
+    for name, dtype, shape in (("dh", bf, (M, d)), ("dx", bf, (M, d)), ("dgamma", f32, (d,)),
+                               ("dW0", f32, (d, d)), ("dW1", f32, (d, N1))):
+        if name in o:
+            outs.append(c.t(o[name], dtype, shape, name))
+        else:
+            o[name], p = c.out(None, dtype, shape, name)
+            outs.append(p)
+    ws, wk, wkb = c.scratch(ws, coda_bwd_workspace_bytes(M, d, N1))
+    c.run(_lib.coda_bwd, *ins, M, d, N1, *outs, wk, wkb, stream=stream)
     return o
 
 
