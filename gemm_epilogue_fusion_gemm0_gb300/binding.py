@@ -3,14 +3,13 @@
 Argument marshalling only: torch tensors are checked for device, dtype and
 contiguity and passed as raw device pointers together with the current CUDA
 stream.  Every step of the computation runs in the library's kernels; if the
-library is missing this module raises at import time.
+library is missing this module raises at import time.  A process started with
+CODA_CHECKED_BUILD=1 loads the checked build (libcoda_checked.so) instead.
 
 With stream= (a torch stream or a raw cudaStream_t handle) a call is enqueued there
 and its outputs and workspace, where they are not given, are that stream's memory.
 As with any work on another stream, the caller orders it behind whatever wrote the
 inputs, keeps them until it is done, and waits for it before reading the outputs.
-  A process started with
-CODA_CHECKED_BUILD=1 loads the checked build (libcoda_checked.so) instead.
 """
 
 from __future__ import annotations
