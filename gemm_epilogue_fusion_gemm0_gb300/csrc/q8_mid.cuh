@@ -252,10 +252,14 @@ __global__ void __launch_bounds__(mid_threads(kNarrow), kNarrow ? 2 : 1)
   const int nk = (p.K + kMidK - 1) / kMidK;
   const int kb0 = static_cast<int>(static_cast<long long>(nk) * rank / p.split);
   int nkb = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / p.split) - kb0;
+  bool paired = true;
   if constexpr (kNarrow) {
-    // One address serves both CTAs of the pair.  With two blocks on an SM their allocations could
-    // differ; then the failure is recorded and nothing is multiplied.
-    if (ld_cluster_u32(mapa_shared(smem_u32(tmem_holder), cr ^ 1u)) != tmem_base) {
+    // One address serves both CTAs of the pair.  The two allocate together and get the same columns:
+    // 0.9 million pairs did, among other pairs and beside blocks of one CTA that held columns of one of
+    // the two SMs alone (columns 0..255 there: both got 256).  PTX does not state it, so it is
+    // looked at: otherwise the failure is recorded, nothing is multiplied and the sums are NaN.
+    paired = ld_cluster_u32(mapa_shared(smem_u32(tmem_holder), cr ^ 1u)) == tmem_base;
+    if (!paired) {
       record_failure(wc, kSitePairTmem);
       nkb = 0;
     }
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(mid_threads(kNarrow), kNarrow ? 2 : 1)
   // The sums leave tensor memory as [token][channel] in the ring's place.
   if (warp >= 2 && warp < 10) {
     const bool ok = bounded_wait(bar_done, 0, wc, kSiteDrain);
-    if (__all_sync(0xffffffffu, ok)) {
+    if (__all_sync(0xffffffffu, ok) && paired) {
       tc_fence_after();
       const uint32_t quad = warp & 3;
       const uint32_t ch = 32 * quad + 4 * (lane & 7) + (lane >> 3);  // the channel in this lane
@@ -451,6 +455,9 @@ __global__ void __launch_bounds__(mid_threads(kNarrow), kNarrow ? 2 : 1)
           if (c + j < p.tokens) st_shared_u32(base + 4u * ((c + j) * kMidChannels + ch), v[j]);
       }
       tc_fence_before();
+    } else if (!paired) {
+      for (int i = static_cast<int>(threadIdx.x) - 64; i < p.tokens * kMidChannels; i += 256)
+        st_shared_u32(base + 4u * static_cast<uint32_t>(i), 0x7fffffffu);  // NaN
     }
   } else if (warp == 1) {
     // both CTAs: no TMEM release while products may still write it

@@ -346,7 +346,9 @@ CODA_API coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* 
  * K and N positive multiples of 16; codes may be anything in [-128, 127].  Sums are fp32 sums of
  * exact products: exact while they stay below 2^24.  A NaN scale makes its row or column NaN.
  * workspace: at least coda_matmul_q8_workspace_bytes(M, K, N); NULL will do where that is 0
- * (up to 1024 tokens). */
+ * (up to 1024 tokens).
+ * A tile whose pair of blocks was given different tensor memory (detail 0x10b of
+ * coda_get_device_status; not known to happen) is NaN. */
 CODA_API size_t coda_matmul_q8_workspace_bytes(int64_t M, int64_t K, int64_t N);
 CODA_API coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* W_q,
                                       const float* w_s, const coda_bf16* z, int64_t M, int64_t K,
@@ -372,7 +374,7 @@ CODA_API coda_status_t coda_bwd_swiglu_dgrad_q8(const coda_bf16* dout, const cod
 /* Synchronises `stream`, then reports and clears the library's device-side
  * status word: CODA_OK, CODA_ERR_DEVICE_TIMEOUT if a bounded wait in any
  * kernel of this library ran out since the last call (raw code 0x100 | which
- * wait), or, in the checked build (libcoda_checked.so, compiled with
+ * wait; 0x10b: see coda_matmul_q8), or, in the checked build (libcoda_checked.so, compiled with
  * -DCODA_CHECKED: every staged epilogue load and store, gamma load, TMA box
  * start and workspace index checked on the device), CODA_ERR_DEVICE_BOUNDS if a check failed and
  * its access was skipped (raw code 0x200 | which check).  The first failure
