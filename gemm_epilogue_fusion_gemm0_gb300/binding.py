@@ -98,6 +98,7 @@ EXPORTS = {
     "coda_add_rmsnorm_q8": (_st, [_vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp]),
     "coda_matmul_q8_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "coda_matmul_q8": (_st, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "coda_matmul_q8_plan": (_int, [_i64, _i64, _i64, _int, _int, _vp, _vp]),
     "coda_bwd_swiglu_dgrad_q8": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
                                        _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
@@ -425,6 +426,16 @@ def coda_add_rmsnorm_q8(x, gamma, eps, z=None, h=None, q=None, s=None, stream=No
 
 def coda_matmul_q8_workspace_bytes(M: int, K: int, N: int) -> int:
     return int(_lib.coda_matmul_q8_workspace_bytes(M, K, N))
+
+
+def coda_matmul_q8_plan(M: int, K: int, N: int, sms: int, pairs: int, clusters) -> tuple:
+    """The form that coda_matmul_q8 would take on such a device as (form, parts along K, tokens
+    per CTA pair, two blocks per SM); form 0 refused, 1 few tokens, 2 mid-size, 3 whole GEMM."""
+    fit, out = (ctypes.c_int32 * 3)(*clusters), (ctypes.c_int32 * 3)()
+    form = int(_lib.coda_matmul_q8_plan(M, K, N, int(sms), int(pairs), fit, out))
+    if form < 0:
+        raise ValueError("coda_matmul_q8_plan: invalid arguments")
+    return (form, int(out[0]), int(out[1]), bool(out[2]))
 
 
 def coda_matmul_q8(a_q, a_s, W_q, w_s, z=None, y=None, ws=None, stream=None):

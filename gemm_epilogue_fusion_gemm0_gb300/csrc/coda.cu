@@ -405,7 +405,11 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int n = 0;
-        ok = cudaOccupancyMaxActiveClusters(&n, kProductMid, &cfg) == cudaSuccess && n > 0;
+        // none, for a size that does not fit (part of a device): that split is not planned
+        if (cudaOccupancyMaxActiveClusters(&n, kProductMid, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          n = 0;
+        }
         s.mid_clusters[0][i] = n;
         // Two narrow blocks share an SM (112 pairs of 32 tokens ran in one wave, 30 us, where one
         // block per SM takes two, 39 us); the occupancy query, which knows no tensor memory,
@@ -1013,17 +1017,19 @@ coda_status_t check_product(int64_t M, int64_t K, int64_t N) {
 // Blocks along K (a cluster) of the few-token product: as many as one wave of `slots`
 // blocks holds.  A wave more costs more than the idle slots (N = 28672, K = 4096, one token:
 // 224 blocks 25 us, 448 in two waves 28 us, 896 33 us; N = 4096: 32 blocks 12 us, 256 7 us).
-int small_split(int64_t K, int64_t N, int slots) {
+// `most`: blocks of the largest cluster that fits.
+int small_split(int64_t K, int64_t N, int slots, int most) {
   const int64_t tiles = cdiv(N, kSmallChannels), steps = cdiv(K, kSmallStep);
   int s = 1;
-  while (s < 8 && tiles * s * 2 <= slots && steps >= 2 * s * kSmallWarps) s *= 2;
+  while (s < most && tiles * s * 2 <= slots && steps >= 2 * s * kSmallWarps) s *= 2;
   return s;
 }
 
+int small_groups(int64_t M) { return M <= 8 ? 1 : M <= 16 ? 2 : 4; }
+
 cudaError_t launch_product_small(const SmallQ8Params& p, const uint8_t* a_q, const uint8_t* W_q,
-                                 int sms, cudaStream_t stream) {
-  const int groups = p.M <= 8 ? 1 : p.M <= 16 ? 2 : 4;
-  const int split = small_split(p.K, p.N, groups <= 2 ? 2 * sms : sms);
+                                 int split, cudaStream_t stream) {
+  const int groups = small_groups(p.M);
   CUtensorMap mW, mA;
   if (!tmap_2d_u8(&mW, W_q, p.N, p.K, kSmallChannels, kSmallStep) ||
       !tmap_2d_u8(&mA, a_q, p.K, p.M, kSmallStep, 8 * groups, CU_TENSOR_MAP_SWIZZLE_NONE))
@@ -1060,7 +1066,7 @@ double product_gemm_ns(int64_t M, int64_t K, int64_t N, int pairs) {
 }
 
 // Tokens per CTA pair, pairs along K and blocks per SM of the mid-size product: those with the
-// least estimated time, waves of clusters times a cluster's; more token tiles only where they gain
+// least estimated time, waves of clusters times a cluster's (no tokens where not even a pair fits); more token tiles only where they gain
 // 5 %, as each reads W again.  Fitted to sweeps on GB300 (its picks are 1 % above the best on the
 // average of 40 shapes): a step of 64 rows takes 1.33 ns per token (the tensor cores), below about
 // 300 tokens 235 ns and 0.53 ns per token (the way from a stage to a slot) and no less than with 64,
@@ -1082,7 +1088,7 @@ MidPlan plan_mid(int64_t M, int64_t K, int64_t N, const int (*clusters)[3]) {
     if (tokens > 256) tokens = cdiv(tokens, 32) * 32;
     const double t = static_cast<double>(tokens);
     for (int i = 0, s = 1; s <= kMidMaxSplit; ++i, s *= 2) {
-      if (s > 1 && nk < 4 * s) break;
+      if ((s > 1 && nk < 4 * s) || clusters[0][i] == 0) break;
       const int64_t tiles = ct * cdiv(M, tokens);
       for (int narrow = 0; narrow < 2; ++narrow) {
         // a narrow block alone on its SM is a wide one with shorter rings
@@ -1098,6 +1104,36 @@ MidPlan plan_mid(int64_t M, int64_t K, int64_t N, const int (*clusters)[3]) {
     }
   }
   return best;
+}
+
+enum ProductForm { kFormNone, kFormSmall, kFormMid, kFormGemm };
+
+struct ProductPlan {
+  ProductForm form;
+  int split;    // blocks (few tokens) or pairs (mid-size) along K
+  MidPlan mid;  // mid-size
+};
+
+// The form of a product on a device of `sms` SMs, `pairs` co-resident CTA pairs of the GEMM and so
+// many clusters of the mid-size form; none where that form is needed and does not fit.
+ProductPlan plan_product(int64_t M, int64_t K, int64_t N, int sms, int pairs,
+                         const int (*clusters)[3]) {
+  ProductPlan p = {kFormNone, 1, {}};
+  if (product_small(M, K, N)) {
+    const int most = clusters[0][2] > 0 ? 8 : clusters[0][1] > 0 ? 4 : clusters[0][0] > 0 ? 2 : 1;
+    p.form = kFormSmall;
+    p.split = small_split(K, N, small_groups(M) <= 2 ? 2 * sms : sms, most);
+    return p;
+  }
+  p.mid = plan_mid(M, K, N, clusters);
+  p.split = p.mid.split;
+  // (short K, whose waves the plan takes for some 3 us shorter than they are: 10 % in hand)
+  if (p.mid.tokens > 0 &&
+      (M <= kMidSure || 1.1 * p.mid.ns < product_gemm_ns(M, K, N, std::max(pairs, 1))))
+    p.form = kFormMid;
+  else if (M > kMidSure)
+    p.form = kFormGemm;
+  return p;
 }
 
 cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t* W_q,
@@ -1743,6 +1779,24 @@ size_t coda_matmul_q8_workspace_bytes(int64_t M, int64_t K, int64_t N) {
          align256(static_cast<size_t>(K) * N * 2) + sk_region_bytes(cdiv(M, kPairBM) * cdiv(N, kBN));
 }
 
+int coda_matmul_q8_plan(int64_t M, int64_t K, int64_t N, int sms, int pairs, const int32_t* clusters,
+                        int32_t* plan) {
+  if (plan == nullptr || clusters == nullptr || check_product(M, K, N) != CODA_OK || M == 0 ||
+      sms < 1 || pairs < 0)
+    return -1;
+  int fit[2][3];
+  for (int i = 0; i < 3; ++i) {
+    if (clusters[i] < 0) return -1;
+    fit[0][i] = clusters[i];
+    fit[1][i] = 2 * clusters[i];
+  }
+  const ProductPlan p = plan_product(M, K, N, sms, pairs, fit);
+  plan[0] = p.split;
+  plan[1] = p.form == kFormMid ? p.mid.tokens : 0;
+  plan[2] = p.form == kFormMid && p.mid.narrow;
+  return static_cast<int>(p.form);
+}
+
 coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* W_q,
                              const float* w_s, const coda_bf16* z, int64_t M, int64_t K, int64_t N,
                              coda_bf16* y_out, void* workspace, size_t workspace_bytes,
@@ -1766,7 +1820,10 @@ coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* 
   const uint64_t tmo = g_timeout_ns.load();
   const int Mi = static_cast<int>(M), Ki = static_cast<int>(K), Ni = static_cast<int>(N);
 
-  if (product_small(M, K, N)) {
+  const ProductPlan plan = plan_product(M, K, N, sms, max_pairs, clusters);
+  if (plan.form == kFormNone) return CODA_ERR_LAUNCH;
+
+  if (plan.form == kFormSmall) {
     SmallQ8Params sp = {};
     sp.a_s = a_s;
     sp.w_s = w_s;
@@ -1776,17 +1833,14 @@ coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* 
     sp.K = Ki;
     sp.N = Ni;
     if (launch_product_small(sp, reinterpret_cast<const uint8_t*>(a_q),
-                             reinterpret_cast<const uint8_t*>(W_q), sms, stream) != cudaSuccess) {
+                             reinterpret_cast<const uint8_t*>(W_q), plan.split, stream) != cudaSuccess) {
       cudaGetLastError();
       return CODA_ERR_LAUNCH;
     }
     after_launch(0, stream);
     return CODA_OK;
   }
-  char* wsb = static_cast<char*>(workspace);
-  const MidPlan plan = plan_mid(M, K, N, clusters);
-  // (short K, whose waves the plan takes for some 3 us shorter than they are: 10 % in hand)
-  if (M <= kMidSure || 1.1 * plan.ns < product_gemm_ns(M, K, N, max_pairs)) {
+  if (plan.form == kFormMid) {
     MidQ8Params mp = {};
     mp.a_s = a_s;
     mp.w_s = w_s;
@@ -1796,12 +1850,13 @@ coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* 
     mp.K = Ki;
     mp.N = Ni;
     if (launch_product_mid(mp, reinterpret_cast<const uint8_t*>(a_q),
-                           reinterpret_cast<const uint8_t*>(W_q), plan, stream) != cudaSuccess) {
+                           reinterpret_cast<const uint8_t*>(W_q), plan.mid, stream) != cudaSuccess) {
       cudaGetLastError();
       return CODA_ERR_LAUNCH;
     }
     return CODA_OK;
   }
+  char* wsb = static_cast<char*>(workspace);
   __nv_bfloat16* a = reinterpret_cast<__nv_bfloat16*>(wsb + kSlotBytes);
   __nv_bfloat16* W =
       reinterpret_cast<__nv_bfloat16*>(wsb + kSlotBytes + align256(static_cast<size_t>(M) * K * 2));

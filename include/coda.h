@@ -355,6 +355,15 @@ CODA_API coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const
                                       int64_t N, coda_bf16* y_out, void* workspace,
                                       size_t workspace_bytes, cudaStream_t stream);
 
+/* The form that coda_matmul_q8 would take on a device of `sms` SMs with `pairs` co-resident CTA pairs
+ * of the GEMM and clusters[i] co-resident clusters of 2 << i blocks of the mid-size form.  Host only;
+ * for tests and measurements.  Writes plan[3] = {parts of a tile along K, tokens per CTA
+ * pair of the mid-size form, 1 for two of its blocks per SM} and returns 1 for few tokens, 2 for
+ * mid-size, 3 for the whole GEMM, 0 where the call is refused with CODA_ERR_LAUNCH (more than a few tokens, up to
+ * 1024, on a device where no pair of the mid-size form fits), -1 for bad arguments. */
+CODA_API int coda_matmul_q8_plan(int64_t M, int64_t K, int64_t N, int sms, int pairs,
+                                 const int32_t* clusters, int32_t* plan);
+
 /* coda_bwd_swiglu_dgrad from an 8-bit checkpoint of the pre-activation y = [g | u]:
  *   y_q [M, N1] INT8 codes, y_s [M, ceil(N1 / 128)] fp32 scales (coda_quant_q8 with block = 128)
  * take y's place, and a_out ([M, N1/2] bf16, may be NULL) receives a = silu(g) * u recomputed
