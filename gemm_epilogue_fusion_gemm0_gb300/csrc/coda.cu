@@ -13,8 +13,6 @@
 #include <atomic>
 #include <chrono>
 #include <cmath>
-#include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -978,8 +976,9 @@ cudaError_t launch_row_q8(const RowQ8Params& p, int sms, cudaStream_t stream) {
   if (threads > 512 && threads <= 1024) {
     // Rows of more than 16384 columns leave one or two blocks to an SM: walked by blocks that stay,
     // where two rows fit and there are at least four for each block (8192 x 28672, norm without a
-    // residual 113 us against 182, quantiser 118 against 133; at 8192 x 8192 it is the other way
-    // around, 82 us against 74 with a residual).
+    // residual 108 us against 139, quantiser 120 against 133; 8192 x 16640, norm with a residual
+    // 107 against 160, without 84 against 71; at 8192 x 8192 it is the other way around, 82 us against 74
+    // with a residual).
     const int stage = (kRes ? 4 : 2) * p.d;
     const int room = kRingSmem - static_cast<int>(row_ring_bytes(p.d, kNorm, kRes, 0));
     const int stages = std::min(kRingMaxStages, room / stage);

@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 1024) row_q8_kernel(const Row
 
 // The same for many rows: blocks that stay and walk the rows, whose bytes arrive by bulk copies in a
 // ring of `stages` rows in shared memory (gamma beside it), so that loads stay in flight while
-// rows are reduced, quantised and stored and cost no registers.  With one block per row,
-// or the next row in registers, too few bytes are in flight: 8192 x 8192, norm without a
-// residual 44 and 41 us, the quantiser 34 and 33 us.
+// rows are reduced, quantised and stored and cost no registers.  A block per row, of which an SM holds
+// one or two at these widths, keeps too few in flight: 8192 x 28672, norm without a residual 139 us
+// and 108 here, the quantiser 133 and 120; 8192 x 20480, norm with one 171 and 142.
 // Shared memory: [gamma | stages x (x row | z row) | barriers, abort flag].
 constexpr int kRingMaxStages = 8;
 

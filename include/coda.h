@@ -329,7 +329,7 @@ CODA_API coda_status_t coda_dequant_q8(const int8_t* q, const float* s, int64_t 
  *   h = x + z,   r = 1 / sqrt(mean_j h^2 + eps),   norm = r * h * gamma
  *   -> h_out = bf16(h), q_out and s_out = the codes and the scale of norm
  * h enters the norm unrounded, in fp32.  A row's sum of squares has to stay below FLT_MAX, as in
- * coda_fwd.  A row of zeros gives codes 0 and, with eps > 0, scale 0 (NaN with eps = 0).
+ * coda_fwd, and so has h * gamma, whose ratios are the codes (below 2^-126 it loses bits).  A row of zeros gives codes 0 and, with eps > 0, scale 0 (NaN with eps = 0).
  *   x [M, d] bf16 in;  z [M, d] bf16 in, may be NULL (h = x);  gamma [d] bf16 in;
  *   h_out [M, d] bf16 out, may be NULL (not wanted);  q_out [M, d] INT8, s_out [M] fp32 out
  * d a positive multiple of 8; eps >= 0, finite. */
@@ -344,7 +344,8 @@ CODA_API coda_status_t coda_add_rmsnorm_q8(const coda_bf16* x, const coda_bf16* 
  *   a_q [M, K] INT8, a_s [M] fp32;  W_q [K, N] INT8 ([in, out]), w_s [N] fp32;
  *   z [M, N] bf16, may be NULL;  y_out [M, N] bf16 out
  * K and N positive multiples of 16; codes may be anything in [-128, 127].  Sums are fp32 sums of
- * exact products: exact while they stay below 2^24.  A NaN scale makes its row or column NaN.
+ * exact products: exact while they stay below 2^24.  A sum is multiplied by a_s first, in
+ * fp32's range, then by w_s.  A NaN scale makes its row or column NaN.
  * workspace: at least coda_matmul_q8_workspace_bytes(M, K, N); NULL will do where that is 0
  * (up to 1024 tokens).
  * A tile whose pair of blocks was given different tensor memory (detail 0x10b of
