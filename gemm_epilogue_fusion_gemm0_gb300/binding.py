@@ -179,7 +179,7 @@ class _Call:
             return torch.empty(shape, dtype=dtype, device=self.device)
         if self.user is None:
             # 1 is CUDA's handle of the legacy default stream, which torch knows as 0
-            self.user = (self.stream if hasattr(self.stream, "cuda_stream")
+            self.user = (self.stream if isinstance(self.stream, torch.cuda.Stream)
                          else torch.cuda.ExternalStream(0 if handle == 1 else handle,
                                                         device=self.device))
         with torch.cuda.stream(self.user):

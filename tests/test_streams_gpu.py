@@ -140,3 +140,23 @@ def test_the_current_stream_by_its_own_name(B):
         torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_a_stream_of_another_library(B):
+    """Any object that names its handle and its device."""
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    t = inputs()
+    side = torch.cuda.Stream()
+    for name in ("norm", "fwd"):
+        want = CALLS[name](B, t, None)
+        torch.cuda.synchronize()
+        got = CALLS[name](B, t, Stream(side.cuda_stream))
+        side.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
