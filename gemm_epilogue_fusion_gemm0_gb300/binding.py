@@ -57,6 +57,9 @@ STATUS_NAMES = {
 _vp, _i64, _sz, _f32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint64
 _st, _int = ctypes.c_int, ctypes.c_int
 
+# the paged cache and the batch: four tensors, pages, Hk, page, D; cu, lens, table, B, width, T
+_CACHE = [_vp] * 4 + [_i64] * 4 + [_vp] * 3 + [_i64] * 3
+
 EXPORTS = {
     # name: (restype, argtypes)
     "coda_fwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
@@ -101,6 +104,10 @@ EXPORTS = {
     "coda_matmul_q8_plan": (_int, [_i64, _i64, _i64, _int, _int, _vp, _vp]),
     "coda_bwd_swiglu_dgrad_q8": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
                                        _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "coda_cache_write_q8": (_st, [_vp, *_CACHE, _i64, _vp, _vp, _i64, _vp, _i64, _int, _vp, _vp]),
+    "coda_cache_read_q8": (_st, [*_CACHE, _vp, _vp, _vp]),
+    "coda_attn_q8_workspace_bytes": (_sz, [_i64] * 5),
+    "coda_attn_q8": (_st, [_vp, *_CACHE, _i64, _f32, _i64, _vp, _vp, _vp, _sz, _vp]),
 }
 
 for _name, (_res, _args) in EXPORTS.items():
@@ -481,6 +488,108 @@ def coda_bwd_swiglu_dgrad_q8(dout, W2, y_q, y_s, W1, h, r, gamma, dy=None, s=Non
     c.run(_lib.coda_bwd_swiglu_dgrad_q8, *ins, M, d, N1, Dout, dyp, sp, dhp, ap, wk, wkb,
           stream=stream)
     return (dy, s, dh, a) if a is not None else (dy, s, dh)
+
+
+# --------------------------------------------------------------------------- 8-bit paged cache
+def coda_cache_q8(pages: int, Hk: int, page: int, D: int, device="cuda") -> tuple:
+    """Memory for a cache of `pages` pages of `page` tokens: (k_q, k_s, v_q, v_s), codes
+    [pages, Hk, page, D] and scales [pages, Hk, page] of keys and of values, not initialised."""
+    codes, scales = (pages, Hk, page, D), (pages, Hk, page)
+    return tuple(torch.empty(shape, dtype=dtype, device=device)
+                 for shape, dtype in ((codes, torch.int8), (scales, torch.float32)) * 2)
+
+
+def _cache_args(c: _Call, cache, cu, lens, table, T: int) -> tuple:
+    """The C arguments of a cache and a batch."""
+    k_q, k_s, v_q, v_s = cache
+    codes = pages, Hk, page, D = k_q.shape
+    B, width = table.shape
+    i8, f32, i32 = torch.int8, torch.float32, torch.int32
+    return (c.t(k_q, i8, codes, "k_q"), c.t(k_s, f32, codes[:3], "k_s"), c.t(v_q, i8, codes, "v_q"),
+            c.t(v_s, f32, codes[:3], "v_s"), pages, Hk, page, D, c.t(cu, i32, (B + 1,), "cu"),
+            c.t(lens, i32, (B,), "lens"), c.t(table, i32, (B, width), "table"), B, width, T)
+
+
+def _host(t, dtype, n: int, name: str) -> int:
+    """Address of a contiguous CPU tensor of n numbers, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} CPU tensor")
+    if tuple(t.shape) != (n,):
+        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def coda_cache_write_q8(y, cache, cu, lens, table, inv_freq=None, axis=None, pos=None, pairs=False,
+                        q=None, stream=None):
+    """The rows y [T, (Hq + 2 Hk) D] = [q | k | v] of the sequences' last tokens: q and k turned by
+    their positions, k and v into the cache (k_q, k_s, v_q, v_s; see coda_cache_q8) as INT8 codes with
+    a scale per token and head.  Returns q [T, Hq D] (bf16).
+
+    Rows cu[b] .. cu[b + 1] - 1 are the last of sequence b's lens[b] tokens; token p lies in page
+    table[b, p // page].  inv_freq: float64 CPU tensor of the pairs' frequencies (None: no turn);
+    axis: int32 CPU tensor, the row of pos [axes, T] that turns each pair (None: row 0); without pos a
+    token's number is its position.  pairs: pair i is values (2 i, 2 i + 1) and not (i, i + half)."""
+    T, n = y.shape
+    _, Hk, _, D = cache[0].shape
+    if n % D or n // D <= 2 * Hk:
+        raise ValueError(f"y must have Hq + 2 * {Hk} heads of {D} values, got {n} values")
+    Hq = n // D - 2 * Hk
+    c = _Call("coda_cache_write_q8", y.device, stream)
+    bf = torch.bfloat16
+    yp = c.t(y, bf, (T, n), "y")
+    args = _cache_args(c, cache, cu, lens, table, T)
+    half = 0 if inv_freq is None else inv_freq.numel()
+    fp, ap = _host(inv_freq, torch.float64, half, "inv_freq"), _host(axis, torch.int32, half, "axis")
+    axes = 1 if pos is None else pos.shape[0]
+    pp = c.opt(pos, torch.int32, (axes, T), "pos")
+    q, qp = c.out(q, bf, (T, Hq * D), "q")
+    c.run(_lib.coda_cache_write_q8, yp, *args, Hq, fp, ap, half, pp, axes, int(bool(pairs)), qp,
+          stream=stream)
+    return q
+
+
+def coda_cache_read_q8(cache, cu, lens, table, T, k=None, v=None, stream=None):
+    """The T rows' tokens out of the cache (arguments as coda_cache_write_q8; with cu the running sum
+    of lens, whole sequences): (k, v), each [T, Hk, D] in bf16."""
+    _, Hk, _, D = cache[0].shape
+    c = _Call("coda_cache_read_q8", cache[0].device, stream)
+    args = _cache_args(c, cache, cu, lens, table, T)
+    bf = torch.bfloat16
+    k, kp = c.out(k, bf, (T, Hk, D), "k")
+    v, vp = c.out(v, bf, (T, Hk, D), "v")
+    c.run(_lib.coda_cache_read_q8, *args, kp, vp, stream=stream)
+    return k, v
+
+
+def coda_attn_q8_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int) -> int:
+    return int(_lib.coda_attn_q8_workspace_bytes(T, B, Hq, Hk, D))
+
+
+def coda_attn_q8(q, cache, cu, lens, table, scale=None, most=0, o=None, lse=None, want_lse=False,
+                 ws=None, stream=None):
+    """Causal attention of the rows q [T, Hq D] over their sequences' tokens in the cache (arguments as
+    coda_cache_write_q8, which has put the rows' own tokens there); scale defaults to 1 / sqrt(D).
+    most: the largest number of rows of a sequence, if known (a hint).  Returns o [T, Hq D], or
+    (o, lse) with want_lse=True (lse [T, Hq] fp32, natural logarithm)."""
+    T, n = q.shape
+    _, Hk, _, D = cache[0].shape
+    if n % D:
+        raise ValueError(f"q must have heads of {D} values, got {n} values")
+    Hq = n // D
+    c = _Call("coda_attn_q8", q.device, stream)
+    bf = torch.bfloat16
+    qp = c.t(q, bf, (T, n), "q")
+    args = _cache_args(c, cache, cu, lens, table, T)
+    o, op = c.out(o, bf, (T, n), "o")
+    lp = None
+    if want_lse or lse is not None:
+        lse, lp = c.out(lse, torch.float32, (T, Hq), "lse")
+    ws, wk, wkb = c.scratch(ws, _lib.coda_attn_q8_workspace_bytes(T, table.shape[0], Hq, Hk, D))
+    c.run(_lib.coda_attn_q8, qp, *args, Hq, float(D ** -0.5 if scale is None else scale), int(most), op, lp,
+          wk, wkb, stream=stream)
+    return (o, lse) if lse is not None else o
 
 
 def coda_bwd_workspace_bytes(M: int, d: int, N1: int) -> int:

@@ -24,6 +24,8 @@
 #include <cudaTypedefs.h>
 
 #include "coda.h"
+#include "attn_q8.cuh"
+#include "cache_q8.cuh"
 #include "epilogues.cuh"
 #include "gemm_pair.cuh"
 #include "q8.cuh"
@@ -1162,6 +1164,104 @@ cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t*
   return e;
 }
 
+// ---------------------------------------------------------------------------
+// The 8-bit paged cache (cache_q8.cuh, attn_q8.cuh)
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxSequences = 8192, kMaxHeads = 1024;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+coda_status_t check_heads(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
+  if (T < 0 || B < 0 || Hq <= 0 || Hk <= 0 || D <= 0) return CODA_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t(1) << 31) - 256;
+  if ((D != 64 && D != 128) || Hq % Hk != 0 || Hq > kMaxHeads || B > kMaxSequences || T > lim ||
+      !fits(T, (Hq + 2 * Hk) * D))
+    return CODA_ERR_UNSUPPORTED_SHAPE;
+  return CODA_OK;
+}
+
+// The sizes, then the pointers of the cache and of the batch (not looked at where nothing is to do).
+coda_status_t check_cache(const int8_t* k_q, const float* k_s, const int8_t* v_q, const float* v_s,
+                          int64_t pages, int64_t Hq, int64_t Hk, int64_t page, int64_t D,
+                          const int32_t* cu, const int32_t* lens, const int32_t* table, int64_t B,
+                          int64_t width, int64_t T, CacheQ8* c, BatchQ8* bt) {
+  const coda_status_t st = check_heads(T, B, Hq, Hk, D);
+  if (st != CODA_OK) return st;
+  if (pages <= 0 || page <= 0 || width <= 0) return CODA_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t(1) << 31) - 256;
+  // (a token's number, and the pages of all sequences, stay far below 2^31)
+  if (page < 16 || page > 256 || (page & (page - 1)) != 0 || pages > lim || !fits(pages, Hk * page * D) ||
+      width > (int64_t(1) << 30) / page)
+    return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0 || B == 0) return CODA_OK;
+  const void* ptrs[] = {k_q, k_s, v_q, v_s};
+  for (const void* p : ptrs)
+    if (!p) return CODA_ERR_INVALID_ARG;
+  if (!cu || !lens || !table) return CODA_ERR_INVALID_ARG;
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return CODA_ERR_MISALIGNED;
+  if (!aligned4(cu) || !aligned4(lens) || !aligned4(table)) return CODA_ERR_MISALIGNED;
+  c->k_q = reinterpret_cast<uint8_t*>(const_cast<int8_t*>(k_q));
+  c->k_s = const_cast<float*>(k_s);
+  c->v_q = reinterpret_cast<uint8_t*>(const_cast<int8_t*>(v_q));
+  c->v_s = const_cast<float*>(v_s);
+  c->pages = static_cast<int>(pages);
+  c->Hk = static_cast<int>(Hk);
+  c->page_log2 = 0;
+  while ((int64_t(1) << c->page_log2) < page) ++c->page_log2;
+  bt->cu = cu;
+  bt->lens = lens;
+  bt->table = table;
+  bt->B = static_cast<int>(B);
+  bt->width = static_cast<int>(width);
+  bt->rows = static_cast<int>(T);
+  return CODA_OK;
+}
+
+// turn[i]: inv_freq[i] / (2 pi) modulo one turn, a turn being 2^64
+coda_status_t rope_of(const double* inv_freq, const int32_t* axis, int64_t half, const int32_t* pos,
+                      int64_t axes, int pairs, int64_t D, RopeQ8* r) {
+  if (half < 0 || axes < 1 || axes > kRopeAxes || (pos == nullptr && axes != 1)) return CODA_ERR_INVALID_ARG;
+  if (half % 8 != 0 || 2 * half > D) return CODA_ERR_UNSUPPORTED_SHAPE;
+  if (half > 0 && inv_freq == nullptr) return CODA_ERR_INVALID_ARG;
+  if (!aligned4(pos)) return CODA_ERR_MISALIGNED;
+  *r = RopeQ8{};
+  for (int64_t i = 0; i < half; ++i) {
+    if (!std::isfinite(inv_freq[i])) return CODA_ERR_INVALID_ARG;
+    if (axis != nullptr && (axis[i] < 0 || axis[i] >= axes)) return CODA_ERR_INVALID_ARG;
+    const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    const double part = turns - std::floor(turns);
+    r->turn[i] = part < 1.0 ? static_cast<uint64_t>(std::ldexp(part, 64)) : 0;
+    r->axis[i] = static_cast<uint8_t>(axis != nullptr ? axis[i] : 0);
+  }
+  r->pos = pos;
+  r->half = static_cast<int>(half);
+  r->pairs = pairs != 0;
+  return CODA_OK;
+}
+
+template <int kD>
+cudaError_t launch_cache_write(const CacheWriteParams& p, const RopeQ8& r, int sms, cudaStream_t stream) {
+  const int T = p.batch.rows, heads = p.Hq + 2 * p.cache.Hk;
+  // four tokens to a block while that leaves every SM some; else one, its heads over several blocks
+  if (T >= 8 * sms)
+    return launch(&cache_write_q8_kernel<kD, 4>, static_cast<int>(cdiv(T, 4)), kCacheThreads, 0, stream,
+                  false, p, r);
+  const int64_t most = cdiv(heads, kCacheThreads / (kD / 8));
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(most, 4 * sms / T));
+  return launch(&cache_write_q8_kernel<kD, 1>, dim3(T, static_cast<unsigned>(parts)), kCacheThreads, 0,
+                stream, false, p, r);
+}
+
+template <int kD>
+cudaError_t launch_cache_read(const CacheReadParams& p, int sms, cudaStream_t stream) {
+  const int64_t blocks = cdiv(p.batch.rows, kReadTokens);
+  const int64_t most = cdiv(kReadTokens * p.cache.Hk, kCacheThreads / (kD / 16));
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(most, 4 * sms / blocks));
+  return launch(&cache_read_q8_kernel<kD>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(parts)),
+                kCacheThreads, 0, stream, false, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1896,6 +1996,105 @@ coda_status_t coda_matmul_q8(const int8_t* a_q, const float* a_s, const int8_t* 
     return CODA_ERR_LAUNCH;
   }
   after_launch(2, stream);
+  return CODA_OK;
+}
+
+coda_status_t coda_cache_write_q8(const coda_bf16* y, int8_t* k_q, float* k_s, int8_t* v_q, float* v_s,
+                                  int64_t pages, int64_t Hk, int64_t page, int64_t D, const int32_t* cu,
+                                  const int32_t* lens, const int32_t* table, int64_t B, int64_t width,
+                                  int64_t T, int64_t Hq, const double* inv_freq, const int32_t* axis,
+                                  int64_t half, const int32_t* pos, int64_t axes, int pairs,
+                                  coda_bf16* q_out, cudaStream_t stream) {
+  CacheWriteParams p = {};
+  coda_status_t st = check_cache(k_q, k_s, v_q, v_s, pages, Hq, Hk, page, D, cu, lens, table, B, width, T,
+                                 &p.cache, &p.batch);
+  if (st != CODA_OK) return st;
+  RopeQ8 r;
+  st = rope_of(inv_freq, axis, half, pos, axes, pairs, D, &r);
+  if (st != CODA_OK) return st;
+  if (T == 0 || B == 0) return CODA_OK;
+  if (!y || !q_out) return CODA_ERR_INVALID_ARG;
+  if (!aligned16(y) || !aligned16(q_out)) return CODA_ERR_MISALIGNED;
+  int sms = 0;
+  st = device_setup(&sms);
+  if (st != CODA_OK) return st;
+  p.y = reinterpret_cast<const __nv_bfloat16*>(y);
+  p.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  p.Hq = static_cast<int>(Hq);
+  const cudaError_t e = D == 64 ? launch_cache_write<64>(p, r, sms, stream)
+                                : launch_cache_write<128>(p, r, sms, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return CODA_ERR_LAUNCH;
+  }
+  after_launch(0, stream);
+  return CODA_OK;
+}
+
+coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, const int8_t* v_q, const float* v_s,
+                                 int64_t pages, int64_t Hk, int64_t page, int64_t D, const int32_t* cu,
+                                 const int32_t* lens, const int32_t* table, int64_t B, int64_t width,
+                                 int64_t T, coda_bf16* k_out, coda_bf16* v_out, cudaStream_t stream) {
+  CacheReadParams p = {};
+  coda_status_t st = check_cache(k_q, k_s, v_q, v_s, pages, Hk, Hk, page, D, cu, lens, table, B, width, T,
+                                 &p.cache, &p.batch);
+  if (st != CODA_OK) return st;
+  if (T == 0 || B == 0) return CODA_OK;
+  if (!k_out || !v_out) return CODA_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return CODA_ERR_MISALIGNED;
+  int sms = 0;
+  st = device_setup(&sms);
+  if (st != CODA_OK) return st;
+  p.k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  p.v_out = reinterpret_cast<__nv_bfloat16*>(v_out);
+  const cudaError_t e = D == 64 ? launch_cache_read<64>(p, sms, stream) : launch_cache_read<128>(p, sms, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return CODA_ERR_LAUNCH;
+  }
+  after_launch(0, stream);
+  return CODA_OK;
+}
+
+size_t coda_attn_q8_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
+  if (check_heads(T, B, Hq, Hk, D) != CODA_OK || T == 0 || B == 0) return 0;
+  return kSlotBytes;
+}
+
+coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k_s, const int8_t* v_q,
+                           const float* v_s, int64_t pages, int64_t Hk, int64_t page, int64_t D,
+                           const int32_t* cu, const int32_t* lens, const int32_t* table, int64_t B,
+                           int64_t width, int64_t T, int64_t Hq, float scale, int64_t most,
+                           coda_bf16* o_out, float* lse_out, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  AttnQ8Params p = {};
+  coda_status_t st = check_cache(k_q, k_s, v_q, v_s, pages, Hq, Hk, page, D, cu, lens, table, B, width, T,
+                                 &p.cache, &p.batch);
+  if (st != CODA_OK) return st;
+  if (!std::isfinite(scale) || scale <= 0.f || most < 0) return CODA_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return CODA_OK;
+  if (!q || !o_out) return CODA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, o_out, lse_out, workspace};  // lse_out may be null
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return CODA_ERR_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < coda_attn_q8_workspace_bytes(T, B, Hq, Hk, D))
+    return CODA_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  st = device_setup(&sms);
+  if (st != CODA_OK) return st;
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.o = reinterpret_cast<__nv_bfloat16*>(o_out);
+  p.lse = lse_out;
+  p.Hq = static_cast<int>(Hq);
+  p.group = static_cast<int>(Hq / Hk);
+  p.scale_log2 = scale * 1.44269504088896f;
+  const cudaError_t e = launch(D == 64 ? &attn_q8_rows_kernel<64> : &attn_q8_rows_kernel<128>,
+                               static_cast<int>(cdiv(T * Hq, 8)), 256, 0, stream, false, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return CODA_ERR_LAUNCH;
+  }
+  after_launch(0, stream);
   return CODA_OK;
 }
 

@@ -79,7 +79,7 @@ typedef enum {
   CODA_ERR_DEVICE_TIMEOUT = 6,     /* a bounded device-side wait ran out */
   CODA_ERR_NO_DEVICE = 7,          /* no CUDA device is current */
   CODA_ERR_UNSUPPORTED_DEVICE = 8, /* the current device is not compute capability 10.3 */
-  CODA_ERR_DEVICE_BOUNDS = 9       /* checked build only: a device-side bounds or alignment check failed */
+  CODA_ERR_DEVICE_BOUNDS = 9       /* a page outside of the cache; checked build: a device-side bounds or alignment check failed */
 } coda_status_t;
 
 /* Bytes of device workspace coda_fwd needs: the 256-byte slot of the launch
@@ -381,10 +381,93 @@ CODA_API coda_status_t coda_bwd_swiglu_dgrad_q8(const coda_bf16* dout, const cod
                                                 coda_bf16* a_out, void* workspace,
                                                 size_t workspace_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The 8-bit paged cache: what stands between y of one chain (W1 the projection to
+ * queries, keys and values) and x of the next (W0 the output projection):
+ *   coda_cache_write_q8(y) -> q, the new tokens in the cache;  coda_attn_q8(q) -> x
+ *
+ * Keys and values are INT8 codes with one fp32 scale per token and head, as coda_quant_q8's
+ * over the head's D values, in pages of `page` tokens:
+ *   k_q, v_q [pages, Hk, page, D] INT8;  k_s, v_s [pages, Hk, page] fp32
+ *   D 64 or 128; page a power of two from 16 to 256.
+ * Token p of sequence b lies in page table[b, p / page], slot p % page:
+ *   table [B, width] int32; entries that no token of the call needs are not read.
+ * A call's rows are the last tokens of the sequences, packed one sequence after the other:
+ *   cu [B + 1] int32: rows cu[b] .. cu[b + 1] - 1 are sequence b's (cu[0] = 0, not decreasing);
+ *   lens [B] int32: its tokens in all, these among them;
+ *   so row i is its token lens[b] - (cu[b + 1] - i).
+ *   T: rows of the tensors; rows behind the last sequence (cu[B] .. T - 1) are not read
+ *   and not written.
+ * A row whose token number is negative (a sequence with more rows than tokens: padding in front)
+ * has no place in the cache.  A sequence may have no rows, or no tokens.
+ * cu, lens and table are device memory, read when the call runs: a captured call follows them.  A
+ * place that the table does not have (token p >= width * page) or a page outside of 0 .. pages - 1 is
+ * never touched: coda_cache_write_q8 writes nothing there, coda_cache_read_q8 gives NaN, every row of
+ * coda_attn_q8 that sees such a token is NaN, and coda_get_device_status reports
+ * CODA_ERR_DEVICE_BOUNDS (detail 0x240).
+ * B at most 8192; Hq a multiple of Hk, both at most 1024; Hq = group * Hk, query head h reads
+ * key head h / group.  cu, lens, table and pos need 4-byte alignment only.  T = 0 or B = 0: nothing is
+ * launched.
+ * ------------------------------------------------------------------------- */
+
+/* A projection's rows into the cache: y's row holds Hq + 2 Hk heads of D values, [q | k | v].
+ * The first 2 * half values of each head of q and k are turned in pairs (rotary positions),
+ *   a' = a cos t - b sin t,  b' = a sin t + b cos t,  t = pos * inv_freq[i],  i = 0 .. half - 1,
+ * pair i being values (i, i + half), or with pairs != 0 values (2 i, 2 i + 1); then
+ *   q_out = bf16(q'), and k' (in fp32) and v become the codes and scales of the rows' tokens.
+ *   y [T, (Hq + 2 Hk) D] bf16 in;  q_out [T, Hq D] bf16 out (rows without a place in the cache too)
+ *   inv_freq [half]: HOST doubles, finite; half 0 (no turn, inv_freq may be NULL) or a multiple
+ *     of 8, 2 half <= D
+ *   axis [half]: HOST int32 in 0 .. axes - 1, the axis whose position turns pair i (time, height,
+ *     width of an image's or a video's patches); NULL: axis 0 for all
+ *   pos [axes, T] int32: the rows' positions on each axis (1 to 4 axes); NULL: a row's token number
+ *     (then axes = 1)
+ * inv_freq and axis are read before the call returns.  Angles are exact to 2^-30 of a turn at any
+ * position.  The rows of a call have to be distinct tokens: of two rows at one place either's codes
+ * and scale may stay. */
+CODA_API coda_status_t coda_cache_write_q8(const coda_bf16* y, int8_t* k_q, float* k_s, int8_t* v_q,
+                                           float* v_s, int64_t pages, int64_t Hk, int64_t page,
+                                           int64_t D, const int32_t* cu, const int32_t* lens,
+                                           const int32_t* table, int64_t B, int64_t width, int64_t T,
+                                           int64_t Hq, const double* inv_freq, const int32_t* axis,
+                                           int64_t half, const int32_t* pos, int64_t axes, int pairs,
+                                           coda_bf16* q_out, cudaStream_t stream);
+
+/* The rows' tokens out of the cache, bf16(code * scale); zeros for rows without a place.  With
+ * cu the running sum of lens: whole sequences.
+ *   k_out, v_out [T, Hk, D] bf16 out */
+CODA_API coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, const int8_t* v_q,
+                                          const float* v_s, int64_t pages, int64_t Hk, int64_t page,
+                                          int64_t D, const int32_t* cu, const int32_t* lens,
+                                          const int32_t* table, int64_t B, int64_t width, int64_t T,
+                                          coda_bf16* k_out, coda_bf16* v_out, cudaStream_t stream);
+
+/* Attention of the rows over their sequences' tokens in the cache, causal: row i of sequence b sees
+ * tokens 0 .. p, p its own token number (which the cache holds already).
+ *   o = sum_j w_j v_j / sum_j w_j,   lse = log sum_j w_j,   w_j = exp(scale * q . k_j)
+ *   q [T, Hq D] bf16 in;  o_out [T, Hq D] bf16 out;  lse_out [T, Hq] fp32 out, may be NULL
+ *   scale > 0, finite.  A row that sees no token: o = 0, lse = -infinity.
+ * One token per sequence, a few, a chunk and a whole prompt (lens = rows) are the same call.  most: a
+ * hint, the largest number of rows of a sequence (0: not known); with any other value the result is
+ * the same and the time may be longer.
+ * fp32 sums and softmax; weights are rounded to fp16 (by 2^-11 of them at most) before their products with v's codes.
+ * Results do not depend on other sequences but in the order of fp32 sums, and are the same on
+ * every run of the same call.
+ *   workspace: at least coda_attn_q8_workspace_bytes(T, B, Hq, Hk, D) */
+CODA_API size_t coda_attn_q8_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D);
+CODA_API coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k_s,
+                                    const int8_t* v_q, const float* v_s, int64_t pages, int64_t Hk,
+                                    int64_t page, int64_t D, const int32_t* cu, const int32_t* lens,
+                                    const int32_t* table, int64_t B, int64_t width, int64_t T,
+                                    int64_t Hq, float scale, int64_t most, coda_bf16* o_out,
+                                    float* lse_out, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
 /* Synchronises `stream`, then reports and clears the library's device-side
  * status word: CODA_OK, CODA_ERR_DEVICE_TIMEOUT if a bounded wait in any
  * kernel of this library ran out since the last call (raw code 0x100 | which
- * wait; 0x10b: see coda_matmul_q8), or, in the checked build (libcoda_checked.so, compiled with
+ * wait; 0x10b: see coda_matmul_q8), CODA_ERR_DEVICE_BOUNDS with the raw code 0x240 if a call met
+ * a page outside of its cache (see the 8-bit paged cache), or, in the checked build (libcoda_checked.so, compiled with
  * -DCODA_CHECKED: every staged epilogue load and store, gamma load, TMA box
  * start and workspace index checked on the device), CODA_ERR_DEVICE_BOUNDS if a check failed and
  * its access was skipped (raw code 0x200 | which check).  The first failure
@@ -505,7 +588,7 @@ CODA_API coda_status_t coda_fwd_unfused(const coda_bf16* x, const coda_bf16* W0,
  * time each launch on the launching stream.  coda_fwd, coda_fwd_swiglu,
  * coda_fwd_unfused, coda_fwd_fp8 and coda_bwd_swiglu_dgrad launch 3 kernels
  * (2 for the forwards with the folded row reduction), coda_bwd 5,
- * coda_bwd_dgrad 1, coda_bwd_swiglu_dgrad_q8 3, coda_matmul_q8 1 or 3 and the
+ * coda_bwd_dgrad 1, coda_bwd_swiglu_dgrad_q8 3, coda_matmul_q8 1 or 3, coda_attn_q8 1 to 3 and the
  * other 8-bit operators 1.  The events are caller-owned; pass NULL to stop.
  * Process-wide setting, not thread-safe; no effect on results.
  */
