@@ -1,14 +1,27 @@
-// attn_q8.cuh -- attention of new tokens over the 8-bit paged cache.
+// attn_q8.cuh -- attention of new tokens over the 8-bit paged cache: the deal of the work, the kernel
+// for few rows (decoding), and the join of parts.
 //
 //   o[i] = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - m_i),  j <= lens - n + i
 //   lse[i] = m_i + log sum_j p_ij
 // i being one of a sequence's n new tokens, k_j and v_j the values of the cache's codes.  A row
 // that sees no key is zero, its lse -inf.
+//
+// The rows of a sequence that share a key head, n tokens of `group` query heads each, are packed
+// (row r is token r / group, head r % group) and cut into tiles; a tile with its keys is an item, and
+// 128 keys of it a unit.  Lengths are known to the device alone, so each block of a persistent grid
+// adds up the units of all sequences, takes an equal, contiguous share of them, and walks it: whatever
+// the lengths, all SMs end together, and a long sequence's keys are spread over as many blocks as its
+// share of the work.  A part of an item leaves its running maximum, sum and unnormalised
+// outputs in the workspace; a second kernel joins the parts of each such item in the order of its keys, so
+// the same call gives the same bits every time.
 #pragma once
 
 #include "cache_q8.cuh"
 
 namespace coda {
+
+constexpr int kAttnUnit = 128;       // keys
+constexpr int kAttnMaxBlocks = 160;  // of the persistent grids
 
 struct AttnQ8Params {
   const __nv_bfloat16* q;  // [rows, Hq, D]
@@ -16,59 +29,648 @@ struct AttnQ8Params {
   float* lse;              // [rows, Hq] or null
   CacheQ8 cache;
   BatchQ8 batch;
-  int Hq, group;  // query heads; of them per key head
-  float scale_log2;
+  int Hq, group;           // query heads; of them per key head
+  float scale_log2;        // scale * log2 e
 };
 
-// A warp per (row, query head): keys one after the other, the softmax's maximum and sum running.
+// ---------------------------------------------------------------------------
+// The deal
+// ---------------------------------------------------------------------------
+// A sequence as the call describes it, whatever cu and lens hold.
+struct AttnSeq {
+  int row0;   // its first row
+  int n;      // rows of q that it has (0: none that exist)
+  int first;  // token number of its first row; row i of it sees the keys 0 .. first + i
+};
+
+__host__ __device__ inline AttnSeq attn_seq(int cu0, int cu1, int len, int rows) {
+  AttnSeq s;
+  s.row0 = cu0;
+  const int64_t n = static_cast<int64_t>(cu1 < rows ? cu1 : rows) - cu0;
+  s.n = cu0 < 0 || n < 0 ? 0 : static_cast<int>(n);
+  s.first = static_cast<int>(static_cast<int64_t>(len > 0 ? len : 0) - (static_cast<int64_t>(cu1) - cu0));
+  return s;
+}
+
+// Keys that a tile of `tile_rows` packed rows sees at most.  `places`: tokens that the table has room
+// for; a row that sees more is NaN by the first of them that has none, so none after it is walked.
+__host__ __device__ inline int attn_extent(const AttnSeq& s, int group, int tile_rows, int64_t tile,
+                                           int places) {
+  const int64_t end = (tile + 1) * tile_rows, all = static_cast<int64_t>(s.n) * group;
+  const int64_t keys = s.first + ((end < all ? end : all) - 1) / group + 1;
+  return keys <= 0 ? 0 : static_cast<int>(keys < places + 1 ? keys : places + 1);
+}
+
+__host__ __device__ inline int attn_units(int extent) {
+  return extent <= kAttnUnit ? 1 : (extent + kAttnUnit - 1) / kAttnUnit;  // (an empty item still writes zeros)
+}
+
+__host__ __device__ inline int64_t attn_tiles(const AttnSeq& s, int group, int tile_rows) {
+  return (static_cast<int64_t>(s.n) * group + tile_rows - 1) / tile_rows;
+}
+
+// Units of a sequence for one key head, where its packed rows number lo + 1 .. hi; else 0.
+__host__ __device__ inline int64_t attn_seq_units(const AttnSeq& s, int group, int tile_rows, int places,
+                                                  int64_t lo, int64_t hi) {
+  const int64_t all = static_cast<int64_t>(s.n) * group;
+  if (all <= lo || all > hi) return 0;
+  int64_t u = 0;
+  const int64_t tiles = attn_tiles(s, group, tile_rows);
+  for (int64_t t = 0; t < tiles; ++t) u += attn_units(attn_extent(s, group, tile_rows, t, places));
+  return u;
+}
+
+// First unit of block c's share.
+__host__ __device__ inline int64_t attn_share(int64_t units, int c, int blocks) {
+  return units * c / blocks;
+}
+
+// Which sequences a launch takes, and the size of its tiles.
+struct AttnDeal {
+  int64_t lo, hi;  // packed rows of a sequence: lo + 1 .. hi
+};
+
+// An item whose first part is the last of block c's share: what the join needs to know.
+struct AttnCut {
+  int64_t units;    // of the launch
+  int64_t end;      // one past the item's last unit
+  int b, hk;
+  int64_t tile;
+  int valid, pad;
+};
+
+struct AttnWs {
+  AttnCut* cut;     // [blocks]
+  float2* ml;       // [2 blocks][tile rows]: maximum (of base 2 exponents) and sum
+  float* o;         // [2 blocks][tile rows][D]
+};
+
+__device__ __forceinline__ AttnSeq load_seq(const AttnQ8Params& p, int b) {
+  return attn_seq(__ldg(p.batch.cu + b), __ldg(p.batch.cu + b + 1), __ldg(p.batch.lens + b), p.batch.rows);
+}
+
+// Where a block is in its share.
+struct AttnWalk {
+  AttnSeq s;
+  int b, hk;
+  int64_t tile, tiles;
+  int unit, units, extent;
+};
+
+template <int kRows>
+__device__ __forceinline__ void walk_tile(AttnWalk& w, const AttnQ8Params& p, int places) {
+  w.extent = attn_extent(w.s, p.group, kRows, w.tile, places);
+  w.units = attn_units(w.extent);
+}
+
+// The next unit (there is one).
+template <int kRows>
+__device__ __forceinline__ void walk_on(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
+  if (++w.unit < w.units) return;
+  w.unit = 0;
+  if (++w.tile == w.tiles) {
+    w.tile = 0;
+    if (++w.hk == p.cache.Hk) {
+      w.hk = 0;
+      int64_t all;
+      do {
+        ++w.b;
+        if (w.b >= p.batch.B) return;  // (the end of the last share)
+        w.s = load_seq(p, w.b);
+        all = static_cast<int64_t>(w.s.n) * p.group;
+      } while (all <= d.lo || all > d.hi);
+      w.tiles = attn_tiles(w.s, p.group, kRows);
+    }
+  }
+  walk_tile<kRows>(w, p, places);
+}
+
+// Adds up the units (all threads of the block, kThreads of them), and puts the walk at unit `u0`
+// of this block's share.  Returns the launch's units; u1 the end of the share.
+template <int kRows, int kThreads>
+__device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d,
+                                              int places, int64_t& u0, int64_t& u1) {
+  __shared__ int64_t warp_sum[kThreads / 32];
+  __shared__ int64_t start_rest;
+  __shared__ int start_b;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int per = (p.batch.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.batch.B, tid * per), b1 = min(p.batch.B, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b)
+    mine += attn_seq_units(load_seq(p, b), p.group, kRows, places, d.lo, d.hi) * p.cache.Hk;
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) upto += warp_sum[i];
+    total += warp_sum[i];
+  }
+  u0 = attn_share(total, blockIdx.x, gridDim.x);
+  u1 = attn_share(total, blockIdx.x + 1, gridDim.x);
+  if (u0 < u1 && upto - mine <= u0 && u0 < upto) {  // one thread: u0 is in its sequences
+    int64_t rest = u0 - (upto - mine);
+    int b = b0;
+    while (true) {
+      const int64_t u = attn_seq_units(load_seq(p, b), p.group, kRows, places, d.lo, d.hi) * p.cache.Hk;
+      if (rest < u) break;
+      rest -= u;
+      ++b;
+    }
+    start_b = b;
+    start_rest = rest;
+  }
+  __syncthreads();
+  if (u0 >= u1) return total;
+  w.b = start_b;
+  w.s = load_seq(p, w.b);
+  w.tiles = attn_tiles(w.s, p.group, kRows);
+  int64_t rest = start_rest;
+  const int64_t per_head = attn_seq_units(w.s, p.group, kRows, places, d.lo, d.hi);
+  w.hk = static_cast<int>(rest / per_head);
+  rest -= w.hk * per_head;
+  for (w.tile = 0;; ++w.tile) {
+    walk_tile<kRows>(w, p, places);
+    if (rest < w.units) break;
+    rest -= w.units;
+  }
+  w.unit = static_cast<int>(rest);
+  return total;
+}
+
+// Row r of a tile: its row of q and its query head.  False behind the sequence's last.
+struct AttnRow {
+  int64_t at;  // row * Hq + head
+  int limit;   // the last key that it sees
+  bool in;
+};
+
+__device__ __forceinline__ AttnRow attn_row(const AttnQ8Params& p, const AttnSeq& s, int hk, int64_t packed) {
+  AttnRow r;
+  const int64_t all = static_cast<int64_t>(s.n) * p.group;
+  r.in = packed < all;
+  const int64_t i = (r.in ? packed : all - 1) / p.group;
+  const int g = static_cast<int>((r.in ? packed : all - 1) - i * p.group);
+  r.limit = s.first + static_cast<int>(i);
+  r.at = (s.row0 + i) * p.Hq + static_cast<int64_t>(hk) * p.group + g;
+  return r;
+}
+
+// Natural logarithm of a row's sum (0: it sees no key) with the maximum `top` taken out, in base 2.
+__device__ __forceinline__ float attn_lse(float top, float sum) {
+  return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: tiles of 16
+//
+// Bound by HBM: 2 (D + 4) bytes per key, used for at most 16 rows.  As in the product for few tokens, each
+// of 8 warps has its own ring: 16 keys of a unit, codes and scales, by cp.async three units ahead (100 KB in flight
+// per SM), and no barrier but the warp's in the loop.  The page of a unit is looked up one
+// unit before its copies start.
+//
+// S = q k^T and o += p v run as mma.sync.m16n8k16 on fp16, the 16 rows as its rows.  q's rows are brought
+// into fp16's range by a power of two each (exact); codes are exact in fp16 (1024 + 128 + code by bits,
+// less 1152).  A thread (g = lane / 4, t = lane % 4) reads 16 codes of key g of each 8 at a time: its
+// operand k of 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are four neighbouring values, the same of q.  For p v it reads 16
+// values (8 for D = 64) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, column g of tile j being value j of the g-th
+// 16: the same keys that its own sums of S are.  So nothing is exchanged between threads but a row's
+// maximum.  Both reads are free of bank conflicts with the 16-byte groups of a key exchanged as below.
+//
+// Scales: a key's multiplies its column of S; a value's its column of p, relative to the largest so far
+// (a power of two, `rv` its reciprocal), so that p stays within fp16.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 16, kFewWarps = 8, kFewStages = 4;
+constexpr int kFewKeys = kAttnUnit / kFewWarps;  // of a warp's stage: 16
+static_assert(kFewKeys == 16, "a page holds a warp's keys");
+
 template <int kD>
-__global__ void __launch_bounds__(256) attn_q8_rows_kernel(const AttnQ8Params p) {
-  constexpr int kE = kD / 32;
+struct FewSmem {
+  static constexpr uint32_t kStage = 2 * kFewKeys * kD + 2 * kFewKeys * 4;  // k, v, their scales
+  static constexpr uint32_t kJoin = kFewWarps * kFewStages * kStage;        // the warps' outputs
+  static constexpr uint32_t kBytes = kJoin + kFewWarps * kFewRows * kD * 4;
+  static_assert(kStage % 128 == 0 && kBytes <= 232448u - 4096u, "shared memory");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The power of two that brings a row with the given largest magnitude to 2^14 .. 2^15 in fp16 (as
+// near as fp32 has one), and its reciprocal.  A NaN or an infinity gives a reciprocal of NaN.
+__device__ __forceinline__ void row_power(float amax, float& up, float& down) {
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+  const int f = min(14 - e, 126);
+  up = __uint_as_float(static_cast<uint32_t>(f + 127) << 23);
+  down = f < 0 || f <= 126 ? __uint_as_float(static_cast<uint32_t>(127 - f) << 23) : 0.f;
+  if (!(amax <= 3.402823466e38f)) {
+    up = 0.f;
+    down = __int_as_float(0x7fffffff);
+  }
+}
+
+// Four codes of a word to fp16, in order
+__device__ __forceinline__ void q8_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = q8_less_1152(__byte_perm(u, 0x64646464u, 0x4140));
+  hi = q8_less_1152(__byte_perm(u, 0x64646464u, 0x4342));
+}
+
+// Where the 16-byte group c of key r of a stage sits, for k and for v (8 groups of 16 bytes are a line
+// of 128; a key is one line, or half of one).  Eight lanes read together: keys g = 0, 1 with groups
+// t = 0..3 of k; keys 0, 2, 4, 6 with groups 0, 1 (halves of them: D = 64) of v.
+template <int kD>
+__device__ __forceinline__ uint32_t few_k_at(uint32_t r, uint32_t c) {
+  if constexpr (kD == 128) return 128u * r + 16u * (c ^ ((r & 1u) << 2));
+  return 128u * (r >> 1) + 16u * (((r & 1u) << 2 | c) ^ ((r >> 1 & 3u) << 1));
+}
+template <int kD>
+__device__ __forceinline__ uint32_t few_v_at(uint32_t r, uint32_t c) {
+  if constexpr (kD == 128) return 128u * r + 16u * (c ^ (r & 6u));
+  return 128u * (r >> 1) + 16u * (((r & 1u) << 2 | c) ^ ((r >> 1 & 3u) << 1));
+}
+
+template <int kD>
+__global__ void __launch_bounds__(32 * kFewWarps, 1)
+    attn_q8_few_kernel(const AttnQ8Params p, const AttnWs ws, const AttnDeal deal) {
+  using Smem = FewSmem<kD>;
+  constexpr int kSteps = kD / 16;   // instructions along D of S
+  constexpr int kTiles = kD / 8;    // tiles of 8 columns of o
+  constexpr int kF4 = kD / 16;      // float4s of a row of o in a thread
+  extern __shared__ __align__(1024) uint8_t smem_few[];
+  __shared__ float2 warp_ml[kFewWarps][kFewRows];
+  __shared__ float2 row_ml[kFewRows];
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int g = lane >> 2, t = lane & 3;
+  const int places = p.batch.width << p.cache.page_log2;
+  const uint32_t ring = smem_u32(smem_few) + static_cast<uint32_t>(warp) * kFewStages * Smem::kStage;
+  float4* const join = reinterpret_cast<float4*>(smem_few + Smem::kJoin);
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (u >= static_cast<int64_t>(p.batch.rows) * p.Hq) return;
-  const int row = static_cast<int>(u / p.Hq), h = static_cast<int>(u % p.Hq), hk = h / p.group;
-  const int b = sequence_of(p.batch, row, lane);
-  if (b >= p.batch.B || row < __ldg(p.batch.cu)) return;
-  // (the first token beyond the table's end makes the row NaN; none after it is walked)
-  const int last = min(__ldg(p.batch.lens + b) - (__ldg(p.batch.cu + b + 1) - row),
-                       p.batch.width << p.cache.page_log2);
-  float q[kE], acc[kE] = {};
+
+  AttnWalk w;
+  int64_t u0, u1;
+  const int64_t total = walk_start<kFewRows, 32 * kFewWarps>(w, p, deal, places, u0, u1);
+  if (threadIdx.x == 0) ws.cut[blockIdx.x].valid = 0;
+  if (u0 >= u1) return;
+  AttnWalk ahead = w;
+  // page of the warp's keys of a unit; -1 also where it has none of them
+  const auto page_at = [&](const AttnWalk& a) {
+    const int key = a.unit * kAttnUnit + warp * kFewKeys;
+    return key < a.extent ? page_of(p.batch, p.cache, a.b, key) : -1;
+  };
+  int page = page_at(ahead);
+  int64_t issued = u0;
+  const auto issue = [&]() {  // the unit `ahead` is at
+    const int key = ahead.unit * kAttnUnit + warp * kFewKeys;
+    if (key < ahead.extent) {
+      const uint32_t st = ring + static_cast<uint32_t>(issued & (kFewStages - 1)) * Smem::kStage;
+      const uint32_t sc = st + 2 * kFewKeys * kD + 4u * lane;  // k's 16 scales, then v's
+      if (page >= 0) {
+        const size_t e = cache_entry(p.cache, page, ahead.hk, key & ((1 << p.cache.page_log2) - 1));
+        constexpr int kGroups = kD / 16;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) q[e] = __bfloat162float(p.q[u * kD + lane * kE + e]) * p.scale_log2;
-  float m = -INFINITY, l = 0.f;
-  int page = -1;
-  for (int j = 0; j <= last; ++j) {
-    const int slot = j & ((1 << p.cache.page_log2) - 1);
-    if (slot == 0) page = page_of(p.batch, p.cache, b, j);
-    float ks = __int_as_float(0x7fffffff), vs = ks;
-    size_t e0 = 0;
-    if (page >= 0) {
-      e0 = cache_entry(p.cache, page, hk, slot);
-      ks = p.cache.k_s[e0];
-      vs = p.cache.v_s[e0];
+        for (int i = 0; i < kFewKeys * kGroups / 32; ++i) {
+          const uint32_t r = (i * 32 + lane) / kGroups, c = lane % kGroups;
+          const size_t at = (e + r) * kD + 16 * c;
+          cp_async16(st + few_k_at<kD>(r, c), p.cache.k_q + at);
+          cp_async16(st + kFewKeys * kD + few_v_at<kD>(r, c), p.cache.v_q + at);
+        }
+        cp_async4(sc, (lane < 16 ? p.cache.k_s : p.cache.v_s) + e + (lane & 15));
+      } else {
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc), "r"(0x7fffffff) : "memory");
+      }
     }
-    float x = 0.f;
+    if (++issued < u1) {
+      walk_on<kFewRows>(ahead, p, deal, places);
+      page = page_at(ahead);
+    }
+  };
 #pragma unroll
-    for (int e = 0; e < kE; ++e)
-      x += q[e] * static_cast<float>(static_cast<int8_t>(p.cache.k_q[e0 * kD + lane * kE + e]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    x *= ks;
-    const float n = fmaxf(m, x), c = exp2f(m - n), w = exp2f(x - n);
-    m = n;
-    l = l * c + w;
-#pragma unroll
-    for (int e = 0; e < kE; ++e)
-      acc[e] = acc[e] * c + w * vs * static_cast<float>(static_cast<int8_t>(p.cache.v_q[e0 * kD + lane * kE + e]));
+  for (int i = 0; i < kFewStages - 1; ++i) {
+    if (issued < u1) issue();
+    cp_async_commit();
   }
+
+  uint32_t qa[kSteps][4];
+  float acc[kTiles][4];
+  float m[2], l[2], rf[2], rv;
+  int limit[2];
+  bool fresh = true;
+  const int64_t item0 = u0 - w.unit;  // first unit of the first item
+  int64_t item = item0;
+  for (int64_t u = u0; u < u1; ++u) {
+    if (issued < u1) issue();
+    cp_async_commit();
+    if (fresh) {  // a new item: its rows of q
+      fresh = false;
+      item = u - w.unit;
+      rv = 0x1p100f;
 #pragma unroll
-  for (int e = 0; e < kE; ++e)
-    p.o[u * kD + lane * kE + e] = __float2bfloat16(last < 0 ? 0.f : acc[e] / l);
-  if (p.lse != nullptr && lane == 0)
-    p.lse[u] = last < 0 ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+      for (int r = 0; r < 2; ++r) {
+        const AttnRow row = attn_row(p, w.s, w.hk, w.tile * kFewRows + g + 8 * r);
+        limit[r] = row.limit;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        Chunk8 c[kSteps / 2];
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSteps / 2; ++i) {
+          c[i] = Chunk8{{0u, 0u, 0u, 0u}};
+          if (row.in) c[i] = ldg8(p.q + row.at * kD + 64 * (i / 2) + 16 * t + 8 * (i % 2));
+          float v[8];
+          unpack8(c[i], v);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) amax = max3_abs_nan(amax, v[e], v[e + 1]);
+        }
+        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        float up, down;
+        row_power(amax, up, down);
+        rf[r] = p.scale_log2 * down;
+#pragma unroll
+        for (int i = 0; i < kSteps / 2; ++i) {
+          float v[8];
+          unpack8(c[i], v);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // two instructions of four values each
+            const float* x = v + 4 * e;
+            qa[2 * i + e][r] = pack_f16x2(x[0] * up, x[1] * up);
+            qa[2 * i + e][2 + r] = pack_f16x2(x[2] * up, x[3] * up);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+    }
+    cp_async_wait<kFewStages - 1>();
+    __syncwarp();
+    const int key = w.unit * kAttnUnit + warp * kFewKeys;
+    if (key < w.extent) {
+      const uint32_t st = ring + static_cast<uint32_t>(u & (kFewStages - 1)) * Smem::kStage;
+      float s[2][4] = {};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < kD / 64; ++h) {
+          const uint4 c = ld_shared_v4(st + few_k_at<kD>(8 * n + g, 4 * h + t));
+          const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0, b1;
+            q8_to_f16x2(word[i], b0, b1);
+            const uint32_t(&a)[4] = qa[4 * h + i];
+            mma_f16_16816(s[n], a[0], a[1], a[2], a[3], b0, b1);
+          }
+        }
+      // keys key + 8 n + 2 t + e: their scales
+      const float* sc = reinterpret_cast<const float*>(
+          smem_few + (st - smem_u32(smem_few)) + 2 * kFewKeys * kD);
+      float ks[2][2], vs[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float2 a = *reinterpret_cast<const float2*>(sc + 8 * n + 2 * t);
+        const float2 b = *reinterpret_cast<const float2*>(sc + 16 + 8 * n + 2 * t);
+        ks[n][0] = a.x, ks[n][1] = a.y;
+        vs[n][0] = b.x, vs[n][1] = b.y;
+      }
+      const bool edge = key + kFewKeys - 1 > w.s.first + static_cast<int>(w.tile * kFewRows / p.group);
+      if (edge) {  // what lies behind the last key is not looked at
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (key + 8 * n + 2 * t + e >= w.extent) vs[n][e] = 0.f;
+      }
+      float vm = fmaxf(fmaxf(fabsf(vs[0][0]), fabsf(vs[0][1])), fmaxf(fabsf(vs[1][0]), fabsf(vs[1][1])));
+      float mx[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = s[n][2 * r + e] * ks[n][e] * rf[r];
+            if (edge && key + 8 * n + 2 * t + e > limit[r]) x = -INFINITY;
+            s[n][2 * r + e] = x;
+          }
+        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+      }
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+      }
+      float less = 1.0f;  // what the outputs so far are multiplied by for the values' scales
+      if (vm * rv > 1.0f) {
+        const float nv = 1.0f / __uint_as_float((__float_as_uint(vm) + 0x7fffffu) & 0x7f800000u);
+        less = nv / rv;
+        rv = nv;
+      }
+      float c[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float n = fmaxf(m[r], mx[r]);
+        const float base = n == -INFINITY ? 0.f : n;  // (no key seen yet)
+        c[r] = ex2(m[r] - base);
+        m[r] = n;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = ex2(s[k][2 * r + e] - base);
+            sum += x;
+            float y = x * (vs[k][e] * rv);
+            if (edge && key + 8 * k + 2 * t + e > limit[r]) y = 0.f;
+            s[k][2 * r + e] = y;
+          }
+        l[r] = fmaf(l[r], c[r], sum);
+        c[r] *= less;
+      }
+      if (__any_sync(0xffffffffu, c[0] != 1.0f || c[1] != 1.0f)) {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] *= c[e >> 1];
+      }
+      const uint32_t a0 = pack_f16x2(s[0][0], s[0][1]), a1 = pack_f16x2(s[0][2], s[0][3]);
+      const uint32_t a2 = pack_f16x2(s[1][0], s[1][1]), a3 = pack_f16x2(s[1][2], s[1][3]);
+      uint32_t v[4][kD / 32];  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: kD / 8 values of each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t r = 8 * (i >> 1) + 2 * t + (i & 1);
+        const uint32_t at = st + kFewKeys * kD;
+        if constexpr (kD == 128) {
+          const uint4 x = ld_shared_v4(at + few_v_at<kD>(r, g));
+          v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+        } else {
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(v[i][0]), "=r"(v[i][1])
+                       : "r"(at + few_v_at<kD>(r, g >> 1) + 8u * (g & 1))
+                       : "memory");
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kD / 32; ++i) {
+        uint32_t b[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = v[2 * h][i] ^ 0x80808080u, y = v[2 * h + 1][i] ^ 0x80808080u;
+          const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
+          b[h][0] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4140));
+          b[h][1] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4342));
+          b[h][2] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4140));
+          b[h][3] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4342));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_f16_16816(acc[4 * i + j], a0, a1, a2, a3, b[0][j], b[1][j]);
+      }
+    }
+    __syncwarp();  // the stage is read: the next unit's copies may take it
+    const bool ends = w.unit == w.units - 1;
+    if (ends || u == u1 - 1) {
+      // The warps' parts meet.
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (t == 0) warp_ml[warp][g + 8 * r] = make_float2(m[r], l[r]);
+      }
+      __syncthreads();
+      const int64_t left = static_cast<int64_t>(w.s.n) * p.group - w.tile * kFewRows;
+      const int rows = static_cast<int>(left < kFewRows ? left : kFewRows);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFewWarps; ++i) top = fmaxf(top, warp_ml[i][g + 8 * r].x);
+        const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int i = 0; i < kFewWarps; ++i) {
+          const float2 x = warp_ml[i][g + 8 * r];
+          sum = fmaf(x.y, ex2(x.x - base), sum);
+        }
+        if (warp == 0 && t == 0) row_ml[g + 8 * r] = make_float2(top, sum);
+        const float f = ex2(m[r] - base) / rv;
+        if (g + 8 * r < rows) {
+#pragma unroll
+          for (int i = 0; i < kF4; ++i) {  // values of the thread's two groups of columns
+            const int half = i / (kF4 / 2), j = 4 * (i % (kF4 / 2));
+            const int e = 2 * r + half;
+            const int at = kF4 * t + (i ^ ((t | (g & 1) << 2) & (kF4 - 1)));
+            join[(warp * kFewRows + g + 8 * r) * (kD / 4) + at] =
+                make_float4(acc[j][e] * f, acc[j + 1][e] * f, acc[j + 2][e] * f, acc[j + 3][e] * f);
+          }
+        }
+      }
+      __syncthreads();
+      const bool whole = ends && item >= u0;
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (item >= u0 ? 1 : 0);
+      for (int i = threadIdx.x; i < rows * (kD / 4); i += 32 * kFewWarps) {
+        const int r = i / (kD / 4), c = i % (kD / 4);
+        const int tt = c / kF4, at = kF4 * tt + ((c % kF4) ^ ((tt | (r & 1) << 2) & (kF4 - 1)));
+        float4 x = join[r * (kD / 4) + at];
+#pragma unroll
+        for (int k = 1; k < kFewWarps; ++k) {
+          const float4 y = join[(k * kFewRows + r) * (kD / 4) + at];
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        const float2 ml = row_ml[r];
+        if (whole) {
+          const AttnRow row = attn_row(p, w.s, w.hk, w.tile * kFewRows + r);
+          const float inv = ml.y == 0.f ? 0.f : 1.0f / ml.y;
+          *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * c) =
+              make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+          if (c == 0 && p.lse != nullptr)
+            p.lse[row.at] = attn_lse(ml.x, ml.y);
+        } else {
+          reinterpret_cast<float4*>(ws.o)[(slot * kFewRows + r) * (kD / 4) + c] = x;
+          if (c == 0) ws.ml[slot * kFewRows + r] = ml;
+        }
+      }
+      if (!ends && item >= u0 && threadIdx.x == 0)
+        ws.cut[blockIdx.x] = AttnCut{total, item + w.units, w.b, w.hk, w.tile, 1, 0};
+      fresh = true;
+    }
+    if (u + 1 < u1) walk_on<kFewRows>(w, p, deal, places);
+  }
+  cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------------------
+// The join of an item's parts: block c has the item whose first part ends block c's share; the parts
+// follow in the next blocks' first slots.
+// ---------------------------------------------------------------------------
+template <int kD, int kRows>
+__global__ void __launch_bounds__(256) attn_q8_join_kernel(const AttnQ8Params p, const AttnWs ws, int blocks) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x;
+  const AttnCut cut = ws.cut[c];
+  if (!cut.valid) return;
+  const AttnSeq s = load_seq(p, cut.b);
+  const int64_t left = static_cast<int64_t>(s.n) * p.group - cut.tile * kRows;
+  const int rows = static_cast<int>(left < kRows ? left : kRows);
+  int last = c + 1;  // the last block with a part
+  while (attn_share(cut.units, last + 1, blocks) < cut.end) ++last;
+  // (a block whose share is empty has none)
+  const auto has = [&](int j) { return attn_share(cut.units, j, blocks) < attn_share(cut.units, j + 1, blocks); };
+  const auto slot = [&](int j) { return static_cast<size_t>(2 * j + (j == c ? 1 : 0)); };
+  for (int i = threadIdx.x; i < rows * (kD / 4); i += 256) {
+    const int r = i / (kD / 4), col = i % (kD / 4);
+    float top = -INFINITY;
+    for (int j = c; j <= last; ++j)
+      if (has(j)) top = fmaxf(top, ws.ml[slot(j) * kRows + r].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = c; j <= last; ++j) {
+      if (!has(j)) continue;
+      const float2 ml = ws.ml[slot(j) * kRows + r];
+      const float4 y = reinterpret_cast<const float4*>(ws.o)[(slot(j) * kRows + r) * (kD / 4) + col];
+      const float f = ex2(ml.x - base);
+      sum = fmaf(ml.y, f, sum);
+      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+    }
+    const AttnRow row = attn_row(p, s, cut.hk, cut.tile * kRows + r);
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * col) =
+        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+    if (col == 0 && p.lse != nullptr)
+      p.lse[row.at] = attn_lse(top, sum);
+  }
 }
 
 }  // namespace coda

@@ -378,6 +378,10 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
                                  MidShape<false>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kProductNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  MidShape<true>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<64>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<128>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kDgradGivenS, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kDgradGivenSSmem) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kPairDgradGivenS, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1240,6 +1244,23 @@ coda_status_t rope_of(const double* inv_freq, const int32_t* axis, int64_t half,
   return CODA_OK;
 }
 
+// Parts of the attention's items: [cuts | maxima and sums | outputs], two parts per block
+size_t attn_ws_bytes(int tile_rows, int64_t D) {
+  return align256(kAttnMaxBlocks * sizeof(AttnCut)) +
+         align256(size_t(2) * kAttnMaxBlocks * tile_rows * sizeof(float2)) +
+         size_t(2) * kAttnMaxBlocks * tile_rows * D * sizeof(float);
+}
+
+AttnWs attn_ws(char* at, int tile_rows, int64_t D) {
+  AttnWs w;
+  w.cut = reinterpret_cast<AttnCut*>(at);
+  at += align256(kAttnMaxBlocks * sizeof(AttnCut));
+  w.ml = reinterpret_cast<float2*>(at);
+  at += align256(size_t(2) * kAttnMaxBlocks * tile_rows * sizeof(float2));
+  w.o = reinterpret_cast<float*>(at);
+  return w;
+}
+
 template <int kD>
 cudaError_t launch_cache_write(const CacheWriteParams& p, const RopeQ8& r, int sms, cudaStream_t stream) {
   const int T = p.batch.rows, heads = p.Hq + 2 * p.cache.Hk;
@@ -2058,7 +2079,7 @@ coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, const int8
 
 size_t coda_attn_q8_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
   if (check_heads(T, B, Hq, Hk, D) != CODA_OK || T == 0 || B == 0) return 0;
-  return kSlotBytes;
+  return kSlotBytes + attn_ws_bytes(kFewRows, D);
 }
 
 coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k_s, const int8_t* v_q,
@@ -2088,13 +2109,22 @@ coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k
   p.Hq = static_cast<int>(Hq);
   p.group = static_cast<int>(Hq / Hk);
   p.scale_log2 = scale * 1.44269504088896f;
-  const cudaError_t e = launch(D == 64 ? &attn_q8_rows_kernel<64> : &attn_q8_rows_kernel<128>,
-                               static_cast<int>(cdiv(T * Hq, 8)), 256, 0, stream, false, p);
+  const int blocks = std::min(sms, kAttnMaxBlocks);
+  char* wsb = static_cast<char*>(workspace) + kSlotBytes;
+  const AttnWs ws = attn_ws(wsb, kFewRows, D);
+  const AttnDeal deal = {0, int64_t(1) << 40};
+  cudaError_t e = launch(D == 64 ? &attn_q8_few_kernel<64> : &attn_q8_few_kernel<128>, blocks, 32 * kFewWarps,
+                         D == 64 ? FewSmem<64>::kBytes : FewSmem<128>::kBytes, stream, false, p, ws, deal);
+  if (e == cudaSuccess) {
+    after_launch(0, stream);
+    e = launch(D == 64 ? &attn_q8_join_kernel<64, kFewRows> : &attn_q8_join_kernel<128, kFewRows>, blocks, 256, 0,
+               stream, false, p, ws, blocks);
+  }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return CODA_ERR_LAUNCH;
   }
-  after_launch(0, stream);
+  after_launch(1, stream);
   return CODA_OK;
 }
 
