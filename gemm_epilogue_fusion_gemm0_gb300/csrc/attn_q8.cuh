@@ -54,10 +54,11 @@ __host__ __device__ inline AttnSeq attn_seq(int cu0, int cu1, int len, int rows)
 
 // Keys that a tile of `tile_rows` packed rows sees at most.  `places`: tokens that the table has room
 // for; a row that sees more is NaN by the first of them that has none, so none after it is walked.
-__host__ __device__ inline int attn_extent(const AttnSeq& s, int group, int tile_rows, int64_t tile,
-                                           int places) {
-  const int64_t end = (tile + 1) * tile_rows, all = static_cast<int64_t>(s.n) * group;
-  const int64_t keys = s.first + ((end < all ? end : all) - 1) / group + 1;
+// (Packed rows and tiles are 32-bit numbers: rows times heads of a call are.)
+__host__ __device__ inline int attn_extent(const AttnSeq& s, int group, int tile_rows, int tile, int places) {
+  const int all = s.n * group, room = all - tile * tile_rows;  // (tile * tile_rows < all)
+  const int last = tile * tile_rows + (room < tile_rows ? room : tile_rows) - 1;
+  const int64_t keys = static_cast<int64_t>(s.first) + last / group + 1;
   return keys <= 0 ? 0 : static_cast<int>(keys < places + 1 ? keys : places + 1);
 }
 
@@ -65,19 +66,17 @@ __host__ __device__ inline int attn_units(int extent) {
   return extent <= kAttnUnit ? 1 : (extent + kAttnUnit - 1) / kAttnUnit;  // (an empty item still writes zeros)
 }
 
-__host__ __device__ inline int64_t attn_tiles(const AttnSeq& s, int group, int tile_rows) {
-  return (static_cast<int64_t>(s.n) * group + tile_rows - 1) / tile_rows;
+__host__ __device__ inline int attn_tiles(const AttnSeq& s, int group, int tile_rows) {
+  return static_cast<int>((static_cast<int64_t>(s.n) * group + tile_rows - 1) / tile_rows);
 }
 
-// Units of a sequence for one key head, where its packed rows number lo + 1 .. hi; else 0.
-__host__ __device__ inline int64_t attn_seq_units(const AttnSeq& s, int group, int tile_rows, int places,
-                                                  int64_t lo, int64_t hi) {
-  const int64_t all = static_cast<int64_t>(s.n) * group;
-  if (all <= lo || all > hi) return 0;
-  int64_t u = 0;
-  const int64_t tiles = attn_tiles(s, group, tile_rows);
-  for (int64_t t = 0; t < tiles; ++t) u += attn_units(attn_extent(s, group, tile_rows, t, places));
-  return u;
+// Which sequences a launch takes: those of lo + 1 .. hi packed rows.
+struct AttnDeal {
+  int lo, hi;
+};
+
+__host__ __device__ inline bool attn_takes(const AttnDeal& d, const AttnSeq& s, int group) {
+  return s.n * group > d.lo && s.n * group <= d.hi;
 }
 
 // First unit of block c's share.
@@ -85,23 +84,17 @@ __host__ __device__ inline int64_t attn_share(int64_t units, int c, int blocks) 
   return units * c / blocks;
 }
 
-// Which sequences a launch takes, and the size of its tiles.
-struct AttnDeal {
-  int64_t lo, hi;  // packed rows of a sequence: lo + 1 .. hi
-};
-
 // An item whose first part is the last of block c's share: what the join needs to know.
 struct AttnCut {
   int64_t units;    // of the launch
   int64_t end;      // one past the item's last unit
-  int b, hk;
-  int64_t tile;
-  int valid, pad;
+  int b, hk, tile;
+  int valid;
 };
 
 struct AttnWs {
   AttnCut* cut;     // [blocks]
-  float2* ml;       // [2 blocks][tile rows]: maximum (of base 2 exponents) and sum
+  float2* ml;       // [2 blocks][tile rows]: what was taken out of the exponents (base 2), and the sum
   float* o;         // [2 blocks][tile rows][D]
 };
 
@@ -113,7 +106,7 @@ __device__ __forceinline__ AttnSeq load_seq(const AttnQ8Params& p, int b) {
 struct AttnWalk {
   AttnSeq s;
   int b, hk;
-  int64_t tile, tiles;
+  int tile, tiles;
   int unit, units, extent;
 };
 
@@ -132,33 +125,49 @@ __device__ __forceinline__ void walk_on(AttnWalk& w, const AttnQ8Params& p, cons
     w.tile = 0;
     if (++w.hk == p.cache.Hk) {
       w.hk = 0;
-      int64_t all;
       do {
         ++w.b;
-        if (w.b >= p.batch.B) return;  // (the end of the last share)
+        if (w.b >= p.batch.B) return;  // (cu or lens written while the call runs)
         w.s = load_seq(p, w.b);
-        all = static_cast<int64_t>(w.s.n) * p.group;
-      } while (all <= d.lo || all > d.hi);
+      } while (!attn_takes(d, w.s, p.group));
       w.tiles = attn_tiles(w.s, p.group, kRows);
     }
   }
   walk_tile<kRows>(w, p, places);
 }
 
+// Units of a sequence for one key head, by a whole warp (0: another launch's sequence).
+template <int kRows>
+__device__ __forceinline__ int64_t seq_units(const AttnSeq& s, const AttnQ8Params& p, const AttnDeal& d,
+                                             int places, int lane) {
+  if (!attn_takes(d, s, p.group)) return 0;
+  const int tiles = attn_tiles(s, p.group, kRows);
+  int64_t u = 0;
+  for (int t = lane; t < tiles; t += 32) u += attn_units(attn_extent(s, p.group, kRows, t, places));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+  return u;
+}
+
 // Adds up the units (all threads of the block, kThreads of them), and puts the walk at unit `u0`
-// of this block's share.  Returns the launch's units; u1 the end of the share.
+// of this block's share, which ends at u1.  Returns the launch's units.  A warp adds up a sequence at a
+// time, a lane a tile; `units` (shared memory, at least B numbers) holds the sequences' sums in between.
 template <int kRows, int kThreads>
-__device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d,
-                                              int places, int64_t& u0, int64_t& u1) {
+__device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places,
+                                              int64_t* units, int64_t& u0, int64_t& u1) {
   __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ int64_t start_rest;
   __shared__ int start_b;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  for (int b = warp; b < p.batch.B; b += kThreads / 32) {
+    const int64_t u = seq_units<kRows>(load_seq(p, b), p, d, places, lane);
+    if (lane == 0) units[b] = u;
+  }
+  __syncthreads();
   const int per = (p.batch.B + kThreads - 1) / kThreads;
   const int b0 = min(p.batch.B, tid * per), b1 = min(p.batch.B, b0 + per);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b)
-    mine += attn_seq_units(load_seq(p, b), p.group, kRows, places, d.lo, d.hi) * p.cache.Hk;
+  for (int b = b0; b < b1; ++b) mine += units[b] * p.cache.Hk;
   int64_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -178,12 +187,7 @@ __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p
   if (u0 < u1 && upto - mine <= u0 && u0 < upto) {  // one thread: u0 is in its sequences
     int64_t rest = u0 - (upto - mine);
     int b = b0;
-    while (true) {
-      const int64_t u = attn_seq_units(load_seq(p, b), p.group, kRows, places, d.lo, d.hi) * p.cache.Hk;
-      if (rest < u) break;
-      rest -= u;
-      ++b;
-    }
+    for (; rest >= units[b] * p.cache.Hk; ++b) rest -= units[b] * p.cache.Hk;
     start_b = b;
     start_rest = rest;
   }
@@ -193,33 +197,47 @@ __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p
   w.s = load_seq(p, w.b);
   w.tiles = attn_tiles(w.s, p.group, kRows);
   int64_t rest = start_rest;
-  const int64_t per_head = attn_seq_units(w.s, p.group, kRows, places, d.lo, d.hi);
+  const int64_t per_head = units[w.b];
   w.hk = static_cast<int>(rest / per_head);
   rest -= w.hk * per_head;
-  for (w.tile = 0;; ++w.tile) {
-    walk_tile<kRows>(w, p, places);
-    if (rest < w.units) break;
-    rest -= w.units;
+  for (w.tile = 0;; w.tile += 32) {  // 32 tiles at a time
+    const int t = w.tile + lane;
+    const int u = t < w.tiles ? attn_units(attn_extent(w.s, p.group, kRows, t, places)) : 0;
+    int64_t before = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, rest < before);
+    if (here != 0u || w.tile + 32 >= w.tiles) {
+      const int at = here != 0u ? __ffs(here) - 1 : 31;
+      rest -= __shfl_sync(0xffffffffu, before - u, at);
+      w.tile += at;
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, before, 31);
   }
+  walk_tile<kRows>(w, p, places);
   w.unit = static_cast<int>(rest);
+  __syncthreads();  // `units` is read: its memory is free
   return total;
 }
 
-// Row r of a tile: its row of q and its query head.  False behind the sequence's last.
+// Row `packed` of a sequence's rows that share a key head: its row of q and its query head.
 struct AttnRow {
   int64_t at;  // row * Hq + head
   int limit;   // the last key that it sees
-  bool in;
+  bool in;     // false behind the sequence's last (`at` and `limit` are then the last's)
 };
 
-__device__ __forceinline__ AttnRow attn_row(const AttnQ8Params& p, const AttnSeq& s, int hk, int64_t packed) {
+__device__ __forceinline__ AttnRow attn_row(const AttnQ8Params& p, const AttnSeq& s, int hk, int packed) {
   AttnRow r;
-  const int64_t all = static_cast<int64_t>(s.n) * p.group;
+  const int all = s.n * p.group;
   r.in = packed < all;
-  const int64_t i = (r.in ? packed : all - 1) / p.group;
-  const int g = static_cast<int>((r.in ? packed : all - 1) - i * p.group);
-  r.limit = s.first + static_cast<int>(i);
-  r.at = (s.row0 + i) * p.Hq + static_cast<int64_t>(hk) * p.group + g;
+  const int i = (r.in ? packed : all - 1) / p.group;
+  r.limit = s.first + i;
+  r.at = static_cast<int64_t>(s.row0 + i) * p.Hq + hk * p.group + ((r.in ? packed : all - 1) - i * p.group);
   return r;
 }
 
@@ -244,8 +262,9 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 // 16: the same keys that its own sums of S are.  So nothing is exchanged between threads but a row's
 // maximum.  Both reads are free of bank conflicts with the 16-byte groups of a key exchanged as below.
 //
-// Scales: a key's multiplies its column of S; a value's its column of p, relative to the largest so far
-// (a power of two, `rv` its reciprocal), so that p stays within fp16.
+// Scales: a key's multiplies its column of S; a value's its column of p.  So that their product stays
+// within fp16, what is taken out of the exponents is not the largest score m alone but m + log2 of
+// the largest value scale so far (rounded up to a power of two): the sums and outputs share it.
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 16, kFewWarps = 8, kFewStages = 4;
 constexpr int kFewKeys = kAttnUnit / kFewWarps;  // of a warp's stage: 16
@@ -296,6 +315,13 @@ __device__ __forceinline__ void row_power(float amax, float& up, float& down) {
   }
 }
 
+// log2 of the power of two that a value scale is at most (2^-60 for smaller ones, a NaN among them)
+constexpr float kLeastScale = -60.f;
+__device__ __forceinline__ float scale_power(float s) {
+  return s > 0x1p-60f ? static_cast<float>(static_cast<int>((__float_as_uint(s) + 0x7fffffu) >> 23) - 127)
+                      : kLeastScale;
+}
+
 // Four codes of a word to fp16, in order
 __device__ __forceinline__ void q8_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = w ^ 0x80808080u;
@@ -338,7 +364,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
 
   AttnWalk w;
   int64_t u0, u1;
-  const int64_t total = walk_start<kFewRows, 32 * kFewWarps>(w, p, deal, places, u0, u1);
+  const int64_t total = walk_start<kFewRows, 32 * kFewWarps>(
+      w, p, deal, places, reinterpret_cast<int64_t*>(smem_few), u0, u1);
   if (threadIdx.x == 0) ws.cut[blockIdx.x].valid = 0;
   if (u0 >= u1) return;
   AttnWalk ahead = w;
@@ -382,23 +409,22 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
 
   uint32_t qa[kSteps][4];
   float acc[kTiles][4];
-  float m[2], l[2], rf[2], rv;
+  float m[2], l[2], rf[2], base[2], lv;
   int limit[2];
   bool fresh = true;
-  const int64_t item0 = u0 - w.unit;  // first unit of the first item
-  int64_t item = item0;
+  int64_t item = 0;  // its first unit
   for (int64_t u = u0; u < u1; ++u) {
     if (issued < u1) issue();
     cp_async_commit();
     if (fresh) {  // a new item: its rows of q
       fresh = false;
       item = u - w.unit;
-      rv = 0x1p100f;
+      lv = kLeastScale;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const AttnRow row = attn_row(p, w.s, w.hk, w.tile * kFewRows + g + 8 * r);
         limit[r] = row.limit;
-        m[r] = -INFINITY;
+        m[r] = base[r] = -INFINITY;
         l[r] = 0.f;
         Chunk8 c[kSteps / 2];
         float amax = 0.f;
@@ -464,7 +490,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         ks[n][0] = a.x, ks[n][1] = a.y;
         vs[n][0] = b.x, vs[n][1] = b.y;
       }
-      const bool edge = key + kFewKeys - 1 > w.s.first + static_cast<int>(w.tile * kFewRows / p.group);
+      const bool edge = key + kFewKeys - 1 > w.s.first + w.tile * kFewRows / p.group;
       if (edge) {  // what lies behind the last key is not looked at
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -492,32 +518,29 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
         mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
       }
-      float less = 1.0f;  // what the outputs so far are multiplied by for the values' scales
-      if (vm * rv > 1.0f) {
-        const float nv = 1.0f / __uint_as_float((__float_as_uint(vm) + 0x7fffffu) & 0x7f800000u);
-        less = nv / rv;
-        rv = nv;
-      }
+      lv = fmaxf(lv, scale_power(vm));
       float c[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float n = fmaxf(m[r], mx[r]);
-        const float base = n == -INFINITY ? 0.f : n;  // (no key seen yet)
-        c[r] = ex2(m[r] - base);
-        m[r] = n;
+        m[r] = fmaxf(m[r], mx[r]);
+        c[r] = 1.0f;
+        if (m[r] + lv > base[r]) {
+          c[r] = ex2(base[r] - (m[r] + lv));
+          base[r] = m[r] + lv;
+        }
+        const float less = base[r] == -INFINITY ? 0.f : base[r];  // (no key seen yet)
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float x = ex2(s[k][2 * r + e] - base);
+            const float x = ex2(s[k][2 * r + e] - less);
             sum += x;
-            float y = x * (vs[k][e] * rv);
+            float y = x * vs[k][e];
             if (edge && key + 8 * k + 2 * t + e > limit[r]) y = 0.f;
             s[k][2 * r + e] = y;
           }
         l[r] = fmaf(l[r], c[r], sum);
-        c[r] *= less;
       }
       if (__any_sync(0xffffffffu, c[0] != 1.0f || c[1] != 1.0f)) {
 #pragma unroll
@@ -566,24 +589,23 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
       for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (t == 0) warp_ml[warp][g + 8 * r] = make_float2(m[r], l[r]);
+        if (t == 0) warp_ml[warp][g + 8 * r] = make_float2(base[r], l[r]);
       }
       __syncthreads();
-      const int64_t left = static_cast<int64_t>(w.s.n) * p.group - w.tile * kFewRows;
-      const int rows = static_cast<int>(left < kFewRows ? left : kFewRows);
+      const int rows = min(kFewRows, w.s.n * p.group - w.tile * kFewRows);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int i = 0; i < kFewWarps; ++i) top = fmaxf(top, warp_ml[i][g + 8 * r].x);
-        const float base = top == -INFINITY ? 0.f : top;
+        const float less = top == -INFINITY ? 0.f : top;
 #pragma unroll
         for (int i = 0; i < kFewWarps; ++i) {
           const float2 x = warp_ml[i][g + 8 * r];
-          sum = fmaf(x.y, ex2(x.x - base), sum);
+          sum = fmaf(x.y, ex2(x.x - less), sum);
         }
         if (warp == 0 && t == 0) row_ml[g + 8 * r] = make_float2(top, sum);
-        const float f = ex2(m[r] - base) / rv;
+        const float f = ex2(base[r] - less);
         if (g + 8 * r < rows) {
 #pragma unroll
           for (int i = 0; i < kF4; ++i) {  // values of the thread's two groups of columns
@@ -621,7 +643,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         }
       }
       if (!ends && item >= u0 && threadIdx.x == 0)
-        ws.cut[blockIdx.x] = AttnCut{total, item + w.units, w.b, w.hk, w.tile, 1, 0};
+        ws.cut[blockIdx.x] = AttnCut{total, item + w.units, w.b, w.hk, w.tile, 1};
       fresh = true;
     }
     if (u + 1 < u1) walk_on<kFewRows>(w, p, deal, places);
@@ -641,8 +663,7 @@ __global__ void __launch_bounds__(256) attn_q8_join_kernel(const AttnQ8Params p,
   const AttnCut cut = ws.cut[c];
   if (!cut.valid) return;
   const AttnSeq s = load_seq(p, cut.b);
-  const int64_t left = static_cast<int64_t>(s.n) * p.group - cut.tile * kRows;
-  const int rows = static_cast<int>(left < kRows ? left : kRows);
+  const int rows = min(kRows, s.n * p.group - cut.tile * kRows);
   int last = c + 1;  // the last block with a part
   while (attn_share(cut.units, last + 1, blocks) < cut.end) ++last;
   // (a block whose share is empty has none)

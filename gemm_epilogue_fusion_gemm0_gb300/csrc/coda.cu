@@ -25,6 +25,7 @@
 
 #include "coda.h"
 #include "attn_q8.cuh"
+#include "attn_q8_tile.cuh"
 #include "cache_q8.cuh"
 #include "epilogues.cuh"
 #include "gemm_pair.cuh"
@@ -378,6 +379,10 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
                                  MidShape<false>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kProductNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  MidShape<true>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(&attn_q8_tile_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 TileSmem<64>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(&attn_q8_tile_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 TileSmem<128>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  FewSmem<64>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1171,6 +1176,7 @@ cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t*
 // ---------------------------------------------------------------------------
 // The 8-bit paged cache (cache_q8.cuh, attn_q8.cuh)
 // ---------------------------------------------------------------------------
+constexpr int kFewMost = 32;  // packed rows of a sequence that go to the kernel for few
 constexpr int64_t kMaxSequences = 8192, kMaxHeads = 1024;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -1178,7 +1184,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 coda_status_t check_heads(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
   if (T < 0 || B < 0 || Hq <= 0 || Hk <= 0 || D <= 0) return CODA_ERR_INVALID_ARG;
   const int64_t lim = (int64_t(1) << 31) - 256;
-  if ((D != 64 && D != 128) || Hq % Hk != 0 || Hq > kMaxHeads || B > kMaxSequences || T > lim ||
+  if ((D != 64 && D != 128) || Hq % Hk != 0 || Hq > kMaxHeads || B > kMaxSequences || T > lim / Hq ||
       !fits(T, (Hq + 2 * Hk) * D))
     return CODA_ERR_UNSUPPORTED_SHAPE;
   return CODA_OK;
@@ -1259,6 +1265,34 @@ AttnWs attn_ws(char* at, int tile_rows, int64_t D) {
   at += align256(size_t(2) * kAttnMaxBlocks * tile_rows * sizeof(float2));
   w.o = reinterpret_cast<float*>(at);
   return w;
+}
+
+// Sequences of up to kFewMost packed rows go to the kernel for few, the others to the one for tiles, each with
+// its own share of the blocks and its join; without a hint of `rows` (the most of a sequence) both
+// run, and one of them may find nothing.  If a sequence has more rows than the hint says, the kernel for
+// few takes it.
+template <int kD>
+cudaError_t launch_attn(const AttnQ8Params& p, char* at, int64_t rows, int blocks, cudaStream_t stream) {
+  const bool tiles = rows > kFewMost;
+  int k = 0;
+  AttnWs ws = attn_ws(at, kFewRows, kD);
+  cudaError_t e = launch(&attn_q8_few_kernel<kD>, blocks, 32 * kFewWarps, FewSmem<kD>::kBytes, stream, false, p, ws,
+                         AttnDeal{0, tiles ? kFewMost : 0x7fffffff});
+  if (e == cudaSuccess) {
+    after_launch(k++, stream);
+    e = launch(&attn_q8_join_kernel<kD, kFewRows>, blocks, 256, 0, stream, false, p, ws, blocks);
+  }
+  if (e == cudaSuccess) after_launch(k++, stream);
+  if (e != cudaSuccess || !tiles) return e;
+  ws = attn_ws(at, kTileRows, kD);
+  e = launch(&attn_q8_tile_kernel<kD>, blocks, kTileThreads, TileSmem<kD>::kBytes, stream, false, p, ws,
+             AttnDeal{kFewMost, 0x7fffffff}, g_timeout_ns.load());
+  if (e == cudaSuccess) {
+    after_launch(k++, stream);
+    e = launch(&attn_q8_join_kernel<kD, kTileRows>, blocks, 256, 0, stream, false, p, ws, blocks);
+  }
+  if (e == cudaSuccess) after_launch(k++, stream);
+  return e;
 }
 
 template <int kD>
@@ -2079,7 +2113,7 @@ coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, const int8
 
 size_t coda_attn_q8_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
   if (check_heads(T, B, Hq, Hk, D) != CODA_OK || T == 0 || B == 0) return 0;
-  return kSlotBytes + attn_ws_bytes(kFewRows, D);
+  return kSlotBytes + attn_ws_bytes(T * (Hq / Hk) > kFewMost ? kTileRows : kFewRows, D);
 }
 
 coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k_s, const int8_t* v_q,
@@ -2110,21 +2144,15 @@ coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k
   p.group = static_cast<int>(Hq / Hk);
   p.scale_log2 = scale * 1.44269504088896f;
   const int blocks = std::min(sms, kAttnMaxBlocks);
-  char* wsb = static_cast<char*>(workspace) + kSlotBytes;
-  const AttnWs ws = attn_ws(wsb, kFewRows, D);
-  const AttnDeal deal = {0, int64_t(1) << 40};
-  cudaError_t e = launch(D == 64 ? &attn_q8_few_kernel<64> : &attn_q8_few_kernel<128>, blocks, 32 * kFewWarps,
-                         D == 64 ? FewSmem<64>::kBytes : FewSmem<128>::kBytes, stream, false, p, ws, deal);
-  if (e == cudaSuccess) {
-    after_launch(0, stream);
-    e = launch(D == 64 ? &attn_q8_join_kernel<64, kFewRows> : &attn_q8_join_kernel<128, kFewRows>, blocks, 256, 0,
-               stream, false, p, ws, blocks);
-  }
+  char* const wsb = static_cast<char*>(workspace) + kSlotBytes;
+  // the most packed rows that a sequence may have
+  const int64_t rows = std::min(most > 0 ? most : T, T) * p.group;
+  const cudaError_t e = D == 64 ? launch_attn<64>(p, wsb, rows, blocks, stream)
+                                : launch_attn<128>(p, wsb, rows, blocks, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return CODA_ERR_LAUNCH;
   }
-  after_launch(1, stream);
   return CODA_OK;
 }
 

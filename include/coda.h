@@ -405,7 +405,7 @@ CODA_API coda_status_t coda_bwd_swiglu_dgrad_q8(const coda_bf16* dout, const cod
  * never touched: coda_cache_write_q8 writes nothing there, coda_cache_read_q8 gives NaN, every row of
  * coda_attn_q8 that sees such a token is NaN, and coda_get_device_status reports
  * CODA_ERR_DEVICE_BOUNDS (detail 0x240).
- * B at most 8192; Hq a multiple of Hk, both at most 1024; Hq = group * Hk, query head h reads
+ * B at most 8192; Hq a multiple of Hk, both at most 1024, T * Hq below 2^31; Hq = group * Hk, query head h reads
  * key head h / group.  cu, lens, table and pos need 4-byte alignment only.  T = 0 or B = 0: nothing is
  * launched.
  * ------------------------------------------------------------------------- */
