@@ -116,10 +116,9 @@ __device__ __forceinline__ void walk_tile(AttnWalk& w, const AttnQ8Params& p, in
   w.units = attn_units(w.extent);
 }
 
-// The next unit (there is one).
+// The next item (there is one), its first unit.
 template <int kRows>
-__device__ __forceinline__ void walk_on(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
-  if (++w.unit < w.units) return;
+__device__ __forceinline__ void walk_item(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
   w.unit = 0;
   if (++w.tile == w.tiles) {
     w.tile = 0;
@@ -134,6 +133,12 @@ __device__ __forceinline__ void walk_on(AttnWalk& w, const AttnQ8Params& p, cons
     }
   }
   walk_tile<kRows>(w, p, places);
+}
+
+// The next unit (there is one).
+template <int kRows>
+__device__ __forceinline__ void walk_on(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
+  if (++w.unit == w.units) walk_item<kRows>(w, p, d, places);
 }
 
 // Units of a sequence for one key head, by a whole warp (0: another launch's sequence).
@@ -652,45 +657,69 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The join of an item's parts: block c has the item whose first part ends block c's share; the parts
-// follow in the next blocks' first slots.
+// The join of an item's parts: block (c, y) has rows 16 y .. 16 y + 15 of the item whose first part ends
+// block c's share; the parts follow in the next blocks' first slots.  The parts' weights are formed once,
+// then a thread adds four columns of a row over the parts, in order.
 // ---------------------------------------------------------------------------
 template <int kD, int kRows>
 __global__ void __launch_bounds__(256) attn_q8_join_kernel(const AttnQ8Params p, const AttnWs ws, int blocks) {
+  constexpr int kGroup = 16;
+  __shared__ float weight[kAttnMaxBlocks][kGroup];
+  __shared__ int slots[kAttnMaxBlocks];
+  __shared__ float2 row_ml[kGroup];
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, tid = static_cast<int>(threadIdx.x);
   const AttnCut cut = ws.cut[c];
   if (!cut.valid) return;
   const AttnSeq s = load_seq(p, cut.b);
-  const int rows = min(kRows, s.n * p.group - cut.tile * kRows);
-  int last = c + 1;  // the last block with a part
-  while (attn_share(cut.units, last + 1, blocks) < cut.end) ++last;
-  // (a block whose share is empty has none)
-  const auto has = [&](int j) { return attn_share(cut.units, j, blocks) < attn_share(cut.units, j + 1, blocks); };
-  const auto slot = [&](int j) { return static_cast<size_t>(2 * j + (j == c ? 1 : 0)); };
-  for (int i = threadIdx.x; i < rows * (kD / 4); i += 256) {
+  const int r0 = static_cast<int>(blockIdx.y) * kGroup;
+  const int rows = min(kGroup, s.n * p.group - cut.tile * kRows - r0);
+  if (rows <= 0) return;
+  // blocks c .. c + parts - 1; one whose share is empty (fewer units than blocks) has no part
+  const int parts = static_cast<int>((cut.end * blocks + cut.units - 1) / cut.units) - c;
+  for (int j = tid; j < parts; j += 256) {
+    const bool has = attn_share(cut.units, c + j, blocks) < attn_share(cut.units, c + j + 1, blocks);
+    slots[j] = has ? 2 * (c + j) + (j == 0 ? 1 : 0) : -1;
+  }
+  __syncthreads();
+  {  // a half warp per row
+    const int r = tid >> 4, l = tid & 15;
+    float top = -INFINITY, sum = 0.f;
+    for (int j = l; j < parts; j += 16)
+      if (slots[j] >= 0 && r < rows) top = fmaxf(top, ws.ml[slots[j] * kRows + r0 + r].x);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float less = top == -INFINITY ? 0.f : top;
+    for (int j = l; j < parts; j += 16)
+      if (slots[j] >= 0 && r < rows) {
+        const float2 ml = ws.ml[slots[j] * kRows + r0 + r];
+        const float f = ex2(ml.x - less);
+        weight[j][r] = f;
+        sum = fmaf(ml.y, f, sum);
+      }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (l == 0) row_ml[r] = make_float2(top, sum);
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * (kD / 4); i += 256) {
     const int r = i / (kD / 4), col = i % (kD / 4);
-    float top = -INFINITY;
-    for (int j = c; j <= last; ++j)
-      if (has(j)) top = fmaxf(top, ws.ml[slot(j) * kRows + r].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
+    const float4* const part = reinterpret_cast<const float4*>(ws.o) + static_cast<size_t>(r0 + r) * (kD / 4) + col;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = c; j <= last; ++j) {
-      if (!has(j)) continue;
-      const float2 ml = ws.ml[slot(j) * kRows + r];
-      const float4 y = reinterpret_cast<const float4*>(ws.o)[(slot(j) * kRows + r) * (kD / 4) + col];
-      const float f = ex2(ml.x - base);
-      sum = fmaf(ml.y, f, sum);
+#pragma unroll 8
+    for (int j = 0; j < parts; ++j) {
+      if (slots[j] < 0) continue;
+      const float4 y = part[static_cast<size_t>(slots[j]) * kRows * (kD / 4)];
+      const float f = weight[j][r];
       x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
     }
-    const AttnRow row = attn_row(p, s, cut.hk, cut.tile * kRows + r);
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    const float2 ml = row_ml[r];
+    const AttnRow row = attn_row(p, s, cut.hk, cut.tile * kRows + r0 + r);
+    const float inv = ml.y == 0.f ? 0.f : 1.0f / ml.y;
     *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * col) =
         make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-    if (col == 0 && p.lse != nullptr)
-      p.lse[row.at] = attn_lse(top, sum);
+    if (col == 0 && p.lse != nullptr) p.lse[row.at] = attn_lse(ml.x, ml.y);
   }
 }
 

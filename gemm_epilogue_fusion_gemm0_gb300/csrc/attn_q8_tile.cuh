@@ -85,6 +85,97 @@ __device__ __forceinline__ uint32_t panel_at(uint32_t row, uint32_t c) {
   return (c >> 3) * 16384u + row * 128u + (((c & 7u) ^ (row & 7u)) << 4);
 }
 
+// The softmax's two walks over a row of S, 32 columns at a time with the next 32 on their way; `va` holds
+// the first 32 between them.  `ts`: the thread's lane of S.  `sc`: k's 128 scales, then v's.
+// kEdge: the row sees columns 0 .. seen only.
+template <bool kEdge>
+__device__ __forceinline__ void largest_of_32(const uint32_t (&v)[32], const float* sc, int seen, float& mx) {
+  float m0 = mx, m1 = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 k4 = *reinterpret_cast<const float4*>(sc + e);
+    float x[4];
+    unpack2(mul2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pack2(k4.x, k4.y)), x[0], x[1]);
+    unpack2(mul2(pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), pack2(k4.z, k4.w)), x[2], x[3]);
+    if constexpr (kEdge) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        if (e + f > seen) x[f] = -INFINITY;
+    }
+    m0 = max3(m0, x[0], x[1]);
+    m1 = max3(m1, x[2], x[3]);
+  }
+  mx = fmaxf(m0, m1);
+}
+
+template <bool kEdge>
+__device__ __forceinline__ void largest_score(uint32_t ts, const float* sc, int seen, uint32_t (&va)[32],
+                                              uint32_t (&vb)[32], float& mx) {
+  tmem_ld32(ts, va);
+  tmem_ld_wait(va);
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 64) {
+    tmem_ld32(ts + c + 32, vb);
+    largest_of_32<kEdge>(va, sc + c, seen - c, mx);
+    tmem_ld_wait(vb);
+    tmem_ld32(ts + (c + 64) % 128, va);
+    largest_of_32<kEdge>(vb, sc + c + 32, seen - c - 32, mx);
+    tmem_ld_wait(va);
+  }
+}
+
+// P = 2^(S k's scale rf - less) v's scale of 32 columns, in fp16 to tensor memory at `to`; the sum without v's.
+template <bool kEdge>
+__device__ __forceinline__ void weights_of_32(const uint32_t (&v)[32], const float* sc, int seen, uint64_t rf2,
+                                              uint64_t less2, uint32_t to, uint64_t& sum2) {
+  uint32_t pk[16];
+  uint64_t sum[2] = {sum2, 0};
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 k4 = *reinterpret_cast<const float4*>(sc + e);
+    const float4 v4 = *reinterpret_cast<const float4*>(sc + 128 + e);
+    const uint64_t kk[2] = {pack2(k4.x, k4.y), pack2(k4.z, k4.w)};
+    const uint64_t vv[2] = {pack2(v4.x, v4.y), pack2(v4.z, v4.w)};
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int at = e + 2 * f;
+      const uint64_t x = mul2(pack2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), kk[f]);
+      float a, b;
+      unpack2(fma2(x, rf2, less2), a, b);
+      a = ex2(a);
+      b = ex2(b);
+      if constexpr (kEdge) {
+        if (at > seen) a = 0.f;
+        if (at + 1 > seen) b = 0.f;
+      }
+      const uint64_t y = pack2(a, b);
+      sum[f] = add2(sum[f], y);
+      unpack2(mul2(y, vv[f]), a, b);
+      if constexpr (kEdge) {  // (a scale behind the row's last key may be NaN)
+        if (at > seen) a = 0.f;
+        if (at + 1 > seen) b = 0.f;
+      }
+      pk[at / 2] = pack_f16x2(a, b);
+    }
+  }
+  sum2 = add2(sum[0], sum[1]);
+  tmem_st16(to, pk);  // (over columns of S that have been read)
+}
+
+template <bool kEdge>
+__device__ __forceinline__ void weights(uint32_t ts, const float* sc, int seen, uint64_t rf2, uint64_t less2,
+                                        uint32_t (&va)[32], uint32_t (&vb)[32], uint64_t& sum2) {
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 64) {
+    tmem_ld32(ts + c + 32, vb);
+    weights_of_32<kEdge>(va, sc + c, seen - c, rf2, less2, ts + c / 2, sum2);
+    tmem_ld_wait(vb);
+    if (c == 0) tmem_ld32(ts + 64, va);
+    weights_of_32<kEdge>(vb, sc + c + 32, seen - c - 32, rf2, less2, ts + c / 2 + 16, sum2);
+    tmem_ld_wait(va);
+  }
+}
+
 template <int kD>
 __global__ void __launch_bounds__(kTileThreads, 1)
     attn_q8_tile_kernel(const AttnQ8Params p, const AttnWs ws, const AttnDeal deal, uint64_t timeout_ns) {
@@ -152,24 +243,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Smem::kEnd);
-  const int64_t count = u1 - u0;
+  const uint32_t count = static_cast<uint32_t>(u1 - u0);
 
   if (warp >= 8 && warp < 12) {
     // ------------------------------------------------------------- widening
     constexpr int kGroups = kD / 16;          // 16 codes each
     constexpr int kPer = 128 * kGroups / 128;  // of a thread and tensor
     const int pt = tid - 256;
-    const uint32_t c = pt % kGroups, r0 = pt / kGroups;  // its rows: r0 + i * 128 / kGroups
+    // Its 16 codes c of the rows r0 + i * 128 / kGroups.  The eight threads that write together have four
+    // neighbouring groups of two rows: with the swizzle, 128 bytes without a bank twice.
+    const uint32_t c = (pt & 3) + (kD == 128 ? 4 * ((pt >> 5) & 1) : 0);
+    const uint32_t r0 = kD == 128 ? ((pt >> 2) & 7) + 8 * (pt >> 6) : pt >> 2;
     uint4 kr[kPer], vr[kPer];
     float ks = 0.f, vs = 0.f;
-    AttnWalk ahead = w;
-    // pages of the 8 groups of 16 keys of a unit, one per lane 0..7
+    // pages of the 8 groups of 16 keys of a unit, one per lane 0..7: looked up a unit before its loads
     const auto pages_at = [&](const AttnWalk& a) {
       const int key = a.unit * kAttnUnit + 16 * (lane & 7);
       return key < a.extent ? page_of(p.batch, p.cache, a.b, key) : -1;
     };
-    int pages = pages_at(ahead);
     const int mask = (1 << p.cache.page_log2) - 1;
+    int pages = pages_at(w), pages_next = -1, key0 = 0, extent = 0, hk = 0;  // of the unit that is loaded
+    uint32_t walked = 0;
+    const auto next = [&]() {  // takes over the unit that `w` is at, and moves w to the one behind it
+      key0 = w.unit * kAttnUnit;
+      extent = w.extent;
+      hk = w.hk;
+      if (++walked < count) {
+        walk_on<kTileRows>(w, p, deal, places);
+        pages_next = pages_at(w);
+      }
+    };
+    next();
     const auto load = [&](const uint8_t* q, uint4 (&to)[kPer]) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -177,17 +281,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
         to[i] = make_uint4(0u, 0u, 0u, 0u);
         if (page >= 0) {
-          const int key = ahead.unit * kAttnUnit + r;
-          const size_t e = cache_entry(p.cache, page, ahead.hk, key & mask);
+          const size_t e = cache_entry(p.cache, page, hk, (key0 + r) & mask);
           to[i] = *reinterpret_cast<const uint4*>(q + e * kD + 16 * c);
         }
       }
     };
     const auto load_scales = [&]() {
-      const int page = __shfl_sync(0xffffffffu, pages, pt >> 4), key = ahead.unit * kAttnUnit + pt;
-      ks = vs = key < ahead.extent ? __int_as_float(0x7fffffff) : 0.f;  // a page that does not exist: NaN
-      if (page >= 0 && key < ahead.extent) {
-        const size_t e = cache_entry(p.cache, page, ahead.hk, key & mask);
+      const int page = __shfl_sync(0xffffffffu, pages, pt >> 4), key = key0 + pt;
+      ks = vs = key < extent ? __int_as_float(0x7fffffff) : 0.f;  // a page that does not exist: NaN
+      if (page >= 0 && key < extent) {
+        const size_t e = cache_entry(p.cache, page, hk, key & mask);
         ks = p.cache.k_s[e];
         vs = p.cache.v_s[e];
       }
@@ -201,40 +304,34 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         q8_to_f16x2(from[i].y, x[2], x[3]);
         q8_to_f16x2(from[i].z, x[4], x[5]);
         q8_to_f16x2(from[i].w, x[6], x[7]);
-        // the upper half of a row's groups the other way around: the eight threads that write together
-        // then fill 128 bytes of both panels
-        const bool swap = (c & 4u) != 0u;
-        const uint32_t a = to + panel_at(r, 2 * c + (swap ? 1 : 0)), b = to + panel_at(r, 2 * c + (swap ? 0 : 1));
-        st_shared_v4(a, swap ? x[4] : x[0], swap ? x[5] : x[1], swap ? x[6] : x[2], swap ? x[7] : x[3]);
-        st_shared_v4(b, swap ? x[0] : x[4], swap ? x[1] : x[5], swap ? x[2] : x[6], swap ? x[3] : x[7]);
+        st_shared_v4(to + panel_at(r, 2 * c), x[0], x[1], x[2], x[3]);
+        st_shared_v4(to + panel_at(r, 2 * c + 1), x[4], x[5], x[6], x[7]);
       }
     };
     load_scales();
     load(p.cache.k_q, kr);
     load(p.cache.v_q, vr);
-    for (int64_t i = 0; i < count; ++i) {
-      const uint32_t st = static_cast<uint32_t>(i) % kTileStages, ph = static_cast<uint32_t>(i) / kTileStages & 1u;
-      const uint32_t sl = static_cast<uint32_t>(i) % kTileScales, sph = static_cast<uint32_t>(i) / kTileScales & 1u;
+    for (uint32_t i = 0; i < count; ++i) {
+      const uint32_t st = i % kTileStages, ph = i / kTileStages & 1u;
+      const uint32_t sl = i % kTileScales, sph = i / kTileScales & 1u;
       if (!warp_wait(sc_empty(sl), sph ^ 1u, kSiteAttn)) break;
       float* const sc = reinterpret_cast<float*>(smem + Smem::kScale + sl * Smem::kScaleSlot);
       sc[pt] = ks;
       sc[128 + pt] = vs;
       const uint32_t vbits = fabsf(vs) <= 3.402823466e38f ? __float_as_uint(fabsf(vs)) : 0u;
       const uint32_t vmax = __reduce_max_sync(0xffffffffu, vbits);
-      if (lane == 0) {
-        sc[256 + warp - 8] = __uint_as_float(vmax);
-      }
+      if (lane == 0) sc[256 + warp - 8] = __uint_as_float(vmax);
       __syncwarp();
       if (lane == 0) mbar_arrive(sc_full(sl));
-      const bool more = i + 1 < count;
       if (!warp_wait(k_empty(st), ph ^ 1u, kSiteAttn + 1)) break;
       widen(kr, base + Smem::kK + st * Smem::kOperand);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full(st));
+      const bool more = i + 1 < count;
       if (more) {
-        walk_on<kTileRows>(ahead, p, deal, places);
-        pages = pages_at(ahead);
+        pages = pages_next;
+        next();
         load_scales();
         load(p.cache.k_q, kr);
       }
@@ -273,43 +370,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc_fence_after();
       return ok;
     };
-    bool ok = true, fresh = true;
-    uint32_t items = 0;
-    for (int64_t i = 0; ok && i < count; ++i) {
-      const uint32_t st = static_cast<uint32_t>(i) % kTileStages, ph = static_cast<uint32_t>(i) / kTileStages & 1u;
-      const uint32_t uph = static_cast<uint32_t>(i) & 1u;
-      const bool first = fresh;
-      if (fresh) {  // the item's first S (of the others, below)
-        ok = wait_all(q_full(0), items & 1u, kSiteAttn + 3) && wait_all(q_full(1), items & 1u, kSiteAttn + 3) &&
-             wait_all(k_full(st), ph, kSiteAttn + 4);
-        if (!ok) break;
-        s_mma(0, st);
-        s_mma(1, st);
-        if (issuer) umma_commit(k_empty(st));
-        ++items;
-        fresh = false;
-      }
-      const bool last = w.unit == w.units - 1 || i + 1 == count;
-      const uint32_t nst = static_cast<uint32_t>(i + 1) % kTileStages;
-      const uint32_t nph = static_cast<uint32_t>(i + 1) / kTileStages & 1u;
-      ok = wait_all(v_full(st), ph, kSiteAttn + 5) && wait_all(p_full(0), uph, kSiteAttn + 6);
+    uint32_t i = 0;
+    bool ok = true;
+    for (uint32_t items = 0; ok && i < count; ++items) {
+      const uint32_t end = i + min(static_cast<uint32_t>(w.units - w.unit), count - i);  // of the item here
+      uint32_t st = i % kTileStages;
+      ok = wait_all(q_full(0), items & 1u, kSiteAttn + 3) && wait_all(q_full(1), items & 1u, kSiteAttn + 3) &&
+           wait_all(k_full(st), i / kTileStages & 1u, kSiteAttn + 4);
       if (!ok) break;
-      o_mma(0, st, first);
-      if (!last) {
-        ok = wait_all(k_full(nst), nph, kSiteAttn + 4);
+      s_mma(0, st);
+      s_mma(1, st);
+      if (issuer) umma_commit(k_empty(st));
+      for (bool first = true; i < end; ++i, first = false) {
+        st = i % kTileStages;
+        const uint32_t ph = i / kTileStages & 1u, uph = i & 1u;
+        const uint32_t nst = (i + 1) % kTileStages, nph = (i + 1) / kTileStages & 1u;
+        const bool more = i + 1 < end;
+        ok = wait_all(v_full(st), ph, kSiteAttn + 5) && wait_all(p_full(0), uph, kSiteAttn + 6);
         if (!ok) break;
-        s_mma(0, nst);
+        o_mma(0, st, first);
+        if (more) {
+          ok = wait_all(k_full(nst), nph, kSiteAttn + 4);
+          if (!ok) break;
+          s_mma(0, nst);
+        }
+        ok = wait_all(p_full(1), uph, kSiteAttn + 6);
+        if (!ok) break;
+        o_mma(1, st, first);
+        if (issuer) umma_commit(v_empty(st));
+        if (more) {
+          s_mma(1, nst);
+          if (issuer) umma_commit(k_empty(nst));
+        }
       }
-      ok = wait_all(p_full(1), uph, kSiteAttn + 6);
-      if (!ok) break;
-      o_mma(1, st, first);
-      if (issuer) umma_commit(v_empty(st));
-      if (!last) {
-        s_mma(1, nst);
-        if (issuer) umma_commit(k_empty(nst));
-      }
-      fresh = last;
-      if (i + 1 < count) walk_on<kTileRows>(w, p, deal, places);
+      if (ok && i < count) walk_item<kTileRows>(w, p, deal, places);
     }
     // (no product is left in flight when the tensor memory is given back)
     if (issuer) umma_commit(drained);
@@ -320,31 +414,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // its quarter of tensor memory's lanes
     const uint32_t ts = tmem + 128u * tl + lanes, to = tmem + 256u + kD * tl + lanes;
     const uint32_t r = static_cast<uint32_t>(tid) & 127u;  // its row of the tile
-    float m = 0.f, l = 0.f, bs = 0.f, rf = 0.f, lv = 0.f;
-    int limit = 0, low = 0;  // its last key; the smallest of the warp's rows
-    int64_t item = 0, out_at = 0;
-    bool row_in = false, fresh = true, ok = true;
-    for (int64_t i = 0; ok && i < count; ++i) {
-      const uint32_t uph = static_cast<uint32_t>(i) & 1u;
-      const uint32_t sl = static_cast<uint32_t>(i) % kTileScales, sph = static_cast<uint32_t>(i) / kTileScales & 1u;
-      const bool first = fresh;
-      if (fresh) {  // a new item: its row of q, in fp16
-        fresh = false;
-        item = u0 + i - w.unit;
-        const AttnRow row = attn_row(p, w.s, w.hk, w.tile * kTileRows + 128 * static_cast<int>(tl) + static_cast<int>(r));
-        limit = row.limit;
-        low = __shfl_sync(0xffffffffu, limit, 0);
-        row_in = row.in;
-        out_at = row.at;
-        m = bs = -INFINITY;
-        l = 0.f;
-        lv = kLeastScale;
-        const __nv_bfloat16* q = p.q + row.at * kD;
+    const float* const scales = reinterpret_cast<const float*>(smem + Smem::kScale);
+    uint32_t i = 0;
+    bool ok = true;
+    while (ok && i < count) {
+      // an item, or what of it lies in this block's share: its row of q, in fp16
+      const uint32_t begin = i, end = i + min(static_cast<uint32_t>(w.units - w.unit), count - i);
+      const AttnRow row = attn_row(p, w.s, w.hk, w.tile * kTileRows + static_cast<int>(128 * tl + r));
+      const int limit = row.limit, low = __shfl_sync(0xffffffffu, limit, 0);  // (the smallest of the warp's rows)
+      float rf;
+      {
+        Chunk8 c[kD / 8];
         float amax = 0.f;
 #pragma unroll
-        for (int c = 0; c < kD / 8; ++c) {
+        for (int j = 0; j < kD / 8; ++j) c[j] = ldg8(p.q + row.at * kD + 8 * j);
+#pragma unroll
+        for (int j = 0; j < kD / 8; ++j) {
           float v[8];
-          unpack8(ldg8(q + 8 * c), v);
+          unpack8(c[j], v);
 #pragma unroll
           for (int e = 0; e < 8; e += 2) amax = max3_abs_nan(amax, v[e], v[e + 1]);
         }
@@ -352,158 +439,114 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         row_power(amax, up, down);
         rf = p.scale_log2 * down;
 #pragma unroll
-        for (int c = 0; c < kD / 8; ++c) {
+        for (int j = 0; j < kD / 8; ++j) {
           float v[8];
-          unpack8(ldg8(q + 8 * c), v);
-          st_shared_v4(base + Smem::kQ + tl * Smem::kOperand + panel_at(r, c), pack_f16x2(v[0] * up, v[1] * up),
+          unpack8(c[j], v);
+          st_shared_v4(base + Smem::kQ + tl * Smem::kOperand + panel_at(r, j), pack_f16x2(v[0] * up, v[1] * up),
                        pack_f16x2(v[2] * up, v[3] * up), pack_f16x2(v[4] * up, v[5] * up),
                        pack_f16x2(v[6] * up, v[7] * up));
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full(tl));
       }
-      ok = warp_wait(sc_full(sl), sph, kSiteAttn + 8) && warp_wait(s_full(tl), uph, kSiteAttn + 9);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(tl));
+      float m = -INFINITY, bs = -INFINITY, l = 0.f, lv = kLeastScale;
+      int key = w.unit * kAttnUnit;
+      for (; i < end; ++i, key += kAttnUnit) {
+        const uint32_t uph = i & 1u, sl = i % kTileScales;
+        ok = warp_wait(sc_full(sl), i / kTileScales & 1u, kSiteAttn + 8) && warp_wait(s_full(tl), uph, kSiteAttn + 9);
+        if (!ok) break;
+        tc_fence_after();
+        const float* const sc = scales + sl * (Smem::kScaleSlot / 4);
+        const bool edge = key + kAttnUnit - 1 > low;
+        // The row's largest score.  The next 32 columns are on their way while 32 are looked at.
+        const int seen = limit - key;  // columns 0 .. seen
+        float mx = -INFINITY;
+        uint32_t va[32], vb[32];
+        if (edge)
+          largest_score<true>(ts, sc, seen, va, vb, mx);
+        else
+          largest_score<false>(ts, sc, seen, va, vb, mx);
+        const float4 vm = *reinterpret_cast<const float4*>(sc + 256);
+        lv = fmaxf(lv, scale_power(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))));
+        m = fmaxf(m, mx == -INFINITY ? mx : mx * rf);
+        // what is taken out of the exponents: moved where P would leave fp16
+        const bool move = m + lv > bs + 8.0f;
+        if (__any_sync(0xffffffffu, move)) {
+          const float corr = move ? ex2(bs - (m + lv)) : 1.0f;
+          if (move) bs = m + lv;
+          l *= corr;
+          if (i > begin) {
+            ok = warp_wait(pv_done(tl), uph ^ 1u, kSiteAttn + 10);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 32) {
+              tmem_ld32(to + c, vb);
+              tmem_ld_wait(vb);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) vb[e] = __float_as_uint(__uint_as_float(vb[e]) * corr);
+              tmem_st32(to + c, vb);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float less = bs == -INFINITY ? 0.f : bs;  // (no key seen yet)
+        uint64_t sum2 = 0;
+        if (edge)
+          weights<true>(ts, sc, seen, pack2(rf, rf), pack2(-less, -less), va, vb, sum2);
+        else
+          weights<false>(ts, sc, seen, pack2(rf, rf), pack2(-less, -less), va, vb, sum2);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(p_full(tl));
+          mbar_arrive(sc_empty(sl));
+        }
+        float s0, s1;
+        unpack2(sum2, s0, s1);
+        l += s0 + s1;
+      }
+      if (!ok) break;
+      ok = warp_wait(pv_done(tl), (i - 1) & 1u, kSiteAttn + 10);
       if (!ok) break;
       tc_fence_after();
-      const float* const sc = reinterpret_cast<const float*>(smem + Smem::kScale + sl * Smem::kScaleSlot);
-      const int key = w.unit * kAttnUnit;
-      const bool edge = key + kAttnUnit - 1 > low;
-      const float4 vm = *reinterpret_cast<const float4*>(sc + 256);
-      lv = fmaxf(lv, scale_power(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w))));
-      // the row's largest score
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      const bool begins = w.unit == 0, ends = w.unit + static_cast<int>(end - begin) == w.units;
+      const bool whole = begins && ends;
+      const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0)) * kTileRows + 128 * tl + r;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 32) {
         uint32_t v[32];
-        tmem_ld32(ts + 32u * c, v);
+        tmem_ld32(to + c, v);
         tmem_ld_wait(v);
+        if (row.in && whole) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 k4 = *reinterpret_cast<const float4*>(sc + 32 * c + e);
-          float x[4];
-          unpack2(mul2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pack2(k4.x, k4.y)), x[0], x[1]);
-          unpack2(mul2(pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), pack2(k4.z, k4.w)), x[2], x[3]);
-          if (edge) {
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
 #pragma unroll
             for (int f = 0; f < 4; ++f)
-              if (key + 32 * c + e + f > limit) x[f] = -INFINITY;
+              o[f] = pack_bf16x2(__uint_as_float(v[e + 2 * f]) * inv, __uint_as_float(v[e + 2 * f + 1]) * inv);
+            stg8(p.o + row.at * kD + c + e, o);
           }
-          mx = max3(mx, x[0], x[1]);
-          mx = max3(mx, x[2], x[3]);
+        } else if (row.in) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(ws.o + slot * kD + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
+        __syncwarp();
       }
-      m = fmaxf(m, mx == -INFINITY ? mx : mx * rf);
-      // what is taken out of the exponents: moved where P would leave fp16
-      float corr = 1.0f;
-      if (m + lv > bs + 8.0f) {
-        corr = ex2(bs - (m + lv));
-        bs = m + lv;
+      if (row.in) {
+        if (!whole)
+          ws.ml[slot] = make_float2(bs, l);
+        else if (p.lse != nullptr)
+          p.lse[row.at] = attn_lse(bs, l);
       }
-      l *= corr;
-      if (!first && __any_sync(0xffffffffu, corr != 1.0f)) {
-        ok = warp_wait(pv_done(tl), uph ^ 1u, kSiteAttn + 10);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < kD / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(to + 32u * c, v);
-          tmem_ld_wait(v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * corr);
-          tmem_st32(to + 32u * c, v);
-        }
-        tmem_st_wait();
-      }
-      const float less = bs == -INFINITY ? 0.f : bs;  // (no key seen yet)
-      const uint64_t rf2 = pack2(rf, rf), less2 = pack2(-less, -less);
-      uint64_t sum2 = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32], pk[16];
-        tmem_ld32(ts + 32u * c, v);
-        tmem_ld_wait(v);
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 k4 = *reinterpret_cast<const float4*>(sc + 32 * c + e);
-          const float4 v4 = *reinterpret_cast<const float4*>(sc + 128 + 32 * c + e);
-          const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-          for (int f = 0; f < 4; f += 2) {
-            uint64_t x = mul2(pack2(__uint_as_float(v[e + f]), __uint_as_float(v[e + f + 1])), pack2(kk[f], kk[f + 1]));
-            float a, b;
-            unpack2(fma2(x, rf2, less2), a, b);
-            a = ex2(a);
-            b = ex2(b);
-            const int at = key + 32 * c + e + f;
-            if (edge) {
-              if (at > limit) a = 0.f;
-              if (at + 1 > limit) b = 0.f;
-            }
-            const uint64_t y = pack2(a, b);
-            sum2 = add2(sum2, y);
-            unpack2(mul2(y, pack2(vv[f], vv[f + 1])), a, b);
-            if (edge) {  // (a scale behind the row's last key may be NaN)
-              if (at > limit) a = 0.f;
-              if (at + 1 > limit) b = 0.f;
-            }
-            pk[(e + f) / 2] = pack_f16x2(a, b);
-          }
-        }
-        tmem_st16(ts + 16u * c, pk);
-      }
-      float s0, s1;
-      unpack2(sum2, s0, s1);
-      l += s0 + s1;
-      tmem_st_wait();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(p_full(tl));
-        mbar_arrive(sc_empty(sl));
-      }
-      const bool ends = w.unit == w.units - 1;
-      if (ends || i + 1 == count) {
-        ok = warp_wait(pv_done(tl), uph, kSiteAttn + 10);
-        if (!ok) break;
-        tc_fence_after();
-        const bool whole = ends && item >= u0;
-        const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (item >= u0 ? 1 : 0)) * kTileRows + 128 * tl + r;
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-#pragma unroll
-        for (int c = 0; c < kD / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(to + 32u * c, v);
-          tmem_ld_wait(v);
-          if (row_in && whole) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t o[4];
-#pragma unroll
-              for (int f = 0; f < 4; ++f)
-                o[f] = pack_bf16x2(__uint_as_float(v[e + 2 * f]) * inv, __uint_as_float(v[e + 2 * f + 1]) * inv);
-              stg8(p.o + out_at * kD + 32 * c + e, o);
-            }
-          } else if (row_in) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(ws.o + slot * kD + 32 * c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-          }
-          __syncwarp();
-        }
-        if (row_in) {
-          if (!whole)
-            ws.ml[slot] = make_float2(bs, l);
-          else if (p.lse != nullptr)
-            p.lse[out_at] = attn_lse(bs, l);
-        }
-        tc_fence_before();
-        if (!ends && item >= u0 && tid == 0)
-          ws.cut[blockIdx.x] = AttnCut{total, item + w.units, w.b, w.hk, w.tile, 1};
-        fresh = true;
-      }
-      if (i + 1 < count) walk_on<kTileRows>(w, p, deal, places);
+      if (begins && !ends && tid == 0)
+        ws.cut[blockIdx.x] = AttnCut{total, u0 + begin + w.units, w.b, w.hk, w.tile, 1};
+      if (i < count) walk_item<kTileRows>(w, p, deal, places);
     }
   }
   tc_fence_before();

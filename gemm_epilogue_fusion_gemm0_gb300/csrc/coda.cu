@@ -1280,7 +1280,7 @@ cudaError_t launch_attn(const AttnQ8Params& p, char* at, int64_t rows, int block
                          AttnDeal{0, tiles ? kFewMost : 0x7fffffff});
   if (e == cudaSuccess) {
     after_launch(k++, stream);
-    e = launch(&attn_q8_join_kernel<kD, kFewRows>, blocks, 256, 0, stream, false, p, ws, blocks);
+    e = launch(&attn_q8_join_kernel<kD, kFewRows>, dim3(blocks, 1), 256, 0, stream, false, p, ws, blocks);
   }
   if (e == cudaSuccess) after_launch(k++, stream);
   if (e != cudaSuccess || !tiles) return e;
@@ -1289,7 +1289,7 @@ cudaError_t launch_attn(const AttnQ8Params& p, char* at, int64_t rows, int block
              AttnDeal{kFewMost, 0x7fffffff}, g_timeout_ns.load());
   if (e == cudaSuccess) {
     after_launch(k++, stream);
-    e = launch(&attn_q8_join_kernel<kD, kTileRows>, blocks, 256, 0, stream, false, p, ws, blocks);
+    e = launch(&attn_q8_join_kernel<kD, kTileRows>, dim3(blocks, kTileRows / 16), 256, 0, stream, false, p, ws, blocks);
   }
   if (e == cudaSuccess) after_launch(k++, stream);
   return e;
