@@ -164,13 +164,23 @@ def test_bad_pages(B, n):
     clean(B)
 
 
-def test_same_result_every_time(B):
-    batch = Batch([1] * 5 + [70], [400, 3000, 17, 900, 5000, 2000], 2, 128, 64)
-    cache, q = batch.random_cache(B), queries(batch, 16, 1)
+SAME = [  # new, lens, Hq, Hk, D, page
+    ([1] * 5 + [70], [400, 3000, 17, 900, 5000, 2000], 16, 2, 128, 64),
+    ([515], [3001], 4, 1, 128, 256),
+    ([515], [3001], 4, 1, 64, 16),
+    ([1300], [1300], 8, 8, 128, 64),
+]
+
+
+@pytest.mark.parametrize("new,lens,Hq,Hk,D,page", SAME)
+def test_same_result_every_time(B, new, lens, Hq, Hk, D, page):
+    """Bit for bit, many times over: a wait that lets something through a moment early shows as a run that differs."""
+    batch = Batch(new, lens, Hk, D, page)
+    cache, q = batch.random_cache(B), queries(batch, Hq, 1, 2.0)
     args = (q, cache, batch.cu, batch.lens, batch.table)
-    first = B.coda_attn_q8(*args)
-    for _ in range(5):
-        assert torch.equal(B.coda_attn_q8(*args), first)
+    runs = [B.coda_attn_q8(*args, most=max(new)) for _ in range(60)]
+    assert all(torch.equal(r, runs[0]) for r in runs)
+    clean(B)
 
 
 def test_layer(B):
