@@ -8,7 +8,7 @@
 //
 // The rows of a sequence that share a key head, n tokens of `group` query heads each, are packed
 // (row r is token r / group, head r % group) and cut into tiles; a tile with its keys is an item, and
-// 128 keys of it a unit.  Lengths are known to the device alone, so each block of a persistent grid
+// 128 or 256 keys of it a unit.  Lengths are known to the device alone, so each block of a persistent grid
 // adds up the units of all sequences, takes an equal, contiguous share of them, and walks it: whatever
 // the lengths, all SMs end together, and a long sequence's keys are spread over as many blocks as its
 // share of the work.  A part of an item leaves its running maximum, sum and unnormalised
@@ -20,7 +20,8 @@
 
 namespace coda {
 
-constexpr int kAttnUnit = 128;       // keys
+constexpr int kAttnUnit = 128;       // keys of the kernel for tiles
+constexpr int kFewUnit = 256;        // of the kernel for few
 constexpr int kAttnMaxBlocks = 160;  // of the persistent grids
 
 struct AttnQ8Params {
@@ -62,8 +63,9 @@ __host__ __device__ inline int attn_extent(const AttnSeq& s, int group, int tile
   return keys <= 0 ? 0 : static_cast<int>(keys < places + 1 ? keys : places + 1);
 }
 
+template <int kUnit>
 __host__ __device__ inline int attn_units(int extent) {
-  return extent <= kAttnUnit ? 1 : (extent + kAttnUnit - 1) / kAttnUnit;  // (an empty item still writes zeros)
+  return extent <= kUnit ? 1 : (extent + kUnit - 1) / kUnit;  // (an empty item still writes zeros)
 }
 
 __host__ __device__ inline int attn_tiles(const AttnSeq& s, int group, int tile_rows) {
@@ -110,14 +112,14 @@ struct AttnWalk {
   int unit, units, extent;
 };
 
-template <int kRows>
+template <int kRows, int kUnit>
 __device__ __forceinline__ void walk_tile(AttnWalk& w, const AttnQ8Params& p, int places) {
   w.extent = attn_extent(w.s, p.group, kRows, w.tile, places);
-  w.units = attn_units(w.extent);
+  w.units = attn_units<kUnit>(w.extent);
 }
 
 // The next item (there is one), its first unit.
-template <int kRows>
+template <int kRows, int kUnit>
 __device__ __forceinline__ void walk_item(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
   w.unit = 0;
   if (++w.tile == w.tiles) {
@@ -132,23 +134,23 @@ __device__ __forceinline__ void walk_item(AttnWalk& w, const AttnQ8Params& p, co
       w.tiles = attn_tiles(w.s, p.group, kRows);
     }
   }
-  walk_tile<kRows>(w, p, places);
+  walk_tile<kRows, kUnit>(w, p, places);
 }
 
 // The next unit (there is one).
-template <int kRows>
+template <int kRows, int kUnit>
 __device__ __forceinline__ void walk_on(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
-  if (++w.unit == w.units) walk_item<kRows>(w, p, d, places);
+  if (++w.unit == w.units) walk_item<kRows, kUnit>(w, p, d, places);
 }
 
 // Units of a sequence for one key head, by a whole warp (0: another launch's sequence).
-template <int kRows>
+template <int kRows, int kUnit>
 __device__ __forceinline__ int64_t seq_units(const AttnSeq& s, const AttnQ8Params& p, const AttnDeal& d,
                                              int places, int lane) {
   if (!attn_takes(d, s, p.group)) return 0;
   const int tiles = attn_tiles(s, p.group, kRows);
   int64_t u = 0;
-  for (int t = lane; t < tiles; t += 32) u += attn_units(attn_extent(s, p.group, kRows, t, places));
+  for (int t = lane; t < tiles; t += 32) u += attn_units<kUnit>(attn_extent(s, p.group, kRows, t, places));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
   return u;
@@ -157,7 +159,7 @@ __device__ __forceinline__ int64_t seq_units(const AttnSeq& s, const AttnQ8Param
 // Adds up the units (all threads of the block, kThreads of them), and puts the walk at unit `u0`
 // of this block's share, which ends at u1.  Returns the launch's units.  A warp adds up a sequence at a
 // time, a lane a tile; `units` (shared memory, at least B numbers) holds the sequences' sums in between.
-template <int kRows, int kThreads>
+template <int kRows, int kUnit, int kThreads>
 __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places,
                                               int64_t* units, int64_t& u0, int64_t& u1) {
   __shared__ int64_t warp_sum[kThreads / 32];
@@ -165,7 +167,7 @@ __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p
   __shared__ int start_b;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   for (int b = warp; b < p.batch.B; b += kThreads / 32) {
-    const int64_t u = seq_units<kRows>(load_seq(p, b), p, d, places, lane);
+    const int64_t u = seq_units<kRows, kUnit>(load_seq(p, b), p, d, places, lane);
     if (lane == 0) units[b] = u;
   }
   __syncthreads();
@@ -207,7 +209,7 @@ __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p
   rest -= w.hk * per_head;
   for (w.tile = 0;; w.tile += 32) {  // 32 tiles at a time
     const int t = w.tile + lane;
-    const int u = t < w.tiles ? attn_units(attn_extent(w.s, p.group, kRows, t, places)) : 0;
+    const int u = t < w.tiles ? attn_units<kUnit>(attn_extent(w.s, p.group, kRows, t, places)) : 0;
     int64_t before = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -223,7 +225,7 @@ __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p
     }
     rest -= __shfl_sync(0xffffffffu, before, 31);
   }
-  walk_tile<kRows>(w, p, places);
+  walk_tile<kRows, kUnit>(w, p, places);
   w.unit = static_cast<int>(rest);
   __syncthreads();  // `units` is read: its memory is free
   return total;
@@ -255,9 +257,11 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 // Few rows: tiles of 16
 //
 // Bound by HBM: 2 (D + 4) bytes per key, used for at most 16 rows.  As in the product for few tokens, each
-// of 8 warps has its own ring: 16 keys of a unit, codes and scales, by cp.async three units ahead (100 KB in flight
-// per SM), and no barrier but the warp's in the loop.  The page of a unit is looked up one
-// unit before its copies start.
+// of 8 warps has its own ring: 2 x 16 keys of a unit (so that a short context is spread over all warps too),
+// codes and scales, by cp.async up to two units ahead (67 to 135 KB in flight per SM), and no barrier but the warp's
+// in the loop.  The pages of a unit are looked up one unit before its copies start.  Its instructions are as
+// near a bound: 16 keys at a time took 590 of them per 16 keys, 32 together share a row's maximum and the
+// bookkeeping.
 //
 // S = q k^T and o += p v run as mma.sync.m16n8k16 on fp16, the 16 rows as its rows.  q's rows are brought
 // into fp16's range by a power of two each (exact); codes are exact in fp16 (1024 + 128 + code by bits,
@@ -269,18 +273,22 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 //
 // Scales: a key's multiplies its column of S; a value's its column of p.  So that their product stays
 // within fp16, what is taken out of the exponents is not the largest score m alone but m + log2 of
-// the largest value scale so far (rounded up to a power of two): the sums and outputs share it.
+// the largest value scale so far (rounded up to a power of two): the sums and outputs share it.  It moves, and the
+// outputs with it, only where p would pass 2^8.
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 16, kFewWarps = 8, kFewStages = 4;
-constexpr int kFewKeys = kAttnUnit / kFewWarps;  // of a warp's stage: 16
-static_assert(kFewKeys == 16, "a page holds a warp's keys");
+constexpr int kFewRows = 16, kFewWarps = 8, kFewStages = 2;
+constexpr int kFewKeys = 16;                  // together: a page holds them
+constexpr int kFewApart = kFewKeys * kFewWarps;  // from a warp's first 16 keys of a unit to its second
+static_assert(kFewUnit == 2 * kFewApart, "a unit");
 
 template <int kD>
 struct FewSmem {
-  static constexpr uint32_t kStage = 2 * kFewKeys * kD + 2 * kFewKeys * 4;  // k, v, their scales
+  static constexpr uint32_t kCodes = kFewKeys * kD;                         // of 16 keys
+  static constexpr uint32_t kGroup = 2 * kCodes + 2 * kFewKeys * 4;         // k, v, their scales
+  static constexpr uint32_t kStage = 2 * kGroup;
   static constexpr uint32_t kJoin = kFewWarps * kFewStages * kStage;        // the warps' outputs
   static constexpr uint32_t kBytes = kJoin + kFewWarps * kFewRows * kD * 4;
-  static_assert(kStage % 128 == 0 && kBytes <= 232448u - 4096u, "shared memory");
+  static_assert(kGroup % 128 == 0 && kBytes <= 232448u - 4096u, "shared memory");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -327,6 +335,19 @@ __device__ __forceinline__ float scale_power(float s) {
                       : kLeastScale;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// max(|a|, |b|, |c|), of those that are numbers
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Four codes of a word to fp16, in order
 __device__ __forceinline__ void q8_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = w ^ 0x80808080u;
@@ -369,45 +390,56 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
 
   AttnWalk w;
   int64_t u0, u1;
-  const int64_t total = walk_start<kFewRows, 32 * kFewWarps>(
+  const int64_t total = walk_start<kFewRows, kFewUnit, 32 * kFewWarps>(
       w, p, deal, places, reinterpret_cast<int64_t*>(smem_few), u0, u1);
   if (threadIdx.x == 0) ws.cut[blockIdx.x].valid = 0;
   if (u0 >= u1) return;
+  const int mine = warp * kFewKeys;  // the warp's first key of a unit
+  const int mask = (1 << p.cache.page_log2) - 1;
   AttnWalk ahead = w;
-  // page of the warp's keys of a unit; -1 also where it has none of them
-  const auto page_at = [&](const AttnWalk& a) {
-    const int key = a.unit * kAttnUnit + warp * kFewKeys;
-    return key < a.extent ? page_of(p.batch, p.cache, a.b, key) : -1;
+  // the table's entry for the warp's first (even lanes) and second 16 keys of a unit
+  const auto entry_at = [&](const AttnWalk& a) {
+    const int key = a.unit * kFewUnit + mine + kFewApart * (lane & 1), i = key >> p.cache.page_log2;
+    return key < a.extent && i < p.batch.width ? __ldg(p.batch.table + static_cast<size_t>(a.b) * p.batch.width + i) : -1;
   };
-  int page = page_at(ahead);
+  int entry = entry_at(ahead);
   int64_t issued = u0;
+  constexpr int kChunks = kD / 16;
+  // this thread's 16 codes of a copy: key kr (+ 32 / kChunks for the next), group kc
+  const uint32_t kr = lane / kChunks, kc = lane % kChunks;
+  const uint32_t lane_at = kr * kD + 16 * kc;
   const auto issue = [&]() {  // the unit `ahead` is at
-    const int key = ahead.unit * kAttnUnit + warp * kFewKeys;
-    if (key < ahead.extent) {
-      const uint32_t st = ring + static_cast<uint32_t>(issued & (kFewStages - 1)) * Smem::kStage;
-      const uint32_t sc = st + 2 * kFewKeys * kD + 4u * lane;  // k's 16 scales, then v's
-      if (page >= 0) {
-        const size_t e = cache_entry(p.cache, page, ahead.hk, key & ((1 << p.cache.page_log2) - 1));
-        constexpr int kGroups = kD / 16;
+    const uint32_t st = ring + static_cast<uint32_t>(issued & (kFewStages - 1)) * Smem::kStage;
 #pragma unroll
-        for (int i = 0; i < kFewKeys * kGroups / 32; ++i) {
-          const uint32_t r = (i * 32 + lane) / kGroups, c = lane % kGroups;
-          const size_t at = (e + r) * kD + 16 * c;
-          cp_async16(st + few_k_at<kD>(r, c), p.cache.k_q + at);
-          cp_async16(st + kFewKeys * kD + few_v_at<kD>(r, c), p.cache.v_q + at);
+    for (int h = 0; h < 2; ++h) {
+      const int key = ahead.unit * kFewUnit + mine + kFewApart * h;
+      const int page = __shfl_sync(0xffffffffu, entry, h);
+      if (key >= ahead.extent) continue;
+      const uint32_t gr = st + h * Smem::kGroup;
+      const uint32_t sc = gr + 2 * Smem::kCodes + 4u * lane;  // k's 16 scales, then v's
+      if (static_cast<unsigned>(page) < static_cast<unsigned>(p.cache.pages)) {
+        const size_t e = cache_entry(p.cache, page, ahead.hk, key & mask);
+        const uint8_t* const k = p.cache.k_q + e * kD + lane_at;
+        const uint8_t* const v = p.cache.v_q + e * kD + lane_at;
+#pragma unroll
+        for (int i = 0; i < kFewKeys * kChunks / 32; ++i) {
+          const uint32_t r = i * (32 / kChunks) + kr;
+          cp_async16(gr + few_k_at<kD>(r, kc), k + i * 512);
+          cp_async16(gr + Smem::kCodes + few_v_at<kD>(r, kc), v + i * 512);
         }
         cp_async4(sc, (lane < 16 ? p.cache.k_s : p.cache.v_s) + e + (lane & 15));
       } else {
+        if (lane == 0) atomicCAS(&g_coda_status, 0u, 0x200u | kChkPage);
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc), "r"(0x7fffffff) : "memory");
       }
     }
     if (++issued < u1) {
-      walk_on<kFewRows>(ahead, p, deal, places);
-      page = page_at(ahead);
+      walk_on<kFewRows, kFewUnit>(ahead, p, deal, places);
+      entry = entry_at(ahead);
     }
   };
 #pragma unroll
-  for (int i = 0; i < kFewStages - 1; ++i) {
+  for (int i = 0; i < kFewStages; ++i) {
     if (issued < u1) issue();
     cp_async_commit();
   }
@@ -419,8 +451,6 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
   bool fresh = true;
   int64_t item = 0;  // its first unit
   for (int64_t u = u0; u < u1; ++u) {
-    if (issued < u1) issue();
-    cp_async_commit();
     if (fresh) {  // a new item: its rows of q
       fresh = false;
       item = u - w.unit;
@@ -437,6 +467,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         for (int i = 0; i < kSteps / 2; ++i) {
           c[i] = Chunk8{{0u, 0u, 0u, 0u}};
           if (row.in) c[i] = ldg8(p.q + row.at * kD + 64 * (i / 2) + 16 * t + 8 * (i % 2));
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps / 2; ++i) {
           float v[8];
           unpack8(c[i], v);
 #pragma unroll
@@ -466,15 +499,17 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
     }
     cp_async_wait<kFewStages - 1>();
     __syncwarp();
-    const int key = w.unit * kAttnUnit + warp * kFewKeys;
+    const int key = w.unit * kFewUnit + mine;
     if (key < w.extent) {
+      const bool two = key + kFewApart < w.extent;  // the second 16 too
       const uint32_t st = ring + static_cast<uint32_t>(u & (kFewStages - 1)) * Smem::kStage;
-      float s[2][4] = {};
+      float s[4][4] = {};  // of keys 8 n + 2 t + e of the first 16 (n = 0, 1) and of the second
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 4; ++n) {
+        if (n >= 2 && !two) continue;
 #pragma unroll
         for (int h = 0; h < kD / 64; ++h) {
-          const uint4 c = ld_shared_v4(st + few_k_at<kD>(8 * n + g, 4 * h + t));
+          const uint4 c = ld_shared_v4(st + (n / 2) * Smem::kGroup + few_k_at<kD>(8 * (n & 1) + g, 4 * h + t));
           const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -484,38 +519,41 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
             mma_f16_16816(s[n], a[0], a[1], a[2], a[3], b0, b1);
           }
         }
-      // keys key + 8 n + 2 t + e: their scales
-      const float* sc = reinterpret_cast<const float*>(
-          smem_few + (st - smem_u32(smem_few)) + 2 * kFewKeys * kD);
-      float ks[2][2], vs[2][2];
+      }
+      // their scales (those of the second 16, where there are none, are not looked at)
+      float ks[4][2], vs[4][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float2 a = *reinterpret_cast<const float2*>(sc + 8 * n + 2 * t);
-        const float2 b = *reinterpret_cast<const float2*>(sc + 16 + 8 * n + 2 * t);
+      for (int n = 0; n < 4; ++n) {
+        const float* sc = reinterpret_cast<const float*>(smem_few + (st - smem_u32(smem_few)) + (n / 2) * Smem::kGroup +
+                                                         2 * Smem::kCodes) + 8 * (n & 1) + 2 * t;
+        const float2 a = *reinterpret_cast<const float2*>(sc), b = *reinterpret_cast<const float2*>(sc + 16);
         ks[n][0] = a.x, ks[n][1] = a.y;
         vs[n][0] = b.x, vs[n][1] = b.y;
       }
-      const bool edge = key + kFewKeys - 1 > w.s.first + w.tile * kFewRows / p.group;
+      const auto key_of = [&](int n, int e) { return key + kFewApart * (n / 2) + 8 * (n & 1) + 2 * t + e; };
+      const bool edge = key + kFewApart + kFewKeys - 1 > w.s.first + w.tile * kFewRows / p.group;
       if (edge) {  // what lies behind the last key is not looked at
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (key + 8 * n + 2 * t + e >= w.extent) vs[n][e] = 0.f;
+            if (key_of(n, e) >= w.extent) vs[n][e] = 0.f;
       }
-      float vm = fmaxf(fmaxf(fabsf(vs[0][0]), fabsf(vs[0][1])), fmaxf(fabsf(vs[1][0]), fabsf(vs[1][1])));
-      float mx[2];
+      float vm = 0.f, mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int n = 0; n < 4; ++n) {
+        vm = max3_abs(vm, vs[n][0], vs[n][1]);
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int r = 0; r < 2; ++r) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = s[n][2 * r + e] * ks[n][e] * rf[r];
-            if (edge && key + 8 * n + 2 * t + e > limit[r]) x = -INFINITY;
-            s[n][2 * r + e] = x;
+          for (int e = 0; e < 2; ++e) s[n][2 * r + e] *= ks[n][e] * rf[r];
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (key_of(n, e) > limit[r]) s[n][2 * r + e] = -INFINITY;
           }
-        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+          mx[r] = max3(mx[r], s[n][2 * r], s[n][2 * r + 1]);
+        }
       }
 #pragma unroll
       for (int o = 1; o <= 2; o <<= 1) {
@@ -524,69 +562,87 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
       }
       lv = fmaxf(lv, scale_power(vm));
-      float c[2];
+      bool move = false;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         m[r] = fmaxf(m[r], mx[r]);
-        c[r] = 1.0f;
-        if (m[r] + lv > base[r]) {
-          c[r] = ex2(base[r] - (m[r] + lv));
-          base[r] = m[r] + lv;
-        }
-        const float less = base[r] == -INFINITY ? 0.f : base[r];  // (no key seen yet)
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = ex2(s[k][2 * r + e] - less);
-            sum += x;
-            float y = x * vs[k][e];
-            if (edge && key + 8 * k + 2 * t + e > limit[r]) y = 0.f;
-            s[k][2 * r + e] = y;
-          }
-        l[r] = fmaf(l[r], c[r], sum);
+        move |= m[r] + lv > base[r] + 8.0f;
       }
-      if (__any_sync(0xffffffffu, c[0] != 1.0f || c[1] != 1.0f)) {
+      if (__any_sync(0xffffffffu, move)) {
+        float c[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          c[r] = 1.0f;
+          if (m[r] + lv > base[r] + 8.0f) {
+            c[r] = ex2(base[r] - (m[r] + lv));
+            base[r] = m[r] + lv;
+          }
+          l[r] *= c[r];
+        }
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[j][e] *= c[e >> 1];
       }
-      const uint32_t a0 = pack_f16x2(s[0][0], s[0][1]), a1 = pack_f16x2(s[0][2], s[0][3]);
-      const uint32_t a2 = pack_f16x2(s[1][0], s[1][1]), a3 = pack_f16x2(s[1][2], s[1][3]);
-      uint32_t v[4][kD / 32];  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: kD / 8 values of each
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t r = 8 * (i >> 1) + 2 * t + (i & 1);
-        const uint32_t at = st + kFewKeys * kD;
-        if constexpr (kD == 128) {
-          const uint4 x = ld_shared_v4(at + few_v_at<kD>(r, g));
-          v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-        } else {
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                       : "=r"(v[i][0]), "=r"(v[i][1])
-                       : "r"(at + few_v_at<kD>(r, g >> 1) + 8u * (g & 1))
-                       : "memory");
-        }
+      for (int r = 0; r < 2; ++r) {
+        const float less = base[r] == -INFINITY ? 0.f : base[r];  // (no key seen yet)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = ex2(s[n][2 * r + e] - less);
+            l[r] += x;
+            s[n][2 * r + e] = x * vs[n][e];
+          }
+      }
+      if (edge) {  // (a scale behind a row's last key may be NaN)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key_of(n, e & 1) > limit[e >> 1]) s[n][e] = 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < kD / 32; ++i) {
-        uint32_t b[2][4];
+      for (int q = 0; q < 2; ++q) {
+        if (q == 1 && !two) continue;
+        const uint32_t a0 = pack_f16x2(s[2 * q][0], s[2 * q][1]), a1 = pack_f16x2(s[2 * q][2], s[2 * q][3]);
+        const uint32_t a2 = pack_f16x2(s[2 * q + 1][0], s[2 * q + 1][1]), a3 = pack_f16x2(s[2 * q + 1][2], s[2 * q + 1][3]);
+        uint32_t v[4][kD / 32];  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: kD / 8 values of each
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x = v[2 * h][i] ^ 0x80808080u, y = v[2 * h + 1][i] ^ 0x80808080u;
-          const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
-          b[h][0] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4140));
-          b[h][1] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4342));
-          b[h][2] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4140));
-          b[h][3] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4342));
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t r = 8 * (i >> 1) + 2 * t + (i & 1);
+          const uint32_t at = st + q * Smem::kGroup + Smem::kCodes;
+          if constexpr (kD == 128) {
+            const uint4 x = ld_shared_v4(at + few_v_at<kD>(r, g));
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+          } else {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(v[i][0]), "=r"(v[i][1])
+                         : "r"(at + few_v_at<kD>(r, g >> 1) + 8u * (g & 1))
+                         : "memory");
+          }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f16_16816(acc[4 * i + j], a0, a1, a2, a3, b[0][j], b[1][j]);
+        for (int i = 0; i < kD / 32; ++i) {
+          uint32_t b[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = v[2 * h][i] ^ 0x80808080u, y = v[2 * h + 1][i] ^ 0x80808080u;
+            const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
+            b[h][0] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4140));
+            b[h][1] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4342));
+            b[h][2] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4140));
+            b[h][3] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4342));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_f16_16816(acc[4 * i + j], a0, a1, a2, a3, b[0][j], b[1][j]);
+        }
       }
     }
-    __syncwarp();  // the stage is read: the next unit's copies may take it
+    __syncwarp();  // the stage is read (and used: what was read is in registers)
+    if (issued < u1) issue();
+    cp_async_commit();
     const bool ends = w.unit == w.units - 1;
     if (ends || u == u1 - 1) {
       // The warps' parts meet.
@@ -651,29 +707,35 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         ws.cut[blockIdx.x] = AttnCut{total, item + w.units, w.b, w.hk, w.tile, 1};
       fresh = true;
     }
-    if (u + 1 < u1) walk_on<kFewRows>(w, p, deal, places);
+    if (u + 1 < u1) walk_on<kFewRows, kFewUnit>(w, p, deal, places);
   }
   cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
-// The join of an item's parts: block (c, y) has rows 16 y .. 16 y + 15 of the item whose first part ends
-// block c's share; the parts follow in the next blocks' first slots.  The parts' weights are formed once,
-// then a thread adds four columns of a row over the parts, in order.
+// The join of an item's parts: block (c, y) has 16 rows of the item whose first part ends block c's share;
+// the parts follow in the next blocks' first slots.  The parts' weights are formed once, then a thread adds
+// four columns of a row over the parts, in order.  y = 0: of the launch for few; 1 ..: rows 16 (y - 1) ..
+// of the launch for tiles; of both in one launch.
 // ---------------------------------------------------------------------------
-template <int kD, int kRows>
-__global__ void __launch_bounds__(256) attn_q8_join_kernel(const AttnQ8Params p, const AttnWs ws, int blocks) {
+constexpr int kTileRows = 256;  // of the kernel for tiles
+
+template <int kD>
+__global__ void __launch_bounds__(256)
+    attn_q8_join_kernel(const AttnQ8Params p, const AttnWs few, const AttnWs tiles, int y0, int blocks) {
   constexpr int kGroup = 16;
   __shared__ float weight[kAttnMaxBlocks][kGroup];
   __shared__ int slots[kAttnMaxBlocks];
   __shared__ float2 row_ml[kGroup];
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x, tid = static_cast<int>(threadIdx.x);
+  const int c = blockIdx.x, tid = static_cast<int>(threadIdx.x), y = static_cast<int>(blockIdx.y) + y0;
+  const AttnWs& ws = y == 0 ? few : tiles;
+  const int kRows = y == 0 ? kFewRows : kTileRows;
   const AttnCut cut = ws.cut[c];
   if (!cut.valid) return;
   const AttnSeq s = load_seq(p, cut.b);
-  const int r0 = static_cast<int>(blockIdx.y) * kGroup;
+  const int r0 = y == 0 ? 0 : (y - 1) * kGroup;
   const int rows = min(kGroup, s.n * p.group - cut.tile * kRows - r0);
   if (rows <= 0) return;
   // blocks c .. c + parts - 1; one whose share is empty (fewer units than blocks) has no part

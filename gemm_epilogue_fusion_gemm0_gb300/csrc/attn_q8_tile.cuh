@@ -30,7 +30,7 @@
 
 namespace coda {
 
-constexpr int kTileRows = 256, kTileThreads = 704;
+constexpr int kTileThreads = 704;
 constexpr int kTileStages = 2, kTileScales = 4;  // rings: of k's and v's tiles, of their scales
 constexpr int kRawStages = 3;                    // ring of halves of a unit's codes (64 keys of k or v)
 constexpr int kWideners = 4;                     // warps: 16 keys of a half each
@@ -104,12 +104,6 @@ __device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_
 // What other threads wrote to shared memory before a barrier is seen by the tensor cores.
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 
 // Where the 16-byte group c (8 values) of a row sits in an operand of panels of 64 columns, 128-byte
@@ -224,7 +218,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   AttnWalk w;
   int64_t u0, u1;
   const int64_t total =
-      walk_start<kTileRows, kTileThreads>(w, p, deal, places, reinterpret_cast<int64_t*>(smem), u0, u1);
+      walk_start<kTileRows, kAttnUnit, kTileThreads>(w, p, deal, places, reinterpret_cast<int64_t*>(smem), u0, u1);
   if (tid == 0) ws.cut[blockIdx.x].valid = 0;
   if (u0 >= u1) return;
   if (tid == 0) {
@@ -361,7 +355,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = ask(p.cache.k_q, 0) && ask(p.cache.k_q, 1);
       if (!ok) break;
       if (i + 1 < count) {
-        walk_on<kTileRows>(w, p, deal, places);
+        walk_on<kTileRows, kAttnUnit>(w, p, deal, places);
         entry = entry_at(w);
       }
       const auto given = [&](float s, int e) {  // nothing behind the last key is looked at; NaN for a page that does not exist
@@ -447,7 +441,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (issuer) umma_commit(k_empty(nst));
         }
       }
-      if (ok && i < count) walk_item<kTileRows>(w, p, deal, places);
+      if (ok && i < count) walk_item<kTileRows, kAttnUnit>(w, p, deal, places);
     }
     // (no product is left in flight when the tensor memory is given back)
     if (issuer) umma_commit(drained);
@@ -629,7 +623,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc_fence_before();
       if (begins && !ends && tid == 0)
         ws.cut[blockIdx.x] = AttnCut{total, u0 + begin + w.units, w.b, w.hk, w.tile, 1};
-      if (i < count) walk_item<kTileRows>(w, p, deal, places);
+      if (i < count) walk_item<kTileRows, kAttnUnit>(w, p, deal, places);
     }
   }
   tc_fence_before();

@@ -1268,30 +1268,30 @@ AttnWs attn_ws(char* at, int tile_rows, int64_t D) {
 }
 
 // Sequences of up to kFewMost packed rows go to the kernel for few, the others to the one for tiles, each with
-// its own share of the blocks and its join; without a hint of `rows` (the most of a sequence) both
-// run, and one of them may find nothing.  If a sequence has more rows than the hint says, the kernel for
-// few takes it.
+// its own share of the blocks; one join serves both.  Without a hint of `rows` (the most of a sequence) both
+// run, and one of them may find nothing; a single sequence goes to tiles if it may have more than a few rows.  If a
+// sequence has more rows than the hint says, the kernel for few takes it.
 template <int kD>
 cudaError_t launch_attn(const AttnQ8Params& p, char* at, int64_t rows, int blocks, cudaStream_t stream) {
-  const bool tiles = rows > kFewMost;
+  const bool tiles = rows > kFewMost, few = !tiles || p.batch.B > 1;
+  const AttnWs wf = attn_ws(at, kFewRows, kD), wt = attn_ws(at + attn_ws_bytes(kFewRows, kD), kTileRows, kD);
   int k = 0;
-  AttnWs ws = attn_ws(at, kFewRows, kD);
-  cudaError_t e = launch(&attn_q8_few_kernel<kD>, blocks, 32 * kFewWarps, FewSmem<kD>::kBytes, stream, false, p, ws,
-                         AttnDeal{0, tiles ? kFewMost : 0x7fffffff});
-  if (e == cudaSuccess) {
-    after_launch(k++, stream);
-    e = launch(&attn_q8_join_kernel<kD, kFewRows>, dim3(blocks, 1), 256, 0, stream, false, p, ws, blocks);
+  cudaError_t e = cudaSuccess;
+  if (few) {
+    e = launch(&attn_q8_few_kernel<kD>, blocks, 32 * kFewWarps, FewSmem<kD>::kBytes, stream, false, p, wf,
+               AttnDeal{0, tiles ? kFewMost : 0x7fffffff});
+    if (e == cudaSuccess) after_launch(k++, stream);
   }
-  if (e == cudaSuccess) after_launch(k++, stream);
-  if (e != cudaSuccess || !tiles) return e;
-  ws = attn_ws(at, kTileRows, kD);
-  e = launch(&attn_q8_tile_kernel<kD>, blocks, kTileThreads, TileSmem<kD>::kBytes, stream, false, p, ws,
-             AttnDeal{kFewMost, 0x7fffffff}, g_timeout_ns.load());
-  if (e == cudaSuccess) {
-    after_launch(k++, stream);
-    e = launch(&attn_q8_join_kernel<kD, kTileRows>, dim3(blocks, kTileRows / 16), 256, 0, stream, false, p, ws, blocks);
+  if (e == cudaSuccess && tiles) {
+    e = launch(&attn_q8_tile_kernel<kD>, blocks, kTileThreads, TileSmem<kD>::kBytes, stream, false, p, wt,
+               AttnDeal{few ? kFewMost : 0, 0x7fffffff}, g_timeout_ns.load());
+    if (e == cudaSuccess) after_launch(k++, stream);
   }
-  if (e == cudaSuccess) after_launch(k++, stream);
+  if (e == cudaSuccess) {
+    e = launch(&attn_q8_join_kernel<kD>, dim3(blocks, (few ? 1 : 0) + (tiles ? kTileRows / 16 : 0)), 256, 0, stream, false,
+               p, wf, wt, few ? 0 : 1, blocks);
+    if (e == cudaSuccess) after_launch(k++, stream);
+  }
   return e;
 }
 
@@ -2113,7 +2113,7 @@ coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, const int8
 
 size_t coda_attn_q8_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
   if (check_heads(T, B, Hq, Hk, D) != CODA_OK || T == 0 || B == 0) return 0;
-  return kSlotBytes + attn_ws_bytes(T * (Hq / Hk) > kFewMost ? kTileRows : kFewRows, D);
+  return kSlotBytes + attn_ws_bytes(kFewRows, D) + (T * (Hq / Hk) > kFewMost ? attn_ws_bytes(kTileRows, D) : 0);
 }
 
 coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k_s, const int8_t* v_q,
