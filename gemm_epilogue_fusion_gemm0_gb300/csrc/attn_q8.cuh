@@ -96,8 +96,9 @@ struct AttnCut {
 
 struct AttnWs {
   AttnCut* cut;     // [blocks]
-  float2* ml;       // [2 blocks][tile rows]: what was taken out of the exponents (base 2), and the sum
-  float* o;         // [2 blocks][tile rows][D]
+  float2* ml;       // [2 blocks][rows]: what was taken out of the exponents (base 2), and the sum
+  float* o;         // [2 blocks][rows][D]
+  int rows;         // of a tile: as many as the call's tiles may have
 };
 
 __device__ __forceinline__ AttnSeq load_seq(const AttnQ8Params& p, int b) {
@@ -699,8 +700,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
           if (c == 0 && p.lse != nullptr)
             p.lse[row.at] = attn_lse(ml.x, ml.y);
         } else {
-          reinterpret_cast<float4*>(ws.o)[(slot * kFewRows + r) * (kD / 4) + c] = x;
-          if (c == 0) ws.ml[slot * kFewRows + r] = ml;
+          reinterpret_cast<float4*>(ws.o)[(slot * ws.rows + r) * (kD / 4) + c] = x;
+          if (c == 0) ws.ml[slot * ws.rows + r] = ml;
         }
       }
       if (!ends && item >= u0 && threadIdx.x == 0)
@@ -731,7 +732,7 @@ __global__ void __launch_bounds__(256)
   griddep_wait();
   const int c = blockIdx.x, tid = static_cast<int>(threadIdx.x), y = static_cast<int>(blockIdx.y) + y0;
   const AttnWs& ws = y == 0 ? few : tiles;
-  const int kRows = y == 0 ? kFewRows : kTileRows;
+  const int kRows = y == 0 ? kFewRows : kTileRows, slot_rows = ws.rows;
   const AttnCut cut = ws.cut[c];
   if (!cut.valid) return;
   const AttnSeq s = load_seq(p, cut.b);
@@ -749,13 +750,13 @@ __global__ void __launch_bounds__(256)
     const int r = tid >> 4, l = tid & 15;
     float top = -INFINITY, sum = 0.f;
     for (int j = l; j < parts; j += 16)
-      if (slots[j] >= 0 && r < rows) top = fmaxf(top, ws.ml[slots[j] * kRows + r0 + r].x);
+      if (slots[j] >= 0 && r < rows) top = fmaxf(top, ws.ml[slots[j] * slot_rows + r0 + r].x);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float less = top == -INFINITY ? 0.f : top;
     for (int j = l; j < parts; j += 16)
       if (slots[j] >= 0 && r < rows) {
-        const float2 ml = ws.ml[slots[j] * kRows + r0 + r];
+        const float2 ml = ws.ml[slots[j] * slot_rows + r0 + r];
         const float f = ex2(ml.x - less);
         weight[j][r] = f;
         sum = fmaf(ml.y, f, sum);
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll 8
     for (int j = 0; j < parts; ++j) {
       if (slots[j] < 0) continue;
-      const float4 y = part[static_cast<size_t>(slots[j]) * kRows * (kD / 4)];
+      const float4 y = part[static_cast<size_t>(slots[j]) * slot_rows * (kD / 4)];
       const float f = weight[j][r];
       x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
     }

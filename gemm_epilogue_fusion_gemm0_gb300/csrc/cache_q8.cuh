@@ -95,7 +95,9 @@ __device__ __forceinline__ RowPlace place_of(const BatchQ8& bt, const CacheQ8& c
 //
 // Bound by HBM: 2 (Hq + 2 Hk) D bytes in, 2 Hq D + 2 Hk (D + 4) out per token.  A block takes kTokens
 // tokens: its threads find the tokens' places and form their angles' cos and sin once, one each, then D / 8
-// threads share a head (16 bytes in each), and a group of them walks the heads of one token.
+// threads share a head (16 bytes in each), and a group of them walks the heads of one token, kWriteBatch at a
+// time: their loads go out together, the first ones before the places are known.  (One head at a time, with the
+// shuffles of its maximum between the loads: 83 us for 8192 tokens of 64 + 16 heads of 128.)
 // ---------------------------------------------------------------------------
 constexpr int kRopeMax = 64;  // pairs
 constexpr int kRopeAxes = 4;
@@ -117,9 +119,10 @@ struct CacheWriteParams {
 };
 
 constexpr int kCacheThreads = 256;
+constexpr int kWriteBatch = 5;
 
 template <int kD, int kTokens>
-__global__ void __launch_bounds__(kCacheThreads)
+__global__ void __launch_bounds__(kCacheThreads, 3)
     cache_write_q8_kernel(const CacheWriteParams p, const __grid_constant__ RopeQ8 rope) {
   constexpr int kLanes = kD / 8;                            // threads per head
   constexpr int kGroups = kCacheThreads / kLanes / kTokens;  // heads of a token at a time
@@ -129,6 +132,25 @@ __global__ void __launch_bounds__(kCacheThreads)
   griddep_wait();
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int row0 = static_cast<int>(blockIdx.x) * kTokens;
+  const int group = tid / kLanes, c = tid % kLanes;  // c: this thread's 8 values of the head
+  const int t = group / kGroups;
+  const size_t row = static_cast<size_t>(row0 + t);
+  const int Hk = p.cache.Hk, heads = p.Hq + 2 * Hk;
+  const int step = kGroups * static_cast<int>(gridDim.y);
+  const int first = static_cast<int>(blockIdx.y) * kGroups + group % kGroups;
+  const int rounds = (heads + step - 1) / step;
+  const __nv_bfloat16* const y = p.y + row * heads * kD + 8 * c;
+  const bool there = row0 + t < p.batch.rows;
+  Chunk8 x[kWriteBatch];
+  const auto load = [&](int r) {
+#pragma unroll
+    for (int b = 0; b < kWriteBatch; ++b) {
+      const int h = first + (r + b) * step;
+      x[b] = Chunk8{{0u, 0u, 0u, 0u}};
+      if (there && h < heads) x[b] = ldg8(y + h * kD);
+    }
+  };
+  load(0);
   for (int i = warp; i < kTokens; i += kCacheThreads / 32) {
     const RowPlace pl = place_of(p.batch, p.cache, row0 + i, lane);
     if (lane == 0) place[i] = pl;
@@ -145,12 +167,8 @@ __global__ void __launch_bounds__(kCacheThreads)
   }
   __syncthreads();
 
-  const int group = tid / kLanes, c = tid % kLanes;  // c: this thread's 8 values of the head
-  const int t = group / kGroups;
   const RowPlace pl = place[t];
   // (no thread leaves before the last shuffle: a warp's groups may be of different tokens)
-  const size_t row = static_cast<size_t>(row0 + t);
-  const int Hk = p.cache.Hk, heads = p.Hq + 2 * Hk;
   const int hc = rope.half / 8;  // 16-byte groups in half of the turned part
   const bool turned = c < 2 * hc;
   const bool pairs = rope.pairs != 0;
@@ -166,51 +184,50 @@ __global__ void __launch_bounds__(kCacheThreads)
   }
   const int base = lane / kLanes * kLanes;  // the group's first lane in the warp
   const int partner = base + (pairs || !turned ? c : c < hc ? c + hc : c - hc);
-  const int step = kGroups * static_cast<int>(gridDim.y);
-  const int first = static_cast<int>(blockIdx.y) * kGroups + group % kGroups;
-  const int rounds = (heads + step - 1) / step;
-#pragma unroll 4
-  for (int r = 0; r < rounds; ++r) {
-    const int h = first + r * step;
-    const bool in = pl.seq >= 0 && h < heads;
-    Chunk8 x = {{0u, 0u, 0u, 0u}};
-    const size_t at = (row * heads + h) * kD + 8 * c;
-    if (in) x = ldg8(p.y + at);
-    Chunk8 o = x;
-    if (!pairs) {
+#pragma unroll 1
+  for (int r0 = 0; r0 < rounds; r0 += kWriteBatch) {
+    if (r0 > 0) load(r0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o.w[e] = __shfl_sync(0xffffffffu, x.w[e], partner);
-    } else {
+    for (int rb = 0; rb < kWriteBatch; ++rb) {
+      const int h = first + (r0 + rb) * step;
+      const bool in = pl.seq >= 0 && h < heads;
+      const Chunk8 xv = x[rb];
+      Chunk8 o = xv;
+      if (!pairs) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o.w[e] = __byte_perm(x.w[e], 0u, 0x1032);  // halves exchanged
-    }
-    float u[1][8], w[8];
-    unpack8(x, u[0]);
-    unpack8(o, w);
-    const bool is_v = h >= p.Hq + Hk;
-    if (turned && !is_v) {
+        for (int e = 0; e < 4; ++e) o.w[e] = __shfl_sync(0xffffffffu, xv.w[e], partner);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u[0][e] = fmaf(w[e], sv[e], u[0][e] * cv[e]);
-    }
-    float amax = 0.f;
+        for (int e = 0; e < 4; ++e) o.w[e] = __byte_perm(xv.w[e], 0u, 0x1032);  // halves exchanged
+      }
+      float u[1][8], w[8];
+      unpack8(xv, u[0]);
+      unpack8(o, w);
+      const bool is_v = h >= p.Hq + Hk;
+      if (turned && !is_v) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) amax = max3_abs_nan(amax, u[0][e], u[0][e + 1]);
+        for (int e = 0; e < 8; ++e) u[0][e] = fmaf(w[e], sv[e], u[0][e] * cv[e]);
+      }
+      float amax = 0.f;
 #pragma unroll
-    for (int o2 = kLanes / 2; o2 > 0; o2 >>= 1)
-      amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o2));
-    if (!in) continue;
-    if (h < p.Hq) {
-      uint32_t v[4];
+      for (int e = 0; e < 8; e += 2) amax = max3_abs_nan(amax, u[0][e], u[0][e + 1]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = pack_bf16x2(u[0][2 * e], u[0][2 * e + 1]);
-      stg8(p.q_out + (row * p.Hq + h) * kD + 8 * c, v);
-    } else if (pl.page >= 0) {
-      const size_t e = cache_entry(p.cache, pl.page, is_v ? h - p.Hq - Hk : h - p.Hq, pl.slot);
-      const Q8Factors f(amax);
-      f.prepare(u);
-      // (a key that is not turned is a bf16 number: the quantiser's rounding)
-      q8_store8<true>((is_v ? p.cache.v_q : p.cache.k_q) + e * kD + 8 * c, u[0], f);
-      if (c == 0) (is_v ? p.cache.v_s : p.cache.k_s)[e] = q8_scale(amax);
+      for (int o2 = kLanes / 2; o2 > 0; o2 >>= 1)
+        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o2));
+      if (!in) continue;
+      if (h < p.Hq) {
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = pack_bf16x2(u[0][2 * e], u[0][2 * e + 1]);
+        stg8(p.q_out + (row * p.Hq + h) * kD + 8 * c, v);
+      } else if (pl.page >= 0) {
+        const size_t e = cache_entry(p.cache, pl.page, is_v ? h - p.Hq - Hk : h - p.Hq, pl.slot);
+        const Q8Factors f(amax);
+        f.prepare(u);
+        // (a key that is not turned is a bf16 number: the quantiser's rounding)
+        q8_store8<true>((is_v ? p.cache.v_q : p.cache.k_q) + e * kD + 8 * c, u[0], f);
+        if (c == 0) (is_v ? p.cache.v_s : p.cache.k_s)[e] = q8_scale(amax);
+      }
     }
   }
 }
@@ -247,38 +264,48 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_q8_kernel(const Cach
   const int c = tid % kLanes, Hk = p.cache.Hk;
   const int units = kReadTokens * Hk;  // token-major: neighbours write neighbouring heads
   const int step = kGroups * static_cast<int>(gridDim.y);
-#pragma unroll 2
-  for (int u = static_cast<int>(blockIdx.y) * kGroups + tid / kLanes; u < units; u += step) {
-    const int t = u / Hk, h = u - t * Hk;
-    const RowPlace pl = place[t];
-    if (pl.seq < 0) continue;
-    const size_t out = (static_cast<size_t>(row0 + t) * Hk + h) * kD + 16 * c;
-    const size_t e = pl.page >= 0 ? cache_entry(p.cache, pl.page, h, pl.slot) : 0;
-    uint4 q[2];
-    float s[2];
+  // two units at a time, their loads together
+  for (int u0 = static_cast<int>(blockIdx.y) * kGroups + tid / kLanes; u0 < units; u0 += 2 * step) {
+    uint4 q[2][2];
+    float s[2][2];
+    size_t out[2];
+    bool in[2];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      q[kv] = make_uint4(0u, 0u, 0u, 0u);
-      s[kv] = pl.pos < 0 ? 0.f : __int_as_float(0x7fffffff);
-      if (pl.page >= 0) {
-        q[kv] = *reinterpret_cast<const uint4*>((kv ? p.cache.v_q : p.cache.k_q) + e * kD + 16 * c);
-        s[kv] = (kv ? p.cache.v_s : p.cache.k_s)[e];
+    for (int b = 0; b < 2; ++b) {
+      const int u = u0 + b * step, t = u / Hk, h = u - t * Hk;
+      const RowPlace pl = place[min(t, kReadTokens - 1)];
+      in[b] = u < units && pl.seq >= 0;
+      out[b] = (static_cast<size_t>(row0 + t) * Hk + h) * kD + 16 * c;
+      const bool held = in[b] && pl.page >= 0;
+      const size_t e = held ? cache_entry(p.cache, pl.page, h, pl.slot) : 0;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        q[b][kv] = make_uint4(0u, 0u, 0u, 0u);
+        s[b][kv] = pl.pos < 0 ? 0.f : __int_as_float(0x7fffffff);
+        if (held) {
+          q[b][kv] = __ldcs(reinterpret_cast<const uint4*>((kv ? p.cache.v_q : p.cache.k_q) + e * kD + 16 * c));
+          s[b][kv] = __ldg((kv ? p.cache.v_s : p.cache.k_s) + e);
+        }
       }
     }
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint32_t w[4] = {q[kv].x, q[kv].y, q[kv].z, q[kv].w};
-      uint32_t v[8];
+    for (int b = 0; b < 2; ++b) {
+      if (!in[b]) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[4];
-        q8_unpack4(w[i], f);
-        v[2 * i] = pack_bf16x2(f[0] * s[kv], f[1] * s[kv]);
-        v[2 * i + 1] = pack_bf16x2(f[2] * s[kv], f[3] * s[kv]);
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t w[4] = {q[b][kv].x, q[b][kv].y, q[b][kv].z, q[b][kv].w};
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[4];
+          q8_unpack4(w[i], f);
+          v[2 * i] = pack_bf16x2(f[0] * s[b][kv], f[1] * s[b][kv]);
+          v[2 * i + 1] = pack_bf16x2(f[2] * s[b][kv], f[3] * s[b][kv]);
+        }
+        __nv_bfloat16* o = (kv ? p.v_out : p.k_out) + out[b];
+        __stcs(reinterpret_cast<uint4*>(o), make_uint4(v[0], v[1], v[2], v[3]));
+        __stcs(reinterpret_cast<uint4*>(o + 8), make_uint4(v[4], v[5], v[6], v[7]));
       }
-      __nv_bfloat16* o = (kv ? p.v_out : p.k_out) + out;
-      *reinterpret_cast<uint4*>(o) = make_uint4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<uint4*>(o + 8) = make_uint4(v[4], v[5], v[6], v[7]);
     }
   }
 }

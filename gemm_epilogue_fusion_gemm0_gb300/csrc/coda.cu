@@ -1176,7 +1176,7 @@ cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t*
 // ---------------------------------------------------------------------------
 // The 8-bit paged cache (cache_q8.cuh, attn_q8.cuh)
 // ---------------------------------------------------------------------------
-constexpr int kFewMost = 32;  // packed rows of a sequence that go to the kernel for few
+constexpr int kFewMost = 48;  // packed rows of a sequence that go to the kernel for few
 constexpr int64_t kMaxSequences = 8192, kMaxHeads = 1024;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -1250,19 +1250,22 @@ coda_status_t rope_of(const double* inv_freq, const int32_t* axis, int64_t half,
   return CODA_OK;
 }
 
-// Parts of the attention's items: [cuts | maxima and sums | outputs], two parts per block
-size_t attn_ws_bytes(int tile_rows, int64_t D) {
-  return align256(kAttnMaxBlocks * sizeof(AttnCut)) +
-         align256(size_t(2) * kAttnMaxBlocks * tile_rows * sizeof(float2)) +
-         size_t(2) * kAttnMaxBlocks * tile_rows * D * sizeof(float);
+// Parts of the attention's items: [cuts | maxima and sums | outputs], two parts per block, of as many rows as
+// a tile may have (`rows`: packed rows of the call at most)
+int attn_ws_rows(int tile_rows, int64_t rows) { return static_cast<int>(std::min<int64_t>(tile_rows, rows)); }
+
+size_t attn_ws_bytes(int tile_rows, int64_t rows, int64_t D) {
+  const size_t parts = size_t(2) * kAttnMaxBlocks * attn_ws_rows(tile_rows, rows);
+  return align256(kAttnMaxBlocks * sizeof(AttnCut)) + align256(parts * sizeof(float2)) + align256(parts * D * sizeof(float));
 }
 
-AttnWs attn_ws(char* at, int tile_rows, int64_t D) {
+AttnWs attn_ws(char* at, int tile_rows, int64_t rows, int64_t D) {
   AttnWs w;
+  w.rows = attn_ws_rows(tile_rows, rows);
   w.cut = reinterpret_cast<AttnCut*>(at);
   at += align256(kAttnMaxBlocks * sizeof(AttnCut));
   w.ml = reinterpret_cast<float2*>(at);
-  at += align256(size_t(2) * kAttnMaxBlocks * tile_rows * sizeof(float2));
+  at += align256(size_t(2) * kAttnMaxBlocks * w.rows * sizeof(float2));
   w.o = reinterpret_cast<float*>(at);
   return w;
 }
@@ -1274,7 +1277,9 @@ AttnWs attn_ws(char* at, int tile_rows, int64_t D) {
 template <int kD>
 cudaError_t launch_attn(const AttnQ8Params& p, char* at, int64_t rows, int blocks, cudaStream_t stream) {
   const bool tiles = rows > kFewMost, few = !tiles || p.batch.B > 1;
-  const AttnWs wf = attn_ws(at, kFewRows, kD), wt = attn_ws(at + attn_ws_bytes(kFewRows, kD), kTileRows, kD);
+  const int64_t all = static_cast<int64_t>(p.batch.rows) * p.group;  // (a hint may be too small)
+  const AttnWs wf = attn_ws(at, kFewRows, all, kD);
+  const AttnWs wt = attn_ws(at + attn_ws_bytes(kFewRows, all, kD), kTileRows, kTileRows, kD);
   int k = 0;
   cudaError_t e = cudaSuccess;
   if (few) {
@@ -2113,7 +2118,8 @@ coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, const int8
 
 size_t coda_attn_q8_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
   if (check_heads(T, B, Hq, Hk, D) != CODA_OK || T == 0 || B == 0) return 0;
-  return kSlotBytes + attn_ws_bytes(kFewRows, D) + (T * (Hq / Hk) > kFewMost ? attn_ws_bytes(kTileRows, D) : 0);
+  const int64_t rows = T * (Hq / Hk);
+  return kSlotBytes + attn_ws_bytes(kFewRows, rows, D) + (rows > kFewMost ? attn_ws_bytes(kTileRows, kTileRows, D) : 0);
 }
 
 coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k_s, const int8_t* v_q,
