@@ -22,6 +22,16 @@ namespace coda {
 
 constexpr int kAttnUnit = 128;       // keys of the kernel for tiles
 constexpr int kFewUnit = 256;        // of the kernel for few
+constexpr int kFewRows = 16, kFewWarps = 8, kFewStages = 2;
+constexpr int kTileRows = 256, kTileThreads = 704;
+
+// What the deal knows of a kernel.  kLead: measured, 64 sequences' decoding and chunks of 500 tokens.
+struct FewDeal {
+  static constexpr int kRows = kFewRows, kUnit = kFewUnit, kThreads = 32 * kFewWarps, kLead = 1;
+};
+struct TileDeal {
+  static constexpr int kRows = kTileRows, kUnit = kAttnUnit, kThreads = kTileThreads, kLead = 3;
+};
 constexpr int kAttnMaxBlocks = 160;  // of the persistent grids
 
 struct AttnQ8Params {
@@ -63,9 +73,10 @@ __host__ __device__ inline int attn_extent(const AttnSeq& s, int group, int tile
   return keys <= 0 ? 0 : static_cast<int>(keys < places + 1 ? keys : places + 1);
 }
 
-template <int kUnit>
-__host__ __device__ inline int attn_units(int extent) {
-  return extent <= kUnit ? 1 : (extent + kUnit - 1) / kUnit;  // (an empty item still writes zeros)
+// An item counts its units and kLead more, for what it costs to begin and to end one.
+template <class K>
+__host__ __device__ inline int attn_cost(int extent) {
+  return K::kLead + (extent <= K::kUnit ? 1 : (extent + K::kUnit - 1) / K::kUnit);  // (an empty item still writes zeros)
 }
 
 __host__ __device__ inline int attn_tiles(const AttnSeq& s, int group, int tile_rows) {
@@ -81,15 +92,15 @@ __host__ __device__ inline bool attn_takes(const AttnDeal& d, const AttnSeq& s, 
   return s.n * group > d.lo && s.n * group <= d.hi;
 }
 
-// First unit of block c's share.
-__host__ __device__ inline int64_t attn_share(int64_t units, int c, int blocks) {
-  return units * c / blocks;
+// Where block c's share of the launch's cost begins.
+__host__ __device__ inline int64_t attn_share(int64_t cost, int c, int blocks) {
+  return cost * c / blocks;
 }
 
-// An item whose first part is the last of block c's share: what the join needs to know.
+// An item that begins in block c's share and does not end there: what the join needs to know.
 struct AttnCut {
-  int64_t units;    // of the launch
-  int64_t end;      // one past the item's last unit
+  int64_t cost;     // of the launch
+  int64_t end;      // where the item ends in it
   int b, hk, tile;
   int valid;
 };
@@ -110,72 +121,92 @@ struct AttnWalk {
   AttnSeq s;
   int b, hk;
   int tile, tiles;
-  int unit, units, extent;
+  int extent, cost;  // of the item
+  int at;            // how much of its cost has been taken, by this block and those before it
+  int unit, last;    // units of the piece in hand: unit .. last - 1
+  bool begins, ends;  // the piece has the item's first unit; its last
+  int64_t left;      // of the share
 };
 
-template <int kRows, int kUnit>
-__device__ __forceinline__ void walk_tile(AttnWalk& w, const AttnQ8Params& p, int places) {
-  w.extent = attn_extent(w.s, p.group, kRows, w.tile, places);
-  w.units = attn_units<kUnit>(w.extent);
+template <class K>
+__device__ __forceinline__ void walk_item(AttnWalk& w, const AttnQ8Params& p, int places) {
+  w.extent = attn_extent(w.s, p.group, K::kRows, w.tile, places);
+  w.cost = attn_cost<K>(w.extent);
 }
 
-// The next item (there is one), its first unit.
-template <int kRows, int kUnit>
-__device__ __forceinline__ void walk_item(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
-  w.unit = 0;
-  if (++w.tile == w.tiles) {
-    w.tile = 0;
-    if (++w.hk == p.cache.Hk) {
-      w.hk = 0;
-      do {
-        ++w.b;
-        if (w.b >= p.batch.B) return;  // (cu or lens written while the call runs)
-        w.s = load_seq(p, w.b);
-      } while (!attn_takes(d, w.s, p.group));
-      w.tiles = attn_tiles(w.s, p.group, kRows);
+// The next piece: the units of one item that lie in the share.  False at the share's end.  (A share that ends or
+// begins in what an item counts beyond its units has none of them, or all.)
+template <class K>
+__device__ __forceinline__ bool walk_piece(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
+  while (w.left > 0) {
+    if (w.at == w.cost) {
+      w.at = 0;
+      if (++w.tile == w.tiles) {
+        w.tile = 0;
+        if (++w.hk == p.cache.Hk) {
+          w.hk = 0;
+          do {
+            ++w.b;
+            if (w.b >= p.batch.B) return false;  // (cu or lens written while the call runs)
+            w.s = load_seq(p, w.b);
+          } while (!attn_takes(d, w.s, p.group));
+          w.tiles = attn_tiles(w.s, p.group, K::kRows);
+        }
+      }
+      walk_item<K>(w, p, places);
     }
+    const int rest = w.cost - w.at, n = w.left < rest ? static_cast<int>(w.left) : rest;
+    w.unit = max(w.at - K::kLead, 0);
+    w.last = max(w.at + n - K::kLead, 0);
+    w.at += n;
+    w.left -= n;
+    w.begins = w.unit == 0;
+    w.ends = n == rest;
+    if (w.unit < w.last) return true;
   }
-  walk_tile<kRows, kUnit>(w, p, places);
+  return false;
 }
 
-// The next unit (there is one).
-template <int kRows, int kUnit>
-__device__ __forceinline__ void walk_on(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
-  if (++w.unit == w.units) walk_item<kRows, kUnit>(w, p, d, places);
+// The next unit, in this piece or in the next.
+template <class K>
+__device__ __forceinline__ bool walk_unit(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places) {
+  return ++w.unit < w.last || walk_piece<K>(w, p, d, places);
 }
 
-// Units of a sequence for one key head, by a whole warp (0: another launch's sequence).
-template <int kRows, int kUnit>
-__device__ __forceinline__ int64_t seq_units(const AttnSeq& s, const AttnQ8Params& p, const AttnDeal& d,
-                                             int places, int lane) {
+// Cost of a sequence for one key head, by a whole warp (0: another launch's sequence).
+template <class K>
+__device__ __forceinline__ int64_t seq_cost(const AttnSeq& s, const AttnQ8Params& p, const AttnDeal& d, int places,
+                                            int lane) {
   if (!attn_takes(d, s, p.group)) return 0;
-  const int tiles = attn_tiles(s, p.group, kRows);
+  const int tiles = attn_tiles(s, p.group, K::kRows);
   int64_t u = 0;
-  for (int t = lane; t < tiles; t += 32) u += attn_units<kUnit>(attn_extent(s, p.group, kRows, t, places));
+  for (int t = lane; t < tiles; t += 32) u += attn_cost<K>(attn_extent(s, p.group, K::kRows, t, places));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
   return u;
 }
 
-// Adds up the units (all threads of the block, kThreads of them), and puts the walk at unit `u0`
-// of this block's share, which ends at u1.  Returns the launch's units.  A warp adds up a sequence at a
-// time, a lane a tile; `units` (shared memory, at least B numbers) holds the sequences' sums in between.
-template <int kRows, int kUnit, int kThreads>
+// Adds up the costs (all threads of the block), and puts the walk at the beginning of this block's share, before
+// its first piece.  Returns the launch's cost; `end`: where the share ends in it.  False in `some`: an empty share.  A
+// warp adds up a sequence at a time, a lane a tile; `costs` (shared memory, at least B numbers) holds the
+// sequences' sums in between.
+template <class K>
 __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p, const AttnDeal& d, int places,
-                                              int64_t* units, int64_t& u0, int64_t& u1) {
+                                              int64_t* costs, int64_t& end, bool& some) {
+  constexpr int kThreads = K::kThreads;
   __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ int64_t start_rest;
   __shared__ int start_b;
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   for (int b = warp; b < p.batch.B; b += kThreads / 32) {
-    const int64_t u = seq_units<kRows, kUnit>(load_seq(p, b), p, d, places, lane);
-    if (lane == 0) units[b] = u;
+    const int64_t u = seq_cost<K>(load_seq(p, b), p, d, places, lane);
+    if (lane == 0) costs[b] = u;
   }
   __syncthreads();
   const int per = (p.batch.B + kThreads - 1) / kThreads;
   const int b0 = min(p.batch.B, tid * per), b1 = min(p.batch.B, b0 + per);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units[b] * p.cache.Hk;
+  for (int b = b0; b < b1; ++b) mine += costs[b] * p.cache.Hk;
   int64_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -190,27 +221,28 @@ __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p
     if (i < warp) upto += warp_sum[i];
     total += warp_sum[i];
   }
-  u0 = attn_share(total, blockIdx.x, gridDim.x);
-  u1 = attn_share(total, blockIdx.x + 1, gridDim.x);
-  if (u0 < u1 && upto - mine <= u0 && u0 < upto) {  // one thread: u0 is in its sequences
-    int64_t rest = u0 - (upto - mine);
+  const int64_t begin = attn_share(total, blockIdx.x, gridDim.x);
+  end = attn_share(total, blockIdx.x + 1, gridDim.x);
+  some = begin < end;
+  if (some && upto - mine <= begin && begin < upto) {  // one thread: the share begins in its sequences
+    int64_t rest = begin - (upto - mine);
     int b = b0;
-    for (; rest >= units[b] * p.cache.Hk; ++b) rest -= units[b] * p.cache.Hk;
+    for (; rest >= costs[b] * p.cache.Hk; ++b) rest -= costs[b] * p.cache.Hk;
     start_b = b;
     start_rest = rest;
   }
   __syncthreads();
-  if (u0 >= u1) return total;
+  if (!some) return total;
   w.b = start_b;
   w.s = load_seq(p, w.b);
-  w.tiles = attn_tiles(w.s, p.group, kRows);
+  w.tiles = attn_tiles(w.s, p.group, K::kRows);
   int64_t rest = start_rest;
-  const int64_t per_head = units[w.b];
+  const int64_t per_head = costs[w.b];
   w.hk = static_cast<int>(rest / per_head);
   rest -= w.hk * per_head;
   for (w.tile = 0;; w.tile += 32) {  // 32 tiles at a time
     const int t = w.tile + lane;
-    const int u = t < w.tiles ? attn_units<kUnit>(attn_extent(w.s, p.group, kRows, t, places)) : 0;
+    const int u = t < w.tiles ? attn_cost<K>(attn_extent(w.s, p.group, K::kRows, t, places)) : 0;
     int64_t before = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -226,10 +258,16 @@ __device__ __forceinline__ int64_t walk_start(AttnWalk& w, const AttnQ8Params& p
     }
     rest -= __shfl_sync(0xffffffffu, before, 31);
   }
-  walk_tile<kRows, kUnit>(w, p, places);
-  w.unit = static_cast<int>(rest);
-  __syncthreads();  // `units` is read: its memory is free
+  walk_item<K>(w, p, places);
+  w.at = static_cast<int>(rest);
+  w.left = end - begin;
+  __syncthreads();  // `costs` is read: its memory is free
   return total;
+}
+
+// Tells the join of the item whose piece `w` is, if it begins here and ends elsewhere.
+__device__ __forceinline__ void tell_cut(const AttnWalk& w, AttnCut* cut, int64_t total, int64_t end) {
+  if (w.begins && !w.ends) *cut = AttnCut{total, end - w.left + (w.cost - w.at), w.b, w.hk, w.tile, 1};
 }
 
 // Row `packed` of a sequence's rows that share a key head: its row of q and its query head.
@@ -277,7 +315,6 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 // the largest value scale so far (rounded up to a power of two): the sums and outputs share it.  It moves, and the
 // outputs with it, only where p would pass 2^8.
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 16, kFewWarps = 8, kFewStages = 2;
 constexpr int kFewKeys = 16;                  // together: a page holds them
 constexpr int kFewApart = kFewKeys * kFewWarps;  // from a warp's first 16 keys of a unit to its second
 static_assert(kFewUnit == 2 * kFewApart, "a unit");
@@ -390,11 +427,11 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
   griddep_wait();
 
   AttnWalk w;
-  int64_t u0, u1;
-  const int64_t total = walk_start<kFewRows, kFewUnit, 32 * kFewWarps>(
-      w, p, deal, places, reinterpret_cast<int64_t*>(smem_few), u0, u1);
+  int64_t end;
+  bool some;
+  const int64_t total = walk_start<FewDeal>(w, p, deal, places, reinterpret_cast<int64_t*>(smem_few), end, some);
   if (threadIdx.x == 0) ws.cut[blockIdx.x].valid = 0;
-  if (u0 >= u1) return;
+  if (!some || !walk_piece<FewDeal>(w, p, deal, places)) return;
   const int mine = warp * kFewKeys;  // the warp's first key of a unit
   const int mask = (1 << p.cache.page_log2) - 1;
   AttnWalk ahead = w;
@@ -404,13 +441,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
     return key < a.extent && i < p.batch.width ? __ldg(p.batch.table + static_cast<size_t>(a.b) * p.batch.width + i) : -1;
   };
   int entry = entry_at(ahead);
-  int64_t issued = u0;
+  uint32_t issued = 0;
+  bool more = true;  // units to ask for
   constexpr int kChunks = kD / 16;
   // this thread's 16 codes of a copy: key kr (+ 32 / kChunks for the next), group kc
   const uint32_t kr = lane / kChunks, kc = lane % kChunks;
   const uint32_t lane_at = kr * kD + 16 * kc;
   const auto issue = [&]() {  // the unit `ahead` is at
-    const uint32_t st = ring + static_cast<uint32_t>(issued & (kFewStages - 1)) * Smem::kStage;
+    const uint32_t st = ring + (issued & (kFewStages - 1)) * Smem::kStage;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int key = ahead.unit * kFewUnit + mine + kFewApart * h;
@@ -434,14 +472,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(sc), "r"(0x7fffffff) : "memory");
       }
     }
-    if (++issued < u1) {
-      walk_on<kFewRows, kFewUnit>(ahead, p, deal, places);
-      entry = entry_at(ahead);
-    }
+    ++issued;
+    more = walk_unit<FewDeal>(ahead, p, deal, places);
+    if (more) entry = entry_at(ahead);
   };
 #pragma unroll
   for (int i = 0; i < kFewStages; ++i) {
-    if (issued < u1) issue();
+    if (more) issue();
     cp_async_commit();
   }
 
@@ -449,12 +486,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
   float acc[kTiles][4];
   float m[2], l[2], rf[2], base[2], lv;
   int limit[2];
-  bool fresh = true;
-  int64_t item = 0;  // its first unit
-  for (int64_t u = u0; u < u1; ++u) {
-    if (fresh) {  // a new item: its rows of q
-      fresh = false;
-      item = u - w.unit;
+  uint32_t n_unit = 0;
+  do {
+    {  // a piece of an item: its rows of q
       lv = kLeastScale;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -498,154 +532,155 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
     }
-    cp_async_wait<kFewStages - 1>();
-    __syncwarp();
-    const int key = w.unit * kFewUnit + mine;
-    if (key < w.extent) {
-      const bool two = key + kFewApart < w.extent;  // the second 16 too
-      const uint32_t st = ring + static_cast<uint32_t>(u & (kFewStages - 1)) * Smem::kStage;
-      float s[4][4] = {};  // of keys 8 n + 2 t + e of the first 16 (n = 0, 1) and of the second
+    for (; w.unit < w.last; ++w.unit, ++n_unit) {
+      cp_async_wait<kFewStages - 1>();
+      __syncwarp();
+      const int key = w.unit * kFewUnit + mine;
+      if (key < w.extent) {
+        const bool two = key + kFewApart < w.extent;  // the second 16 too
+        const uint32_t st = ring + (n_unit & (kFewStages - 1)) * Smem::kStage;
+        float s[4][4] = {};  // of keys 8 n + 2 t + e of the first 16 (n = 0, 1) and of the second
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        if (n >= 2 && !two) continue;
+        for (int n = 0; n < 4; ++n) {
+          if (n >= 2 && !two) continue;
 #pragma unroll
-        for (int h = 0; h < kD / 64; ++h) {
-          const uint4 c = ld_shared_v4(st + (n / 2) * Smem::kGroup + few_k_at<kD>(8 * (n & 1) + g, 4 * h + t));
-          const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+          for (int h = 0; h < kD / 64; ++h) {
+            const uint4 c = ld_shared_v4(st + (n / 2) * Smem::kGroup + few_k_at<kD>(8 * (n & 1) + g, 4 * h + t));
+            const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            q8_to_f16x2(word[i], b0, b1);
-            const uint32_t(&a)[4] = qa[4 * h + i];
-            mma_f16_16816(s[n], a[0], a[1], a[2], a[3], b0, b1);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b0, b1;
+              q8_to_f16x2(word[i], b0, b1);
+              const uint32_t(&a)[4] = qa[4 * h + i];
+              mma_f16_16816(s[n], a[0], a[1], a[2], a[3], b0, b1);
+            }
           }
         }
-      }
-      // their scales (those of the second 16, where there are none, are not looked at)
-      float ks[4][2], vs[4][2];
+        // their scales (those of the second 16, where there are none, are not looked at)
+        float ks[4][2], vs[4][2];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float* sc = reinterpret_cast<const float*>(smem_few + (st - smem_u32(smem_few)) + (n / 2) * Smem::kGroup +
-                                                         2 * Smem::kCodes) + 8 * (n & 1) + 2 * t;
-        const float2 a = *reinterpret_cast<const float2*>(sc), b = *reinterpret_cast<const float2*>(sc + 16);
-        ks[n][0] = a.x, ks[n][1] = a.y;
-        vs[n][0] = b.x, vs[n][1] = b.y;
-      }
-      const auto key_of = [&](int n, int e) { return key + kFewApart * (n / 2) + 8 * (n & 1) + 2 * t + e; };
-      const bool edge = key + kFewApart + kFewKeys - 1 > w.s.first + w.tile * kFewRows / p.group;
-      if (edge) {  // what lies behind the last key is not looked at
+        for (int n = 0; n < 4; ++n) {
+          const float* sc = reinterpret_cast<const float*>(smem_few + (st - smem_u32(smem_few)) + (n / 2) * Smem::kGroup +
+                                                           2 * Smem::kCodes) + 8 * (n & 1) + 2 * t;
+          const float2 a = *reinterpret_cast<const float2*>(sc), b = *reinterpret_cast<const float2*>(sc + 16);
+          ks[n][0] = a.x, ks[n][1] = a.y;
+          vs[n][0] = b.x, vs[n][1] = b.y;
+        }
+        const auto key_of = [&](int n, int e) { return key + kFewApart * (n / 2) + 8 * (n & 1) + 2 * t + e; };
+        const bool edge = key + kFewApart + kFewKeys - 1 > w.s.first + w.tile * kFewRows / p.group;
+        if (edge) {  // what lies behind the last key is not looked at
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (key_of(n, e) >= w.extent) vs[n][e] = 0.f;
-      }
-      float vm = 0.f, mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        vm = max3_abs(vm, vs[n][0], vs[n][1]);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) s[n][2 * r + e] *= ks[n][e] * rf[r];
-          if (edge) {
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (key_of(n, e) > limit[r]) s[n][2 * r + e] = -INFINITY;
-          }
-          mx[r] = max3(mx[r], s[n][2 * r], s[n][2 * r + 1]);
+              if (key_of(n, e) >= w.extent) vs[n][e] = 0.f;
         }
-      }
+        float vm = 0.f, mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) {
-        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-      }
-      lv = fmaxf(lv, scale_power(vm));
-      bool move = false;
+        for (int n = 0; n < 4; ++n) {
+          vm = max3_abs(vm, vs[n][0], vs[n][1]);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        m[r] = fmaxf(m[r], mx[r]);
-        move |= m[r] + lv > base[r] + 8.0f;
-      }
-      if (__any_sync(0xffffffffu, move)) {
-        float c[2];
+          for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[n][2 * r + e] *= ks[n][e] * rf[r];
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (key_of(n, e) > limit[r]) s[n][2 * r + e] = -INFINITY;
+            }
+            mx[r] = max3(mx[r], s[n][2 * r], s[n][2 * r + 1]);
+          }
+        }
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+        }
+        lv = fmaxf(lv, scale_power(vm));
+        bool move = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          c[r] = 1.0f;
-          if (m[r] + lv > base[r] + 8.0f) {
-            c[r] = ex2(base[r] - (m[r] + lv));
-            base[r] = m[r] + lv;
+          m[r] = fmaxf(m[r], mx[r]);
+          move |= m[r] + lv > base[r] + 8.0f;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          float c[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            c[r] = 1.0f;
+            if (m[r] + lv > base[r] + 8.0f) {
+              c[r] = ex2(base[r] - (m[r] + lv));
+              base[r] = m[r] + lv;
+            }
+            l[r] *= c[r];
           }
-          l[r] *= c[r];
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] *= c[e >> 1];
         }
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
+        for (int r = 0; r < 2; ++r) {
+          const float less = base[r] == -INFINITY ? 0.f : base[r];  // (no key seen yet)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[j][e] *= c[e >> 1];
-      }
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float less = base[r] == -INFINITY ? 0.f : base[r];  // (no key seen yet)
+            for (int e = 0; e < 2; ++e) {
+              const float x = ex2(s[n][2 * r + e] - less);
+              l[r] += x;
+              s[n][2 * r + e] = x * vs[n][e];
+            }
+        }
+        if (edge) {  // (a scale behind a row's last key may be NaN)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = ex2(s[n][2 * r + e] - less);
-            l[r] += x;
-            s[n][2 * r + e] = x * vs[n][e];
-          }
-      }
-      if (edge) {  // (a scale behind a row's last key may be NaN)
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key_of(n, e & 1) > limit[e >> 1]) s[n][e] = 0.f;
-      }
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (q == 1 && !two) continue;
-        const uint32_t a0 = pack_f16x2(s[2 * q][0], s[2 * q][1]), a1 = pack_f16x2(s[2 * q][2], s[2 * q][3]);
-        const uint32_t a2 = pack_f16x2(s[2 * q + 1][0], s[2 * q + 1][1]), a3 = pack_f16x2(s[2 * q + 1][2], s[2 * q + 1][3]);
-        uint32_t v[4][kD / 32];  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: kD / 8 values of each
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t r = 8 * (i >> 1) + 2 * t + (i & 1);
-          const uint32_t at = st + q * Smem::kGroup + Smem::kCodes;
-          if constexpr (kD == 128) {
-            const uint4 x = ld_shared_v4(at + few_v_at<kD>(r, g));
-            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-          } else {
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(v[i][0]), "=r"(v[i][1])
-                         : "r"(at + few_v_at<kD>(r, g >> 1) + 8u * (g & 1))
-                         : "memory");
-          }
+            for (int e = 0; e < 4; ++e)
+              if (key_of(n, e & 1) > limit[e >> 1]) s[n][e] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < kD / 32; ++i) {
-          uint32_t b[2][4];
+        for (int q = 0; q < 2; ++q) {
+          if (q == 1 && !two) continue;
+          const uint32_t a0 = pack_f16x2(s[2 * q][0], s[2 * q][1]), a1 = pack_f16x2(s[2 * q][2], s[2 * q][3]);
+          const uint32_t a2 = pack_f16x2(s[2 * q + 1][0], s[2 * q + 1][1]), a3 = pack_f16x2(s[2 * q + 1][2], s[2 * q + 1][3]);
+          uint32_t v[4][kD / 32];  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: kD / 8 values of each
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = v[2 * h][i] ^ 0x80808080u, y = v[2 * h + 1][i] ^ 0x80808080u;
-            const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
-            b[h][0] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4140));
-            b[h][1] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4342));
-            b[h][2] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4140));
-            b[h][3] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4342));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t r = 8 * (i >> 1) + 2 * t + (i & 1);
+            const uint32_t at = st + q * Smem::kGroup + Smem::kCodes;
+            if constexpr (kD == 128) {
+              const uint4 x = ld_shared_v4(at + few_v_at<kD>(r, g));
+              v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+            } else {
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                           : "=r"(v[i][0]), "=r"(v[i][1])
+                           : "r"(at + few_v_at<kD>(r, g >> 1) + 8u * (g & 1))
+                           : "memory");
+            }
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16_16816(acc[4 * i + j], a0, a1, a2, a3, b[0][j], b[1][j]);
+          for (int i = 0; i < kD / 32; ++i) {
+            uint32_t b[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t x = v[2 * h][i] ^ 0x80808080u, y = v[2 * h + 1][i] ^ 0x80808080u;
+              const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
+              b[h][0] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4140));
+              b[h][1] = q8_less_1152(__byte_perm(lo, 0x64646464u, 0x4342));
+              b[h][2] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4140));
+              b[h][3] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4342));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma_f16_16816(acc[4 * i + j], a0, a1, a2, a3, b[0][j], b[1][j]);
+          }
         }
       }
+      __syncwarp();  // the stage is read (and used: what was read is in registers)
+      if (more) issue();
+      cp_async_commit();
     }
-    __syncwarp();  // the stage is read (and used: what was read is in registers)
-    if (issued < u1) issue();
-    cp_async_commit();
-    const bool ends = w.unit == w.units - 1;
-    if (ends || u == u1 - 1) {
+    {
       // The warps' parts meet.
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -680,8 +715,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         }
       }
       __syncthreads();
-      const bool whole = ends && item >= u0;
-      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (item >= u0 ? 1 : 0);
+      const bool whole = w.begins && w.ends;
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.begins ? 1 : 0);
       for (int i = threadIdx.x; i < rows * (kD / 4); i += 32 * kFewWarps) {
         const int r = i / (kD / 4), c = i % (kD / 4);
         const int tt = c / kF4, at = kF4 * tt + ((c % kF4) ^ ((tt | (r & 1) << 2) & (kF4 - 1)));
@@ -704,12 +739,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
           if (c == 0) ws.ml[slot * ws.rows + r] = ml;
         }
       }
-      if (!ends && item >= u0 && threadIdx.x == 0)
-        ws.cut[blockIdx.x] = AttnCut{total, item + w.units, w.b, w.hk, w.tile, 1};
-      fresh = true;
+      if (threadIdx.x == 0) tell_cut(w, ws.cut + blockIdx.x, total, end);
     }
-    if (u + 1 < u1) walk_on<kFewRows, kFewUnit>(w, p, deal, places);
-  }
+  } while (walk_piece<FewDeal>(w, p, deal, places));
   cp_async_wait<0>();
 }
 
@@ -719,8 +751,6 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
 // four columns of a row over the parts, in order.  y = 0: of the launch for few; 1 ..: rows 16 (y - 1) ..
 // of the launch for tiles; of both in one launch.
 // ---------------------------------------------------------------------------
-constexpr int kTileRows = 256;  // of the kernel for tiles
-
 template <int kD>
 __global__ void __launch_bounds__(256)
     attn_q8_join_kernel(const AttnQ8Params p, const AttnWs few, const AttnWs tiles, int y0, int blocks) {
@@ -740,9 +770,9 @@ __global__ void __launch_bounds__(256)
   const int rows = min(kGroup, s.n * p.group - cut.tile * kRows - r0);
   if (rows <= 0) return;
   // blocks c .. c + parts - 1; one whose share is empty (fewer units than blocks) has no part
-  const int parts = static_cast<int>((cut.end * blocks + cut.units - 1) / cut.units) - c;
+  const int parts = static_cast<int>((cut.end * blocks + cut.cost - 1) / cut.cost) - c;
   for (int j = tid; j < parts; j += 256) {
-    const bool has = attn_share(cut.units, c + j, blocks) < attn_share(cut.units, c + j + 1, blocks);
+    const bool has = attn_share(cut.cost, c + j, blocks) < attn_share(cut.cost, c + j + 1, blocks);
     slots[j] = has ? 2 * (c + j) + (j == 0 ? 1 : 0) : -1;
   }
   __syncthreads();

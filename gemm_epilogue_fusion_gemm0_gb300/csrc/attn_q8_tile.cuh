@@ -30,7 +30,6 @@
 
 namespace coda {
 
-constexpr int kTileThreads = 704;
 constexpr int kTileStages = 2, kTileScales = 4;  // rings: of k's and v's tiles, of their scales
 constexpr int kRawStages = 3;                    // ring of halves of a unit's codes (64 keys of k or v)
 constexpr int kWideners = 4;                     // warps: 16 keys of a half each
@@ -216,11 +215,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   griddep_wait();
 
   AttnWalk w;
-  int64_t u0, u1;
-  const int64_t total =
-      walk_start<kTileRows, kAttnUnit, kTileThreads>(w, p, deal, places, reinterpret_cast<int64_t*>(smem), u0, u1);
+  int64_t end;
+  bool some;
+  const int64_t total = walk_start<TileDeal>(w, p, deal, places, reinterpret_cast<int64_t*>(smem), end, some);
   if (tid == 0) ws.cut[blockIdx.x].valid = 0;
-  if (u0 >= u1) return;
+  // (the first piece; each role walks the others by itself)
+  if (!some || !walk_piece<TileDeal>(w, p, deal, places)) return;
   if (tid == 0) {
     *abort_flag = 0u;
     for (uint32_t s = 0; s < kTileStages; ++s) {
@@ -255,7 +255,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   // (from one lane: known to be the same in the whole warp)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + Smem::kEnd), 0);
-  const uint32_t count = static_cast<uint32_t>(u1 - u0);
 
   if (warp >= 16 && warp < 20) {
     // ------------------------------------------------------------- widening
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) mbar_arrive(raw_empty(slot));
       return true;
     };
-    for (uint32_t i = 0; i < count; ++i) {
+    for (uint32_t i = 0; i == 0 || walk_unit<TileDeal>(w, p, deal, places); ++i) {
       const uint32_t st = i % kTileStages, ph = i / kTileStages & 1u;
       const uint32_t k = base + Smem::kK + st * Smem::kOperand, v = base + Smem::kV + st * Smem::kOperand;
       if (!warp_wait(k_empty(st), ph ^ 1u, kSiteAttn + 1) || !widen(k) || !widen(k + 64 * 128)) break;
@@ -318,8 +317,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     int entry = entry_at(w);
     uint32_t half = 0;
-    bool ok = true;
-    for (uint32_t i = 0; i < count; ++i) {
+    bool ok = true, more = true;
+    for (uint32_t i = 0; more; ++i) {
       const int key0 = w.unit * kAttnUnit, extent = w.extent, hk = w.hk;
       const bool bad = static_cast<unsigned>(entry) >= static_cast<unsigned>(p.cache.pages);
       if (bad && lane < kAttnUnit / keys && key0 + lane * keys < extent) atomicCAS(&g_coda_status, 0u, 0x200u | kChkPage);
@@ -354,10 +353,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       };
       ok = ask(p.cache.k_q, 0) && ask(p.cache.k_q, 1);
       if (!ok) break;
-      if (i + 1 < count) {
-        walk_on<kTileRows, kAttnUnit>(w, p, deal, places);
-        entry = entry_at(w);
-      }
+      more = walk_unit<TileDeal>(w, p, deal, places);
+      if (more) entry = entry_at(w);
       const auto given = [&](float s, int e) {  // nothing behind the last key is looked at; NaN for a page that does not exist
         return skey + e >= extent ? 0.f : spage < 0 ? __int_as_float(0x7fffffff) : s;
       };
@@ -410,20 +407,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     uint32_t i = 0;
     bool ok = true;
-    for (uint32_t items = 0; ok && i < count; ++items) {
-      const uint32_t end = i + min(static_cast<uint32_t>(w.units - w.unit), count - i);  // of the item here
+    for (uint32_t pieces = 0; pieces == 0 || walk_piece<TileDeal>(w, p, deal, places); ++pieces) {
+      const uint32_t stop = i + static_cast<uint32_t>(w.last - w.unit);
       uint32_t st = i % kTileStages;
-      ok = wait_all(q_full(0), items & 1u, kSiteAttn + 3) && wait_all(q_full(1), items & 1u, kSiteAttn + 3) &&
+      ok = wait_all(q_full(0), pieces & 1u, kSiteAttn + 3) && wait_all(q_full(1), pieces & 1u, kSiteAttn + 3) &&
            wait_all(k_full(st), i / kTileStages & 1u, kSiteAttn + 4);
       if (!ok) break;
       s_mma(0, st);
       s_mma(1, st);
       if (issuer) umma_commit(k_empty(st));
-      for (bool first = true; i < end; ++i, first = false) {
+      for (bool first = true; i < stop; ++i, first = false) {
         st = i % kTileStages;
         const uint32_t ph = i / kTileStages & 1u, uph = i & 1u;
         const uint32_t nst = (i + 1) % kTileStages, nph = (i + 1) / kTileStages & 1u;
-        const bool more = i + 1 < end;
+        const bool more = i + 1 < stop;
         ok = wait_all(v_full(st), ph, kSiteAttn + 5) && wait_all(p_full(0), uph, kSiteAttn + 6);
         if (!ok) break;
         o_mma(0, st, first);
@@ -441,7 +438,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (issuer) umma_commit(k_empty(nst));
         }
       }
-      if (ok && i < count) walk_item<kTileRows, kAttnUnit>(w, p, deal, places);
+      if (!ok) break;
     }
     // (no product is left in flight when the tensor memory is given back)
     if (issuer) umma_commit(drained);
@@ -455,39 +452,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const float* const scales = reinterpret_cast<const float*>(smem + Smem::kScale);
     uint32_t i = 0;
     bool ok = true;
-    while (ok && i < count) {
-      // an item, or what of it lies in this block's share
-      const uint32_t begin = i, end = i + min(static_cast<uint32_t>(w.units - w.unit), count - i);
+    do {
+      // a piece of an item
+      const uint32_t begin = i, stop = i + static_cast<uint32_t>(w.last - w.unit);
       const int packed = w.tile * kTileRows + static_cast<int>(128 * tl + r0);
       float rf[2];
-      {  // the rows of q, in fp16; two threads have half a row each
-        const uint32_t r = lane & 15, half = static_cast<uint32_t>(lane) >> 4;
-        const AttnRow row = attn_row(p, w.s, w.hk, packed + static_cast<int>(r));
-        Chunk8 c[kD / 16];
-        float amax = 0.f;
+      {  // The rows of q, in fp16: D / 8 lanes read a row, so a read is whole rows.
+        constexpr int kLanes = kD / 8, kPer = kD / 16;  // lanes of a row; reads, of 32 / kLanes rows each
+        const int c = lane % kLanes, up_row = lane / kLanes;
+        Chunk8 x[kPer];
 #pragma unroll
-        for (int j = 0; j < kD / 16; ++j) c[j] = ldg8(p.q + row.at * kD + kD / 2 * half + 8 * j);
+        for (int j = 0; j < kPer; ++j) {
+          const AttnRow row = attn_row(p, w.s, w.hk, packed + j * (32 / kLanes) + up_row);
+          x[j] = ldg8(p.q + row.at * kD + 8 * c);
+        }
+        float mine = 0.f;  // what row lane % 16 is multiplied by afterwards
 #pragma unroll
-        for (int j = 0; j < kD / 16; ++j) {
-          float v[8];
-          unpack8(c[j], v);
+        for (int j = 0; j < kPer; ++j) {
+          float v[8], amax = 0.f;
+          unpack8(x[j], v);
 #pragma unroll
           for (int e = 0; e < 8; e += 2) amax = max3_abs_nan(amax, v[e], v[e + 1]);
-        }
-        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
-        float up, down;
-        row_power(amax, up, down);
-        down *= p.scale_log2;
-        rf[0] = __shfl_sync(0xffffffffu, down, g);
-        rf[1] = __shfl_sync(0xffffffffu, down, g + 8);
 #pragma unroll
-        for (int j = 0; j < kD / 16; ++j) {
-          float v[8];
-          unpack8(c[j], v);
-          st_shared_v4(base + Smem::kQ + tl * Smem::kOperand + panel_at(r0 + r, kD / 16 * half + j),
+          for (int o = kLanes / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          float up, down;
+          row_power(amax, up, down);
+          const float got = __shfl_sync(0xffffffffu, down, lane % (32 / kLanes) * kLanes);
+          if ((lane & 15) / (32 / kLanes) == j) mine = got;
+          st_shared_v4(base + Smem::kQ + tl * Smem::kOperand + panel_at(r0 + j * (32 / kLanes) + up_row, c),
                        pack_f16x2(v[0] * up, v[1] * up), pack_f16x2(v[2] * up, v[3] * up),
                        pack_f16x2(v[4] * up, v[5] * up), pack_f16x2(v[6] * up, v[7] * up));
         }
+        mine *= p.scale_log2;
+        rf[0] = __shfl_sync(0xffffffffu, mine, g);
+        rf[1] = __shfl_sync(0xffffffffu, mine, g + 8);
       }
       fence_async_smem();
       __syncwarp();
@@ -502,7 +500,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         sum[k] = 0;
       }
       int key = w.unit * kAttnUnit;
-      for (; i < end; ++i, key += kAttnUnit) {
+      for (; i < stop; ++i, key += kAttnUnit) {
         const uint32_t uph = i & 1u, sl = i % kTileScales;
         ok = warp_wait(sc_full(sl), i / kTileScales & 1u, kSiteAttn + 8) && warp_wait(s_full(tl), uph, kSiteAttn + 9);
         if (!ok) break;
@@ -578,36 +576,65 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = warp_wait(pv_done(tl), (i - 1) & 1u, kSiteAttn + 10);
       if (!ok) break;
       tc_fence_after();
-      const bool begins = w.unit == 0, ends = w.unit + static_cast<int>(end - begin) == w.units;
-      const bool whole = begins && ends;
-      const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (begins ? 1 : 0)) * kTileRows + 128 * tl + r0;
+      const bool whole = w.begins && w.ends;
+      const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (w.begins ? 1 : 0)) * kTileRows + 128 * tl + r0;
+      // The outputs go through the warp's rows of q's place, which the products have left, so that whole rows, or
+      // halves of them in fp32, are written at a time.
+      const uint32_t stage = base + Smem::kQ + tl * Smem::kOperand;
+      const int in_rows = min(16, max(0, w.s.n * p.group - packed));
 #pragma unroll 1
       for (int c = 0; c < kD; c += 64) {
         uint32_t v[32];
         tmem_ld_16x64(to + c, v);
         tmem_ld_wait(v);
+        if (whole) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float inv = l[k] == 0.f ? 0.f : 1.0f / l[k];
-          if (whole) {
-            // Two threads exchange, so that each has four neighbouring columns (of one 8, or of the next) and four
-            // threads write 32 bytes of a row.
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const uint32_t x = pack_bf16x2(__uint_as_float(v[4 * j + 2 * k]) * inv, __uint_as_float(v[4 * j + 2 * k + 1]) * inv);
-              const uint32_t y = pack_bf16x2(__uint_as_float(v[4 * j + 4 + 2 * k]) * inv,
-                                             __uint_as_float(v[4 * j + 4 + 2 * k + 1]) * inv);
-              const bool odd = lane & 1;
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
-              if (row[k].in)
-                *reinterpret_cast<uint2*>(p.o + row[k].at * kD + c + 8 * (j + (odd ? 1 : 0)) + 2 * (lane & 2)) =
-                    odd ? make_uint2(got, y) : make_uint2(x, got);
-            }
-          } else if (row[k].in) {
+          for (int k = 0; k < 2; ++k) {
+            const float inv = l[k] == 0.f ? 0.f : 1.0f / l[k];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint2*>(ws.o + (slot + g + 8 * k) * kD + c + 8 * j + t2) =
-                  make_uint2(v[4 * j + 2 * k], v[4 * j + 2 * k + 1]);
+              st_shared_u32(stage + panel_at(r0 + g + 8 * k, c / 8 + j) + 2 * t2,
+                            pack_bf16x2(__uint_as_float(v[4 * j + 2 * k]) * inv, __uint_as_float(v[4 * j + 2 * k + 1]) * inv));
+          }
+        } else {
+          // 16 rows of 256 bytes: 32 columns in one panel's row, 32 in the other's (D = 64: in the row of another 16)
+          const auto place = [&](uint32_t r, uint32_t c16) {  // the 16-byte group c16 of row r
+            return kD == 128 ? stage + panel_at(r0 + r, c16)
+                             : stage + (r0 + r) * 128u + (((c16 & 7u) ^ (r & 7u)) << 4);
+          };
+#pragma unroll
+          for (int b = 0; b < (kD == 128 ? 1 : 2); ++b) {
+            if (b > 0) __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                if (kD == 64 && j / 4 != b) continue;
+                const uint32_t at = place(g + 8 * k, 2 * j + (t2 >> 2)) + 4 * (t2 & 2);
+                st_shared_u32(at, v[4 * j + 2 * k]);
+                st_shared_u32(at + 4, v[4 * j + 2 * k + 1]);
+              }
+            __syncwarp();
+            constexpr int kLanes = kD == 128 ? 16 : 8;  // of a row
+#pragma unroll
+            for (int j = 0; j < 16 * kLanes / 32; ++j) {
+              const int r = j * (32 / kLanes) + lane / kLanes, c16 = lane % kLanes;
+              if (r < in_rows)
+                *reinterpret_cast<uint4*>(ws.o + (slot + r) * kD + c + 32 * b + 4 * c16) = ld_shared_v4(place(r, c16));
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (whole) {
+        __syncwarp();
+        constexpr int kLanes = kD / 8;
+#pragma unroll
+        for (int j = 0; j < kD / 16; ++j) {
+          const int r = j * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
+          if (r < in_rows) {
+            const AttnRow at = attn_row(p, w.s, w.hk, packed + r);
+            *reinterpret_cast<uint4*>(p.o + at.at * kD + 8 * c) = ld_shared_v4(stage + panel_at(r0 + r, c));
           }
         }
         __syncwarp();
@@ -621,10 +648,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             p.lse[row[k].at] = attn_lse(bs[k], l[k]);
         }
       tc_fence_before();
-      if (begins && !ends && tid == 0)
-        ws.cut[blockIdx.x] = AttnCut{total, u0 + begin + w.units, w.b, w.hk, w.tile, 1};
-      if (i < count) walk_item<kTileRows, kAttnUnit>(w, p, deal, places);
-    }
+      if (tid == 0) tell_cut(w, ws.cut + blockIdx.x, total, end);
+    } while (walk_piece<TileDeal>(w, p, deal, places));
   }
   tc_fence_before();
   __syncthreads();
