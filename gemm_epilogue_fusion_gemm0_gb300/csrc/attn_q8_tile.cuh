@@ -3,23 +3,24 @@
 //
 // A block holds two tiles of 128 rows of q (fp16, shared memory) and walks the keys 128 at a time:
 //   S_w = q_w k^T     128 x 128, tensor memory, fp32     (w = 0, 1: the two tiles)
-//   P_w = 2^(S_w scale - base) * v's scale, fp16, over the first half of S_w
+//   P_w = 2^(S_w scale - base) * v's scale, fp16, over the first half of S_w's columns of the same keys
 //   o_w += P_w v      128 x D, tensor memory; P_w is the first operand, from tensor memory
+// in two halves of 64 keys each, so that a tile's softmax has one half to work at while the products of the other
+// run (with all 128 together it waited for them: 4900 cycles a unit, of which the softmax was 2800).
 // The tensor cores see codes widened to fp16 (exact); k's scales multiply S's columns and v's P's, in the
 // softmax.  Bound by the tensor cores: 4 * 256 * 128 * D operations per unit, 2048 cycles for D = 128; its 32768
 // exponentials are half of that, and the widening of 32768 codes, once per 256 rows, a fifth of the issue slots.
 //
 // One block of 704 threads per SM:
-//   warps 0..7, 8..15  softmax of tile 0, 1: a warp has 16 rows, a thread 32 columns of two of them.  S is read
-//                      twice, for the maximum and for the exponentials.  (Four such warps to a quarter of the SM:
+//   warps 0..7, 8..15  softmax of tile 0, 1: a warp has 16 rows, a thread 16 columns of a half of two of them.  (Four
+//                      such warps to a quarter of the SM:
 //                      the steps of an exponential depend on one another, and one warp alone takes 660 cycles for 32
 //                      of them in 32 lanes, two 740, four 1100.)
 //   warps 16..19       widen k and v: codes from a ring that bulk copies fill, fp16 to the rings of two tiles each that
 //                      the products read.  (With codes loaded to registers a unit ahead, by these warps, the softmax had
 //                      none to keep its steps in flight; asked for by these warps, five copies a unit took each
 //                      of them 2350 cycles.)
-//   warp 20            issues tcgen05.mma:  S_0(j + 1) behind P_0(j) v, S_1(j + 1) behind P_1(j) v, so that
-//                      one tile's softmax runs beside the other's products
+//   warp 20            issues tcgen05.mma: of each half of each tile, P v of a unit, then S of the next
 //   warp 21            looks up pages, asks for their codes and puts a unit's scales into shared memory
 // o is rescaled only where a row's maximum has grown by more than 2^8 (P stays below fp16's largest): hardly ever
 // after the first units.
@@ -31,6 +32,7 @@
 namespace coda {
 
 constexpr int kTileStages = 2, kTileScales = 4;  // rings: of k's and v's tiles, of their scales
+static_assert(kTileStages == 2, "the stage behind one is the other");
 constexpr int kRawStages = 3;                    // ring of halves of a unit's codes (64 keys of k or v)
 constexpr int kWideners = 4;                     // warps: 16 keys of a half each
 constexpr uint32_t kSiteAttn = 12;               // of bounded waits: kSiteAttn + which
@@ -46,7 +48,7 @@ struct TileSmem {
   static constexpr uint32_t kRawBytes = 64 * kD;
   static constexpr uint32_t kRaw = (kScale + kTileScales * kScaleSlot + 127) / 128 * 128;
   static constexpr uint32_t kBar = kRaw + kRawStages * kRawBytes;
-  static constexpr uint32_t kBars = 4 * kTileStages + 2 * kTileScales + 8 + 1 + 2 * kRawStages;
+  static constexpr uint32_t kBars = 4 * kTileStages + 2 * kTileScales + 14 + 1 + 2 * kRawStages;
   static constexpr uint32_t kEnd = kBar + 8 * kBars;  // tensor memory's address, the abort flag
   static constexpr uint32_t kUsed = kEnd + 16;
   // (the sequences' units at the start take the place of q, k and v)
@@ -78,16 +80,21 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&v)[32])
         "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&v)[32]) {
+// The same for 32 columns.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
-      "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
 }
 
 // 16 lanes x 32 columns: thread (g, t) writes column 4 i + t of lane g from v[2 i] and of lane g + 8 from v[2 i + 1].
@@ -111,72 +118,61 @@ __device__ __forceinline__ uint32_t panel_at(uint32_t row, uint32_t c) {
   return (c >> 3) * 16384u + row * 128u + (((c & 7u) ^ (row & 7u)) << 4);
 }
 
-// The softmax's two walks over a warp's 16 rows of S, 64 columns at a time.  A thread has 16 columns of two rows, so
-// a column's scale, read once, serves two products (with a row to a thread, the reads of scales alone took as
-// long on shared memory as the operands of the products).  `ts`: the warp's place in tensor memory.  `sc`: k's 128
-// scales (v's 128 numbers on) from column 2 t.  kEdge: row k sees columns 0 .. seen[k] of those from 2 t on.
+// The softmax of 64 columns of a warp's 16 rows.  A thread has 16 columns of two rows, so a column's scale, read
+// once, serves two products (with a row to a thread, the reads of scales alone took as long on shared memory as the
+// operands of the products).  `sc`: k's scales (v's 128 numbers on) from the thread's first column.  kEdge: row k
+// sees columns 0 .. seen[k] of those from there on.
+
+// S times k's scales, and its largest.
 template <bool kEdge>
-__device__ __forceinline__ void largest_scores(uint32_t ts, const float* sc, const int (&seen)[2], float (&mx)[2]) {
-#pragma unroll 1
-  for (int c = 0; c < 128; c += 64) {
-    uint32_t v[32];
-    tmem_ld_16x64(ts + c, v);
-    tmem_ld_wait(v);
+__device__ __forceinline__ void scaled(uint32_t (&v)[32], const float* sc, const int (&seen)[2], float (&mx)[2]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 k2 = *reinterpret_cast<const float2*>(sc + c + 8 * i);
+  for (int i = 0; i < 8; ++i) {
+    const float2 k2 = *reinterpret_cast<const float2*>(sc + 8 * i);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x, y;
-        unpack2(mul2(pack2(__uint_as_float(v[4 * i + 2 * k]), __uint_as_float(v[4 * i + 2 * k + 1])), pack2(k2.x, k2.y)),
-                x, y);
-        if constexpr (kEdge) {
-          if (c + 8 * i > seen[k]) x = -INFINITY;
-          if (c + 8 * i + 1 > seen[k]) y = -INFINITY;
-        }
-        mx[k] = max3(mx[k], x, y);
+    for (int k = 0; k < 2; ++k) {
+      float x, y;
+      unpack2(mul2(pack2(__uint_as_float(v[4 * i + 2 * k]), __uint_as_float(v[4 * i + 2 * k + 1])), pack2(k2.x, k2.y)),
+              x, y);
+      if constexpr (kEdge) {
+        if (8 * i > seen[k]) x = -INFINITY;
+        if (8 * i + 1 > seen[k]) y = -INFINITY;
       }
+      mx[k] = max3(mx[k], x, y);
+      v[4 * i + 2 * k] = __float_as_uint(x);
+      v[4 * i + 2 * k + 1] = __float_as_uint(y);
     }
   }
 }
 
-// P = 2^(S k's scale rf - less) v's scale, in fp16 over columns of S that have been read; the sums without v's.
+// P = 2^(what `scaled` left * rf - less) v's scale in fp16; the sums without v's scale.
 template <bool kEdge>
-__device__ __forceinline__ void weights(uint32_t ts, const float* sc, const int (&seen)[2], const float (&rf)[2],
-                                        const float (&less)[2], uint64_t (&sum)[2]) {
-#pragma unroll 1
-  for (int c = 0; c < 128; c += 64) {
-    uint32_t v[32], pk[16];
-    tmem_ld_16x64(ts + c, v);
-    tmem_ld_wait(v);
+__device__ __forceinline__ void weights(const uint32_t (&v)[32], const float* sc, const int (&seen)[2], const float (&rf)[2],
+                                        const float (&less)[2], uint32_t (&pk)[16], uint64_t (&sum)[2]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 k2 = *reinterpret_cast<const float2*>(sc + c + 8 * i);
-      const float2 v2 = *reinterpret_cast<const float2*>(sc + 128 + c + 8 * i);
+  for (int i = 0; i < 8; ++i) {
+    const float2 v2 = *reinterpret_cast<const float2*>(sc + 128 + 8 * i);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x, y;
-        unpack2(fma2(mul2(pack2(__uint_as_float(v[4 * i + 2 * k]), __uint_as_float(v[4 * i + 2 * k + 1])),
-                          pack2(k2.x, k2.y)),
-                     pack2(rf[k], rf[k]), pack2(-less[k], -less[k])),
-                x, y);
-        x = ex2(x);
-        y = ex2(y);
-        if constexpr (kEdge) {
-          if (c + 8 * i > seen[k]) x = 0.f;
-          if (c + 8 * i + 1 > seen[k]) y = 0.f;
-        }
-        const uint64_t xy = pack2(x, y);
-        sum[k] = add2(sum[k], xy);
-        unpack2(mul2(xy, pack2(v2.x, v2.y)), x, y);
-        if constexpr (kEdge) {  // (a scale behind the row's last key may be NaN)
-          if (c + 8 * i > seen[k]) x = 0.f;
-          if (c + 8 * i + 1 > seen[k]) y = 0.f;
-        }
-        pk[2 * i + k] = pack_f16x2(x, y);
+    for (int k = 0; k < 2; ++k) {
+      float x, y;
+      unpack2(fma2(pack2(__uint_as_float(v[4 * i + 2 * k]), __uint_as_float(v[4 * i + 2 * k + 1])), pack2(rf[k], rf[k]),
+                   pack2(-less[k], -less[k])),
+              x, y);
+      x = ex2(x);
+      y = ex2(y);
+      if constexpr (kEdge) {
+        if (8 * i > seen[k]) x = 0.f;
+        if (8 * i + 1 > seen[k]) y = 0.f;
       }
+      const uint64_t xy = pack2(x, y);
+      sum[k] = add2(sum[k], xy);
+      unpack2(mul2(xy, pack2(v2.x, v2.y)), x, y);
+      if constexpr (kEdge) {  // (a scale behind the row's last key may be NaN)
+        if (8 * i > seen[k]) x = 0.f;
+        if (8 * i + 1 > seen[k]) y = 0.f;
+      }
+      pk[2 * i + k] = pack_f16x2(x, y);
     }
-    tmem_st_16x128b_x8(ts + c / 2, pk);
   }
 }
 
@@ -198,13 +194,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const auto sc_full = [&](uint32_t s) { return bars + 8u * (4 * kTileStages + s); };
   const auto sc_empty = [&](uint32_t s) { return bars + 8u * (4 * kTileStages + kTileScales + s); };
   constexpr uint32_t kB = 4 * kTileStages + 2 * kTileScales;
-  const auto s_full = [&](uint32_t w) { return bars + 8u * (kB + w); };       // S_w is there
-  const auto p_full = [&](uint32_t w) { return bars + 8u * (kB + 2 + w); };   // P_w is there
-  const auto pv_done = [&](uint32_t w) { return bars + 8u * (kB + 4 + w); };  // o_w has P_w v
-  const auto q_full = [&](uint32_t w) { return bars + 8u * (kB + 6 + w); };
-  const uint32_t drained = bars + 8u * (kB + 8);
-  const auto raw_full = [&](uint32_t i) { return bars + 8u * (kB + 9 + i); };
-  const auto raw_empty = [&](uint32_t i) { return bars + 8u * (kB + 9 + kRawStages + i); };
+  // w: 2 * tile + half of the unit's keys
+  const auto s_full = [&](uint32_t w) { return bars + 8u * (kB + w); };       // S is there
+  const auto p_full = [&](uint32_t w) { return bars + 8u * (kB + 4 + w); };   // P is there
+  const auto pv_done = [&](uint32_t w) { return bars + 8u * (kB + 8 + w); };  // o has P v
+  const auto q_full = [&](uint32_t t) { return bars + 8u * (kB + 12 + t); };
+  const uint32_t drained = bars + 8u * (kB + 14);
+  const auto raw_full = [&](uint32_t i) { return bars + 8u * (kB + 15 + i); };
+  const auto raw_empty = [&](uint32_t i) { return bars + 8u * (kB + 15 + kRawStages + i); };
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Smem::kEnd + 4);
   const WaitCtl wc{timeout_ns, &g_coda_status, abort_flag};
   // a whole warp waits, and gives up, together
@@ -233,12 +230,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(sc_full(s), 1);
       mbar_init(sc_empty(s), 16);
     }
-    for (uint32_t i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < 4; ++i) {
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), 8);
       mbar_init(pv_done(i), 1);
-      mbar_init(q_full(i), 8);
     }
+    for (uint32_t i = 0; i < 2; ++i) mbar_init(q_full(i), 8);
     mbar_init(drained, 1);
     for (uint32_t i = 0; i < kRawStages; ++i) {
       mbar_init(raw_full(i), 1);
@@ -380,25 +377,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else if (warp == 20) {
     // ------------------------------------------------------------- products
     const bool issuer = elect_one();
-    constexpr uint32_t kIdescS = idesc_f16_f32(128, 128);
+    constexpr uint32_t kIdescS = idesc_f16_f32(128, 64);
     constexpr uint32_t kIdescO = idesc_f16_f32(128, kD) | (1u << 16);  // v: rows are k
-    const auto s_mma = [&](uint32_t t, uint32_t st) {
+    // Descriptors are sums of constants and of what is known to be the same in the whole warp (`stage`: from one
+    // lane), so that an instruction's operands are in uniform registers: 60 cycles each where they were not.
+    const uint64_t dq = sdesc_sw128(base + Smem::kQ, 16, 1024), dk = sdesc_sw128(base + Smem::kK, 16, 1024);
+    const uint64_t dv = sdesc_sw128(base + Smem::kV, 16384, 1024);
+    const auto stage = [&](uint32_t i) { return __shfl_sync(0xffffffffu, i % kTileStages, 0); };
+    const auto s_mma = [&](uint32_t t, uint32_t h, uint32_t st) {
+      const uint64_t a = dq + t * (Smem::kOperand >> 4), b = dk + st * (Smem::kOperand >> 4) + h * (8192u >> 4);
 #pragma unroll
       for (uint32_t k = 0; k < kD / 16; ++k) {
-        const uint32_t off = (k / 4) * 16384u + (k % 4) * 32u;
-        const uint64_t a = sdesc_sw128(base + Smem::kQ + t * Smem::kOperand + off, 16, 1024);
-        const uint64_t b = sdesc_sw128(base + Smem::kK + st * Smem::kOperand + off, 16, 1024);
-        if (issuer) umma_bf16(tmem + 128u * t, a, b, kIdescS, k > 0);
+        const uint32_t off = ((k / 4) * 16384u + (k % 4) * 32u) >> 4;
+        if (issuer) umma_bf16(tmem + 128u * t + 64u * h, a + off, b + off, kIdescS, k > 0);
       }
-      if (issuer) umma_commit(s_full(t));
+      if (issuer) umma_commit(s_full(2 * t + h));
     };
-    const auto o_mma = [&](uint32_t t, uint32_t st, bool first) {
+    const auto o_mma = [&](uint32_t t, uint32_t h, uint32_t st, bool first) {
+      const uint64_t b = dv + st * (Smem::kOperand >> 4) + h * (8192u >> 4);
 #pragma unroll
-      for (uint32_t k = 0; k < 8; ++k) {
-        const uint64_t b = sdesc_sw128(base + Smem::kV + st * Smem::kOperand + k * 2048u, 16384, 1024);
-        if (issuer) umma_f16_ts(tmem + 256u + kD * t, tmem + 128u * t + 8u * k, b, kIdescO, !first || k > 0);
-      }
-      if (issuer) umma_commit(pv_done(t));
+      for (uint32_t k = 0; k < 4; ++k)
+        if (issuer)
+          umma_f16_ts(tmem + 256u + kD * t, tmem + 128u * t + 64u * h + 8u * k, b + k * (2048u >> 4), kIdescO,
+                      !first || k > 0);
+      if (issuer) umma_commit(pv_done(2 * t + h));
     };
     const auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) {
       const bool ok = warp_wait(bar, parity, site);
@@ -409,34 +411,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     for (uint32_t pieces = 0; pieces == 0 || walk_piece<TileDeal>(w, p, deal, places); ++pieces) {
       const uint32_t stop = i + static_cast<uint32_t>(w.last - w.unit);
-      uint32_t st = i % kTileStages;
+      uint32_t st = stage(i);
       ok = wait_all(q_full(0), pieces & 1u, kSiteAttn + 3) && wait_all(q_full(1), pieces & 1u, kSiteAttn + 3) &&
            wait_all(k_full(st), i / kTileStages & 1u, kSiteAttn + 4);
       if (!ok) break;
-      s_mma(0, st);
-      s_mma(1, st);
+#pragma unroll
+      for (uint32_t w4 = 0; w4 < 4; ++w4) s_mma(w4 & 1, w4 >> 1, st);
       if (issuer) umma_commit(k_empty(st));
       for (bool first = true; i < stop; ++i, first = false) {
-        st = i % kTileStages;
+        st = stage(i);
         const uint32_t ph = i / kTileStages & 1u, uph = i & 1u;
-        const uint32_t nst = (i + 1) % kTileStages, nph = (i + 1) / kTileStages & 1u;
+        const uint32_t nst = st ^ 1u, nph = (i + 1) / kTileStages & 1u;
         const bool more = i + 1 < stop;
-        ok = wait_all(v_full(st), ph, kSiteAttn + 5) && wait_all(p_full(0), uph, kSiteAttn + 6);
+        ok = wait_all(v_full(st), ph, kSiteAttn + 5);
         if (!ok) break;
-        o_mma(0, st, first);
-        if (more) {
-          ok = wait_all(k_full(nst), nph, kSiteAttn + 4);
+#pragma unroll
+        for (uint32_t w4 = 0; w4 < 4; ++w4) {
+          const uint32_t t = w4 & 1, h = w4 >> 1;
+          ok = wait_all(p_full(2 * t + h), uph, kSiteAttn + 6);
           if (!ok) break;
-          s_mma(0, nst);
+          o_mma(t, h, st, first && h == 0);
+          if (w4 == 3 && issuer) umma_commit(v_empty(st));
+          if (more) {
+            if (w4 == 0) {
+              ok = wait_all(k_full(nst), nph, kSiteAttn + 4);
+              if (!ok) break;
+            }
+            s_mma(t, h, nst);
+            if (w4 == 3 && issuer) umma_commit(k_empty(nst));
+          }
         }
-        ok = wait_all(p_full(1), uph, kSiteAttn + 6);
         if (!ok) break;
-        o_mma(1, st, first);
-        if (issuer) umma_commit(v_empty(st));
-        if (more) {
-          s_mma(1, nst);
-          if (issuer) umma_commit(k_empty(nst));
-        }
       }
       if (!ok) break;
     }
@@ -492,76 +497,84 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) mbar_arrive(q_full(tl));
       const AttnRow row[2] = {attn_row(p, w.s, w.hk, packed + g), attn_row(p, w.s, w.hk, packed + g + 8)};
       const int low = __shfl_sync(0xffffffffu, row[0].limit, 0);  // the smallest of the warp's rows
-      float m[2], bs[2], lv = kLeastScale;
+      float bs[2];
       uint64_t sum[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        m[k] = bs[k] = -INFINITY;
+        bs[k] = -INFINITY;
         sum[k] = 0;
       }
       int key = w.unit * kAttnUnit;
-      for (; i < stop; ++i, key += kAttnUnit) {
+      for (; ok && i < stop; ++i, key += kAttnUnit) {
         const uint32_t uph = i & 1u, sl = i % kTileScales;
-        ok = warp_wait(sc_full(sl), i / kTileScales & 1u, kSiteAttn + 8) && warp_wait(s_full(tl), uph, kSiteAttn + 9);
+        ok = warp_wait(sc_full(sl), i / kTileScales & 1u, kSiteAttn + 8);
         if (!ok) break;
-        tc_fence_after();
         const float* const sc = scales + sl * (Smem::kScaleSlot / 4);
+        const float lv = scale_power(sc[256]);
         const bool edge = key + kAttnUnit - 1 > low;
-        const int seen[2] = {row[0].limit - t2 - key, row[1].limit - t2 - key};
-        float mx[2] = {-INFINITY, -INFINITY};
-        if (edge)
-          largest_scores<true>(ts, sc + t2, seen, mx);
-        else
-          largest_scores<false>(ts, sc + t2, seen, mx);
-        lv = fmaxf(lv, scale_power(sc[256]));
-        // What is taken out of the exponents: moved where P would leave fp16.
-        bool move = false;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-          mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-          m[k] = fmaxf(m[k], mx[k] == -INFINITY ? mx[k] : mx[k] * rf[k]);
-          move |= m[k] + lv > bs[k] + 8.0f;
-        }
-        if (__any_sync(0xffffffffu, move)) {
-          float corr[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            corr[k] = 1.0f;
-            if (m[k] + lv > bs[k] + 8.0f) {
-              corr[k] = ex2(bs[k] - (m[k] + lv));
-              bs[k] = m[k] + lv;
-            }
-            sum[k] = mul2(sum[k], pack2(corr[k], corr[k]));
-          }
-          if (i > begin) {
-            ok = warp_wait(pv_done(tl), uph ^ 1u, kSiteAttn + 10);
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kD; c += 64) {
-              uint32_t v[32];
-              tmem_ld_16x64(to + c, v);
-              tmem_ld_wait(v);
+        for (uint32_t h = 0; h < 2; ++h) {
+          ok = warp_wait(s_full(2 * tl + h), uph, kSiteAttn + 9);
+          if (!ok) break;
+          tc_fence_after();
+          const float* const hsc = sc + 64 * h + t2;
+          const int before = t2 + key + 64 * static_cast<int>(h);
+          const int seen[2] = {row[0].limit - before, row[1].limit - before};
+          uint32_t v[32];
+          tmem_ld_16x64(ts + 64u * h, v);
+          tmem_ld_wait(v);
+          float mx[2] = {-INFINITY, -INFINITY};
+          if (edge)
+            scaled<true>(v, hsc, seen, mx);
+          else
+            scaled<false>(v, hsc, seen, mx);
+          // What is taken out of the exponents moves where P would leave fp16: to the row's largest score of these
+          // keys and log2 of the largest of their values' scales.
+          const bool fits = mx[0] * rf[0] + lv <= bs[0] + 8.0f && mx[1] * rf[1] + lv <= bs[1] + 8.0f;
+          if (!__all_sync(0xffffffffu, fits)) {
+            bool move = false;
+            float corr[2];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * corr[e >> 1 & 1]);
-              tmem_st_16x64(to + c, v);
+            for (int k = 0; k < 2; ++k) {
+              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+              const float to_be = (mx[k] == -INFINITY ? mx[k] : mx[k] * rf[k]) + lv;
+              corr[k] = 1.0f;
+              if (to_be > bs[k] + 8.0f) {
+                move = true;
+                corr[k] = ex2(bs[k] - to_be);
+                bs[k] = to_be;
+              }
+              sum[k] = mul2(sum[k], pack2(corr[k], corr[k]));
             }
-            tmem_st_wait();
+            if ((i > begin || h > 0) && __any_sync(0xffffffffu, move)) {
+              ok = warp_wait(pv_done(2 * tl + (h ^ 1u)), h == 0 ? uph ^ 1u : uph, kSiteAttn + 10);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < kD; c += 32) {
+                uint32_t o[16];
+                tmem_ld_16x32(to + c, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr[e >> 1 & 1]);
+                tmem_st_16x256b_x4(to + c, o);
+              }
+            }
           }
+          const float less[2] = {bs[0] == -INFINITY ? 0.f : bs[0], bs[1] == -INFINITY ? 0.f : bs[1]};  // (no key seen yet)
+          uint32_t pk[16];
+          if (edge)
+            weights<true>(v, hsc, seen, rf, less, pk, sum);
+          else
+            weights<false>(v, hsc, seen, rf, less, pk, sum);
+          tmem_st_16x128b_x8(ts + 64u * h, pk);  // over S, which is read
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(2 * tl + h));
         }
-        const float less[2] = {bs[0] == -INFINITY ? 0.f : bs[0], bs[1] == -INFINITY ? 0.f : bs[1]};  // (no key seen yet)
-        if (edge)
-          weights<true>(ts, sc + t2, seen, rf, less, sum);
-        else
-          weights<false>(ts, sc + t2, seen, rf, less, sum);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(p_full(tl));
-          mbar_arrive(sc_empty(sl));
-        }
+        if (ok && lane == 0) mbar_arrive(sc_empty(sl));
       }
       if (!ok) break;
       float l[2];
@@ -573,7 +586,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         l[k] = x + __shfl_xor_sync(0xffffffffu, x, 2);
       }
-      ok = warp_wait(pv_done(tl), (i - 1) & 1u, kSiteAttn + 10);
+      // (a barrier for each half: with one for both, of which this waits for the second last phase's successor, the
+      // wait took a phase further back for it)
+      ok = warp_wait(pv_done(2 * tl), (i - 1) & 1u, kSiteAttn + 10) &&
+           warp_wait(pv_done(2 * tl + 1), (i - 1) & 1u, kSiteAttn + 10);
       if (!ok) break;
       tc_fence_after();
       const bool whole = w.begins && w.ends;
