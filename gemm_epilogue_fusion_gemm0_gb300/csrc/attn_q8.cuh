@@ -366,6 +366,12 @@ __device__ __forceinline__ void row_power(float amax, float& up, float& down) {
   }
 }
 
+// What a row's products are multiplied by in the exponents; never zero, which times a masked score's -inf is NaN.
+__device__ __forceinline__ float exponent_factor(float scale_log2, float down) {
+  const float f = scale_log2 * down;
+  return f < 1.17549435e-38f ? 1.17549435e-38f : f;
+}
+
 // log2 of the power of two that a value scale is at most (2^-60 for smaller ones, a NaN among them)
 constexpr float kLeastScale = -60.f;
 __device__ __forceinline__ float scale_power(float s) {
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         float up, down;
         row_power(amax, up, down);
-        rf[r] = p.scale_log2 * down;
+        rf[r] = exponent_factor(p.scale_log2, down);
 #pragma unroll
         for (int i = 0; i < kSteps / 2; ++i) {
           float v[8];
@@ -569,6 +575,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         const auto key_of = [&](int n, int e) { return key + kFewApart * (n / 2) + 8 * (n & 1) + 2 * t + e; };
         const bool edge = key + kFewApart + kFewKeys - 1 > w.s.first + w.tile * kFewRows / p.group;
         if (edge) {  // what lies behind the last key is not looked at
+          __syncwarp();  // (a branch, which predicates instead would cost every unit)
 #pragma unroll
           for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -580,17 +587,20 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         for (int n = 0; n < 4; ++n) {
           vm = max3_abs(vm, vs[n][0], vs[n][1]);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s[n][2 * r + e] *= ks[n][e] * rf[r];
-            if (edge) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (key_of(n, e) > limit[r]) s[n][2 * r + e] = -INFINITY;
-            }
-            mx[r] = max3(mx[r], s[n][2 * r], s[n][2 * r + 1]);
-          }
+          for (int e = 0; e < 4; ++e) s[n][e] *= ks[n][e & 1];
         }
+        if (edge) {
+          __syncwarp();
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key_of(n, e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) mx[r] = max3(mx[r], s[n][2 * r], s[n][2 * r + 1]);
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
           vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
@@ -601,7 +611,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
         bool move = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          m[r] = fmaxf(m[r], mx[r]);
+          m[r] = fmaxf(m[r], mx[r] == -INFINITY ? mx[r] : mx[r] * rf[r]);
           move |= m[r] + lv > base[r] + 8.0f;
         }
         if (__any_sync(0xffffffffu, move)) {
@@ -627,12 +637,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
           for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float x = ex2(s[n][2 * r + e] - less);
+              const float x = ex2(fmaf(s[n][2 * r + e], rf[r], -less));
               l[r] += x;
               s[n][2 * r + e] = x * vs[n][e];
             }
         }
         if (edge) {  // (a scale behind a row's last key may be NaN)
+          __syncwarp();
 #pragma unroll
           for (int n = 0; n < 4; ++n)
 #pragma unroll

@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                        pack_f16x2(v[0] * up, v[1] * up), pack_f16x2(v[2] * up, v[3] * up),
                        pack_f16x2(v[4] * up, v[5] * up), pack_f16x2(v[6] * up, v[7] * up));
         }
-        mine *= p.scale_log2;
+        mine = exponent_factor(p.scale_log2, mine);
         rf[0] = __shfl_sync(0xffffffffu, mine, g);
         rf[1] = __shfl_sync(0xffffffffu, mine, g + 8);
       }
