@@ -503,11 +503,12 @@ def _cache_args(c: _Call, cache, cu, lens, table, T: int) -> tuple:
     """The C arguments of a cache and a batch."""
     k_q, k_s, v_q, v_s = cache
     codes = pages, Hk, page, D = k_q.shape
-    B, width = table.shape
+    scales, seqs = codes[:3], table.shape
+    B, width = seqs
     i8, f32, i32 = torch.int8, torch.float32, torch.int32
-    return (c.t(k_q, i8, codes, "k_q"), c.t(k_s, f32, codes[:3], "k_s"), c.t(v_q, i8, codes, "v_q"),
-            c.t(v_s, f32, codes[:3], "v_s"), pages, Hk, page, D, c.t(cu, i32, (B + 1,), "cu"),
-            c.t(lens, i32, (B,), "lens"), c.t(table, i32, (B, width), "table"), B, width, T)
+    return (c.t(k_q, i8, codes, "k_q"), c.t(k_s, f32, scales, "k_s"), c.t(v_q, i8, codes, "v_q"),
+            c.t(v_s, f32, scales, "v_s"), pages, Hk, page, D, c.t(cu, i32, (B + 1,), "cu"),
+            c.t(lens, i32, (B,), "lens"), c.t(table, i32, seqs, "table"), B, width, T)
 
 
 def _host(t, dtype, n: int, name: str) -> int:

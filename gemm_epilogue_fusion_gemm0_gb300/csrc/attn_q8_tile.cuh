@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = ask(p.cache.v_q, 0) && ask(p.cache.v_q, 1);
       if (!ok) break;
     }
-    // (a wait ran out: copies in flight land before the block may leave)
-    if (!ok && lane == 0) land_copies(raw_full(0), static_cast<int>(half), kRawStages, timeout_ns);
+    // (also where a wait ran out: no copy is in flight when the block leaves)
+    if (lane == 0) land_copies(raw_full(0), static_cast<int>(half), kRawStages, timeout_ns);
   } else if (warp == 20) {
     // ------------------------------------------------------------- products
     const bool issuer = elect_one();

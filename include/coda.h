@@ -396,8 +396,7 @@ CODA_API coda_status_t coda_bwd_swiglu_dgrad_q8(const coda_bf16* dout, const cod
  *   cu [B + 1] int32: rows cu[b] .. cu[b + 1] - 1 are sequence b's (cu[0] = 0, not decreasing);
  *   lens [B] int32: its tokens in all, these among them;
  *   so row i is its token lens[b] - (cu[b + 1] - i).
- *   T: rows of the tensors; rows behind the last sequence (cu[B] .. T - 1) are not read
- *   and not written.
+ *   T: rows of the tensors; nothing is written for rows behind the last sequence (cu[B] .. T - 1).
  * A row whose token number is negative (a sequence with more rows than tokens: padding in front)
  * has no place in the cache.  A sequence may have no rows, or no tokens.
  * cu, lens and table are device memory, read when the call runs: a captured call follows them.  A
@@ -450,7 +449,9 @@ CODA_API coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, c
  * One token per sequence, a few, a chunk and a whole prompt (lens = rows) are the same call.  most: a
  * hint, the largest number of rows of a sequence (0: not known); with any other value the result is
  * the same and the time may be longer.
- * fp32 sums and softmax; weights are rounded to fp16 (by 2^-11 of them at most) before their products with v's codes.
+ * fp32 sums and softmax; weights times v's scales are rounded to fp16 (by 2^-11 of them at most) before their
+ * products with v's codes (scales below 2^-60 of a sequence's values lose bits).  A NaN in a row of q, or a NaN scale of
+ * a token that it sees, makes the row NaN.
  * Results do not depend on other sequences but in the order of fp32 sums, and are the same on
  * every run of the same call.
  *   workspace: at least coda_attn_q8_workspace_bytes(T, B, Hq, Hk, D) */
