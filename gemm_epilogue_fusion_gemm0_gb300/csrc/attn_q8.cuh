@@ -298,9 +298,9 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 // Bound by HBM: 2 (D + 4) bytes per key, used for at most 16 rows.  As in the product for few tokens, each
 // of 8 warps has its own ring: 2 x 16 keys of a unit (so that a short context is spread over all warps too),
 // codes and scales, by cp.async up to two units ahead (67 to 135 KB in flight per SM), and no barrier but the warp's
-// in the loop.  The pages of a unit are looked up one unit before its copies start.  Its instructions are as
-// near a bound: 16 keys at a time took 590 of them per 16 keys, 32 together share a row's maximum and the
-// bookkeeping.
+// in the loop.  The pages of a unit are looked up one unit before its copies start.  Its instructions are the
+// nearer bound, 880 per warp and 32 keys (16 keys at a time took 590 each; 32 share a row's maximum and the
+// bookkeeping): 64 tokens over up to 8192 keys each, 64 / 8 heads of 128, 144 us, 4.7 TB/s.
 //
 // S = q k^T and o += p v run as mma.sync.m16n8k16 on fp16, the 16 rows as its rows.  q's rows are brought
 // into fp16's range by a power of two each (exact); codes are exact in fp16 (1024 + 128 + code by bits,
