@@ -21,13 +21,17 @@
 namespace coda {
 
 constexpr int kAttnUnit = 128;       // keys of the kernel for tiles
-constexpr int kFewUnit = 256;        // of the kernel for few
-constexpr int kFewRows = 16, kFewWarps = 8, kFewStages = 2;
+constexpr int kFewKeys = 16;         // that a warp of the kernel for few takes together: a page holds them
+constexpr int kFewStages = 2;
 constexpr int kTileRows = 256, kTileThreads = 704;
 
 // What the deal knows of a kernel.  kLead: measured, 64 sequences' decoding and chunks of 500 tokens.
+// kN: groups of 8 rows (1 or 2); two have registers for 8 warps.
+template <int kN>
 struct FewDeal {
-  static constexpr int kRows = kFewRows, kUnit = kFewUnit, kThreads = 32 * kFewWarps, kLead = 1;
+  static constexpr int kRows = 8 * kN, kWarps = kN == 1 ? 12 : 8, kThreads = 32 * kWarps, kLead = 1;
+  static constexpr int kApart = kFewKeys * kWarps;  // from a warp's first 16 keys of a unit to its second
+  static constexpr int kUnit = 2 * kApart;
 };
 struct TileDeal {
   static constexpr int kRows = kTileRows, kUnit = kAttnUnit, kThreads = kTileThreads, kLead = 3;
@@ -109,7 +113,8 @@ struct AttnWs {
   AttnCut* cut;     // [blocks]
   float2* ml;       // [2 blocks][rows]: what was taken out of the exponents (base 2), and the sum
   float* o;         // [2 blocks][rows][D]
-  int rows;         // of a tile: as many as the call's tiles may have
+  int tile;         // rows of a tile
+  int rows;         // of a part: as many as the call's tiles may have
 };
 
 __device__ __forceinline__ AttnSeq load_seq(const AttnQ8Params& p, int b) {
@@ -293,39 +298,40 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: tiles of 16
+// Few rows: tiles of 8 or 16
 //
 // Bound by HBM: 2 (D + 4) bytes per key, used for at most 16 rows.  As in the product for few tokens, each
-// of 8 warps has its own ring: 2 x 16 keys of a unit (so that a short context is spread over all warps too),
-// codes and scales, by cp.async up to two units ahead (67 to 135 KB in flight per SM), and no barrier but the warp's
-// in the loop.  The pages of a unit are looked up one unit before its copies start.  Its instructions are the
-// nearer bound, 880 per warp and 32 keys (16 keys at a time took 590 each; 32 share a row's maximum and the
-// bookkeeping): 64 tokens over up to 8192 keys each, 64 / 8 heads of 128, 144 us, 4.7 TB/s.
+// warp has its own ring: 2 x 16 keys of a unit (so that a short context is spread over all warps too), codes and
+// scales, by cp.async up to two units ahead, and no barrier but the warp's in the loop.  The pages of a unit are looked
+// up one unit before its copies start.  Its instructions are the nearer bound, most of them the widening of codes,
+// so the keys are the 16 rows of an instruction and the query rows its 8 columns:
+//   S^T = k q^T,  o^T += v^T p^T    mma.sync.m16n8k16 on fp16
+// which takes half the instructions of the products and of the softmax that 16 query rows to an instruction take where
+// there are at most 8 (one token of 8 heads to a key head), and registers for 12 warps in place of 8: 64 tokens over up
+// to 8192 keys each, 64 / 8 heads of 128, 124 us, 5.5 TB/s (rows as the instruction's rows: 144).
 //
-// S = q k^T and o += p v run as mma.sync.m16n8k16 on fp16, the 16 rows as its rows.  q's rows are brought
-// into fp16's range by a power of two each (exact); codes are exact in fp16 (1024 + 128 + code by bits,
-// less 1152).  A thread (g = lane / 4, t = lane % 4) reads 16 codes of key g of each 8 at a time: its
-// operand k of 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are four neighbouring values, the same of q.  For p v it reads 16
-// values (8 for D = 64) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, column g of tile j being value j of the g-th
-// 16: the same keys that its own sums of S are.  So nothing is exchanged between threads but a row's
-// maximum.  Both reads are free of bank conflicts with the 16-byte groups of a key exchanged as below.
+// q's rows are brought into fp16's range by a power of two each (exact); codes are exact in fp16 (1024 + 128 + code by
+// bits, less 1152).  A thread (g = lane / 4, t = lane % 4) reads 16 codes of keys g and g + 8 at a time: its operand k
+// of 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are four neighbouring values, the same of q.  It has the scores of these keys and of
+// rows 2 t, 2 t + 1; their weights change places by movmatrix to keys 2 t, 2 t + 1 of row g.  For v^T p^T it reads 16
+// values (8 for D = 64) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, rows g and g + 8 of tile j being values 2 j and 2 j + 1 of
+// the g-th 16.  Both reads are free of bank conflicts with the 16-byte groups of a key exchanged as below.
 //
-// Scales: a key's multiplies its column of S; a value's its column of p.  So that their product stays
-// within fp16, what is taken out of the exponents is not the largest score m alone but m + log2 of
-// the largest value scale so far (rounded up to a power of two): the sums and outputs share it.  It moves, and the
-// outputs with it, only where p would pass 2^8.
+// Scales: a key's multiplies its row of S^T; a value's its row of p^T.  So that their product stays within fp16, what is
+// taken out of the exponents is not the largest score alone but that and log2 of the largest value scale (rounded up to
+// a power of two): the sums and outputs share it.  It moves, and the outputs with it, only where p would pass 2^8,
+// which a thread sees in its own scores; only then is a row's maximum found.
 // ---------------------------------------------------------------------------
-constexpr int kFewKeys = 16;                  // together: a page holds them
-constexpr int kFewApart = kFewKeys * kFewWarps;  // from a warp's first 16 keys of a unit to its second
-static_assert(kFewUnit == 2 * kFewApart, "a unit");
-
-template <int kD>
+template <int kD, int kN>
 struct FewSmem {
-  static constexpr uint32_t kCodes = kFewKeys * kD;                         // of 16 keys
-  static constexpr uint32_t kGroup = 2 * kCodes + 2 * kFewKeys * 4;         // k, v, their scales
+  static constexpr int kWarps = FewDeal<kN>::kWarps;
+  static constexpr int kMeet = kN == 1 ? 4 : 16;  // rows whose parts meet at a time: what there is room for
+  static constexpr uint32_t kCodes = kFewKeys * kD;                  // of 16 keys
+  static constexpr uint32_t kGroup = 2 * kCodes + 2 * kFewKeys * 4;  // k, v, their scales
   static constexpr uint32_t kStage = 2 * kGroup;
-  static constexpr uint32_t kJoin = kFewWarps * kFewStages * kStage;        // the warps' outputs
-  static constexpr uint32_t kBytes = kJoin + kFewWarps * kFewRows * kD * 4;
+  static constexpr uint32_t kJoin = kWarps * kFewStages * kStage;    // the warps' outputs
+  static constexpr uint32_t kEnd = kJoin + kWarps * kMeet * kD * 4;
+  static constexpr uint32_t kBytes = kEnd > 65536 ? kEnd : 65536;    // (the sequences' costs at the start)
   static_assert(kGroup % 128 == 0 && kBytes <= 232448u - 4096u, "shared memory");
 };
 
@@ -413,16 +419,25 @@ __device__ __forceinline__ uint32_t few_v_at(uint32_t r, uint32_t c) {
   return 128u * (r >> 1) + 16u * (((r & 1u) << 2 | c) ^ ((r >> 1 & 3u) << 1));
 }
 
-template <int kD>
-__global__ void __launch_bounds__(32 * kFewWarps, 1)
+// An 8 x 8 matrix of 16-bit numbers, two columns 2 t, 2 t + 1 of row g in a register, to its transpose.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+template <int kD, int kN>
+__global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
     attn_q8_few_kernel(const AttnQ8Params p, const AttnWs ws, const AttnDeal deal) {
-  using Smem = FewSmem<kD>;
-  constexpr int kSteps = kD / 16;   // instructions along D of S
-  constexpr int kTiles = kD / 8;    // tiles of 8 columns of o
-  constexpr int kF4 = kD / 16;      // float4s of a row of o in a thread
+  using Smem = FewSmem<kD, kN>;
+  using Deal = FewDeal<kN>;
+  constexpr int kSteps = kD / 16;   // instructions along D of S^T
+  constexpr int kTiles = kD / 16;   // tiles of 16 rows of o^T
+  constexpr int kF4 = kD / 32;      // float4s of a row of o in a thread
+  constexpr int kWarps = Deal::kWarps, kMeet = Smem::kMeet;
   extern __shared__ __align__(1024) uint8_t smem_few[];
-  __shared__ float2 warp_ml[kFewWarps][kFewRows];
-  __shared__ float2 row_ml[kFewRows];
+  __shared__ float2 warp_ml[kWarps][8 * kN];
+  __shared__ float2 row_ml[8 * kN];
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int g = lane >> 2, t = lane & 3;
@@ -435,15 +450,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
   AttnWalk w;
   int64_t end;
   bool some;
-  const int64_t total = walk_start<FewDeal>(w, p, deal, places, reinterpret_cast<int64_t*>(smem_few), end, some);
+  const int64_t total = walk_start<Deal>(w, p, deal, places, reinterpret_cast<int64_t*>(smem_few), end, some);
   if (threadIdx.x == 0) ws.cut[blockIdx.x].valid = 0;
-  if (!some || !walk_piece<FewDeal>(w, p, deal, places)) return;
+  if (!some || !walk_piece<Deal>(w, p, deal, places)) return;
   const int mine = warp * kFewKeys;  // the warp's first key of a unit
   const int mask = (1 << p.cache.page_log2) - 1;
   AttnWalk ahead = w;
   // the table's entry for the warp's first (even lanes) and second 16 keys of a unit
   const auto entry_at = [&](const AttnWalk& a) {
-    const int key = a.unit * kFewUnit + mine + kFewApart * (lane & 1), i = key >> p.cache.page_log2;
+    const int key = a.unit * Deal::kUnit + mine + Deal::kApart * (lane & 1), i = key >> p.cache.page_log2;
     return key < a.extent && i < p.batch.width ? __ldg(p.batch.table + static_cast<size_t>(a.b) * p.batch.width + i) : -1;
   };
   int entry = entry_at(ahead);
@@ -457,7 +472,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
     const uint32_t st = ring + (issued & (kFewStages - 1)) * Smem::kStage;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int key = ahead.unit * kFewUnit + mine + kFewApart * h;
+      const int key = ahead.unit * Deal::kUnit + mine + Deal::kApart * h;
       const int page = __shfl_sync(0xffffffffu, entry, h);
       if (key >= ahead.extent) continue;
       const uint32_t gr = st + h * Smem::kGroup;
@@ -479,7 +494,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
       }
     }
     ++issued;
-    more = walk_unit<FewDeal>(ahead, p, deal, places);
+    more = walk_unit<Deal>(ahead, p, deal, places);
     if (more) entry = entry_at(ahead);
   };
 #pragma unroll
@@ -488,173 +503,191 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
     cp_async_commit();
   }
 
-  uint32_t qa[kSteps][4];
-  float acc[kTiles][4];
-  float m[2], l[2], rf[2], base[2], lv;
-  int limit[2];
-  uint32_t n_unit = 0;
+  uint32_t used = 0;
   do {
-    {  // a piece of an item: its rows of q
-      lv = kLeastScale;
+    // a piece of an item: its rows of q, row 8 n + g in this thread; then of rows 8 n + 2 t + e their factor and limit
+    uint32_t qb[kN][kSteps][2];
+    float acc[kN][kTiles][4];
+    float l[kN][2], rf[kN][2], base[kN][2];
+    int limit[kN][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const AttnRow row = attn_row(p, w.s, w.hk, w.tile * kFewRows + g + 8 * r);
-        limit[r] = row.limit;
-        m[r] = base[r] = -INFINITY;
-        l[r] = 0.f;
-        Chunk8 c[kSteps / 2];
-        float amax = 0.f;
+    for (int n = 0; n < kN; ++n) {
+      const AttnRow row = attn_row(p, w.s, w.hk, w.tile * Deal::kRows + 8 * n + g);
+      Chunk8 c[kSteps / 2];
+      float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < kSteps / 2; ++i) {
-          c[i] = Chunk8{{0u, 0u, 0u, 0u}};
-          if (row.in) c[i] = ldg8(p.q + row.at * kD + 64 * (i / 2) + 16 * t + 8 * (i % 2));
+      for (int i = 0; i < kSteps / 2; ++i) {
+        c[i] = Chunk8{{0u, 0u, 0u, 0u}};
+        if (row.in) c[i] = ldg8(p.q + row.at * kD + 64 * (i / 2) + 16 * t + 8 * (i % 2));
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps / 2; ++i) {
+        float v[8];
+        unpack8(c[i], v);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) amax = max3_abs_nan(amax, v[e], v[e + 1]);
+      }
+      amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      float up, down;
+      row_power(amax, up, down);
+      const float factor = exponent_factor(p.scale_log2, down);
+#pragma unroll
+      for (int i = 0; i < kSteps / 2; ++i) {
+        float v[8];
+        unpack8(c[i], v);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // two instructions of four values each
+          const float* x = v + 4 * e;
+          qb[n][2 * i + e][0] = pack_f16x2(x[0] * up, x[1] * up);
+          qb[n][2 * i + e][1] = pack_f16x2(x[2] * up, x[3] * up);
         }
+      }
 #pragma unroll
-        for (int i = 0; i < kSteps / 2; ++i) {
-          float v[8];
-          unpack8(c[i], v);
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) amax = max3_abs_nan(amax, v[e], v[e + 1]);
-        }
-        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        float up, down;
-        row_power(amax, up, down);
-        rf[r] = exponent_factor(p.scale_log2, down);
-#pragma unroll
-        for (int i = 0; i < kSteps / 2; ++i) {
-          float v[8];
-          unpack8(c[i], v);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // two instructions of four values each
-            const float* x = v + 4 * e;
-            qa[2 * i + e][r] = pack_f16x2(x[0] * up, x[1] * up);
-            qa[2 * i + e][2 + r] = pack_f16x2(x[2] * up, x[3] * up);
-          }
-        }
+      for (int e = 0; e < 2; ++e) {
+        rf[n][e] = __shfl_sync(0xffffffffu, factor, 4 * (2 * t + e));
+        limit[n][e] = __shfl_sync(0xffffffffu, row.limit, 4 * (2 * t + e));
+        base[n][e] = -INFINITY;
+        l[n][e] = 0.f;
       }
 #pragma unroll
       for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.f;
     }
-    for (; w.unit < w.last; ++w.unit, ++n_unit) {
+    const int low = w.s.first + w.tile * Deal::kRows / p.group;  // the smallest limit
+    for (; w.unit < w.last; ++w.unit, ++used) {
       cp_async_wait<kFewStages - 1>();
       __syncwarp();
-      const int key = w.unit * kFewUnit + mine;
+      const int key = w.unit * Deal::kUnit + mine;
       if (key < w.extent) {
-        const bool two = key + kFewApart < w.extent;  // the second 16 too
-        const uint32_t st = ring + (n_unit & (kFewStages - 1)) * Smem::kStage;
-        float s[4][4] = {};  // of keys 8 n + 2 t + e of the first 16 (n = 0, 1) and of the second
+        const bool two = key + Deal::kApart < w.extent;  // the second 16 too
+        const uint32_t st = ring + (used & (kFewStages - 1)) * Smem::kStage;
+        // scores of keys g (e < 2) and g + 8 of the first 16 and of the second, rows 8 n + 2 t + e % 2
+        float s[2][kN][4] = {};
+        float ks[2][2], vs[2][2];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          if (n >= 2 && !two) continue;
+        for (int q = 0; q < 2; ++q) {
+          if (q == 1 && !two) continue;
+          const uint32_t gr = st + q * Smem::kGroup;
 #pragma unroll
           for (int h = 0; h < kD / 64; ++h) {
-            const uint4 c = ld_shared_v4(st + (n / 2) * Smem::kGroup + few_k_at<kD>(8 * (n & 1) + g, 4 * h + t));
-            const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+            const uint4 c0 = ld_shared_v4(gr + few_k_at<kD>(g, 4 * h + t));
+            const uint4 c1 = ld_shared_v4(gr + few_k_at<kD>(g + 8, 4 * h + t));
+            const uint32_t x[4] = {c0.x, c0.y, c0.z, c0.w}, y[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t b0, b1;
-              q8_to_f16x2(word[i], b0, b1);
-              const uint32_t(&a)[4] = qa[4 * h + i];
-              mma_f16_16816(s[n], a[0], a[1], a[2], a[3], b0, b1);
+              uint32_t a0, a1, a2, a3;
+              q8_to_f16x2(x[i], a0, a2);
+              q8_to_f16x2(y[i], a1, a3);
+#pragma unroll
+              for (int n = 0; n < kN; ++n)
+                mma_f16_16816(s[q][n], a0, a1, a2, a3, qb[n][4 * h + i][0], qb[n][4 * h + i][1]);
             }
           }
+          const float* const sc =
+              reinterpret_cast<const float*>(smem_few + (gr - smem_u32(smem_few)) + 2 * Smem::kCodes) + g;
+          ks[q][0] = sc[0], ks[q][1] = sc[8];
+          vs[q][0] = sc[16], vs[q][1] = sc[24];
         }
-        // their scales (those of the second 16, where there are none, are not looked at)
-        float ks[4][2], vs[4][2];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float* sc = reinterpret_cast<const float*>(smem_few + (st - smem_u32(smem_few)) + (n / 2) * Smem::kGroup +
-                                                           2 * Smem::kCodes) + 8 * (n & 1) + 2 * t;
-          const float2 a = *reinterpret_cast<const float2*>(sc), b = *reinterpret_cast<const float2*>(sc + 16);
-          ks[n][0] = a.x, ks[n][1] = a.y;
-          vs[n][0] = b.x, vs[n][1] = b.y;
-        }
-        const auto key_of = [&](int n, int e) { return key + kFewApart * (n / 2) + 8 * (n & 1) + 2 * t + e; };
-        const bool edge = key + kFewApart + kFewKeys - 1 > w.s.first + w.tile * kFewRows / p.group;
+        if (!two) ks[1][0] = ks[1][1] = vs[1][0] = vs[1][1] = 0.f;
+        const auto key_of = [&](int q, int e) { return key + Deal::kApart * q + g + 8 * e; };
+        const bool edge = key + Deal::kApart + kFewKeys - 1 > low;
         if (edge) {  // what lies behind the last key is not looked at
           __syncwarp();  // (a branch, which predicates instead would cost every unit)
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (key_of(n, e) >= w.extent) vs[n][e] = 0.f;
+              if (key_of(q, e) >= w.extent) vs[q][e] = 0.f;
         }
-        float vm = 0.f, mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          vm = max3_abs(vm, vs[n][0], vs[n][1]);
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] *= ks[n][e & 1];
-        }
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[q][n][e] *= ks[q][e >> 1];
         if (edge) {
           __syncwarp();
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key_of(n, e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key_of(q, e >> 1) > limit[n][e & 1]) s[q][n][e] = -INFINITY;
         }
+        const float vm = fmaxf(max3_abs(0.f, vs[0][0], vs[0][1]), max3_abs(0.f, vs[1][0], vs[1][1]));
+        const float lv = scale_power(vm);
+        float mx[kN][2];
+        bool fits = true;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) mx[r] = max3(mx[r], s[n][2 * r], s[n][2 * r + 1]);
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-          vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-        }
-        lv = fmaxf(lv, scale_power(vm));
-        bool move = false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          m[r] = fmaxf(m[r], mx[r] == -INFINITY ? mx[r] : mx[r] * rf[r]);
-          move |= m[r] + lv > base[r] + 8.0f;
-        }
-        if (__any_sync(0xffffffffu, move)) {
-          float c[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            c[r] = 1.0f;
-            if (m[r] + lv > base[r] + 8.0f) {
-              c[r] = ex2(base[r] - (m[r] + lv));
-              base[r] = m[r] + lv;
-            }
-            l[r] *= c[r];
+          for (int e = 0; e < 2; ++e) {
+            mx[n][e] = max3(fmaxf(s[0][n][e], s[0][n][2 + e]), s[1][n][e], s[1][n][2 + e]);
+            fits = fits && mx[n][e] * rf[n][e] + lv <= base[n][e] + 8.0f;
           }
+        if (!__all_sync(0xffffffffu, fits)) {
+          float most = lv;
 #pragma unroll
-          for (int j = 0; j < kTiles; ++j)
+          for (int o = 4; o <= 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] *= c[e >> 1];
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float less = base[r] == -INFINITY ? 0.f : base[r];  // (no key seen yet)
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int n = 0; n < kN; ++n) {
+            float c[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float x = ex2(fmaf(s[n][2 * r + e], rf[r], -less));
-              l[r] += x;
-              s[n][2 * r + e] = x * vs[n][e];
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1)
+                mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
+              const float to_be = mx[n][e] * rf[n][e] + most;
+              c[e] = 1.0f;
+              if (to_be > base[n][e] + 8.0f) {
+                c[e] = ex2(base[n][e] - to_be);
+                base[n][e] = to_be;
+              }
+              l[n][e] *= c[e];
+            }
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[n][j][e] *= c[e & 1];
+          }
+        }
+        uint32_t pb[2][kN][2];  // weights of keys 2 t, 2 t + 1 (and 8 further) of row 8 n + g
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const float less[2] = {base[n][0] == -INFINITY ? 0.f : base[n][0],  // (no key seen yet)
+                                 base[n][1] == -INFINITY ? 0.f : base[n][1]};
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = ex2(fmaf(s[q][n][e], rf[n][e & 1], -less[e & 1]));
+              l[n][e & 1] += x;
+              s[q][n][e] = x * vs[q][e >> 1];
             }
         }
         if (edge) {  // (a scale behind a row's last key may be NaN)
           __syncwarp();
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key_of(n, e & 1) > limit[e >> 1]) s[n][e] = 0.f;
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key_of(q, e >> 1) > limit[n][e & 1]) s[q][n][e] = 0.f;
         }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              pb[q][n][e] = transposed(pack_f16x2(s[q][n][2 * e], s[q][n][2 * e + 1]));
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           if (q == 1 && !two) continue;
-          const uint32_t a0 = pack_f16x2(s[2 * q][0], s[2 * q][1]), a1 = pack_f16x2(s[2 * q][2], s[2 * q][3]);
-          const uint32_t a2 = pack_f16x2(s[2 * q + 1][0], s[2 * q + 1][1]), a3 = pack_f16x2(s[2 * q + 1][2], s[2 * q + 1][3]);
           uint32_t v[4][kD / 32];  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: kD / 8 values of each
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -683,7 +716,10 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
               b[h][3] = q8_less_1152(__byte_perm(hi, 0x64646464u, 0x4342));
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_f16_16816(acc[4 * i + j], a0, a1, a2, a3, b[0][j], b[1][j]);
+            for (int n = 0; n < kN; ++n) {
+              mma_f16_16816(acc[n][2 * i], b[0][0], b[0][1], b[1][0], b[1][1], pb[q][n][0], pb[q][n][1]);
+              mma_f16_16816(acc[n][2 * i + 1], b[0][2], b[0][3], b[1][2], b[1][3], pb[q][n][0], pb[q][n][1]);
+            }
           }
         }
       }
@@ -691,73 +727,86 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
       if (more) issue();
       cp_async_commit();
     }
-    {
-      // The warps' parts meet.
+
+    // The warps' parts meet.
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (t == 0) warp_ml[warp][g + 8 * r] = make_float2(base[r], l[r]);
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
+        if (g == 0) warp_ml[warp][8 * n + 2 * t + e] = make_float2(base[n][e], l[n][e]);
       }
-      __syncthreads();
-      const int rows = min(kFewRows, w.s.n * p.group - w.tile * kFewRows);
+    __syncthreads();
+    const int rows = min(Deal::kRows, w.s.n * p.group - w.tile * Deal::kRows);
+    float f[kN][2];  // of the warp's parts
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kFewWarps; ++i) top = fmaxf(top, warp_ml[i][g + 8 * r].x);
+        for (int i = 0; i < kWarps; ++i) top = fmaxf(top, warp_ml[i][r].x);
         const float less = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int i = 0; i < kFewWarps; ++i) {
-          const float2 x = warp_ml[i][g + 8 * r];
+        for (int i = 0; i < kWarps; ++i) {
+          const float2 x = warp_ml[i][r];
           sum = fmaf(x.y, ex2(x.x - less), sum);
         }
-        if (warp == 0 && t == 0) row_ml[g + 8 * r] = make_float2(top, sum);
-        const float f = ex2(base[r] - less);
-        if (g + 8 * r < rows) {
+        if (warp == 0 && g == 0) row_ml[r] = make_float2(top, sum);
+        f[n][e] = ex2(base[n][e] - less);
+      }
+    const bool whole = w.begins && w.ends;
+    const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.begins ? 1 : 0);
 #pragma unroll
-          for (int i = 0; i < kF4; ++i) {  // values of the thread's two groups of columns
-            const int half = i / (kF4 / 2), j = 4 * (i % (kF4 / 2));
-            const int e = 2 * r + half;
-            const int at = kF4 * t + (i ^ ((t | (g & 1) << 2) & (kF4 - 1)));
-            join[(warp * kFewRows + g + 8 * r) * (kD / 4) + at] =
-                make_float4(acc[j][e] * f, acc[j + 1][e] * f, acc[j + 2][e] * f, acc[j + 3][e] * f);
+    for (int q = 0; q < 8 * kN / kMeet; ++q) {  // rows kMeet q ..
+      if (q * kMeet >= rows) continue;
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * t + e - q * kMeet;
+          if (r < 0 || r >= kMeet) continue;
+#pragma unroll
+          for (int i = 0; i < kF4; ++i) {
+            const float(&a)[kTiles][4] = acc[n];
+            const float by = f[n][e];
+            join[(warp * kMeet + r) * (kD / 4) + kF4 * g + (i ^ (g & (kF4 - 1)))] = make_float4(
+                a[2 * i][e] * by, a[2 * i][2 + e] * by, a[2 * i + 1][e] * by, a[2 * i + 1][2 + e] * by);
           }
         }
-      }
       __syncthreads();
-      const bool whole = w.begins && w.ends;
-      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.begins ? 1 : 0);
-      for (int i = threadIdx.x; i < rows * (kD / 4); i += 32 * kFewWarps) {
-        const int r = i / (kD / 4), c = i % (kD / 4);
-        const int tt = c / kF4, at = kF4 * tt + ((c % kF4) ^ ((tt | (r & 1) << 2) & (kF4 - 1)));
-        float4 x = join[r * (kD / 4) + at];
+      for (int i = threadIdx.x; i < min(kMeet, rows - q * kMeet) * (kD / 4); i += Deal::kThreads) {
+        const int jr = i / (kD / 4), c = i % (kD / 4), row_at = q * kMeet + jr;
+        const int at = c / kF4 * kF4 + ((c % kF4) ^ (c / kF4 & (kF4 - 1)));
+        float4 x = join[jr * (kD / 4) + at];
 #pragma unroll
-        for (int k = 1; k < kFewWarps; ++k) {
-          const float4 y = join[(k * kFewRows + r) * (kD / 4) + at];
+        for (int k = 1; k < kWarps; ++k) {
+          const float4 y = join[(k * kMeet + jr) * (kD / 4) + at];
           x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
-        const float2 ml = row_ml[r];
+        const float2 ml = row_ml[row_at];
         if (whole) {
-          const AttnRow row = attn_row(p, w.s, w.hk, w.tile * kFewRows + r);
+          const AttnRow row = attn_row(p, w.s, w.hk, w.tile * Deal::kRows + row_at);
           const float inv = ml.y == 0.f ? 0.f : 1.0f / ml.y;
           *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * c) =
               make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-          if (c == 0 && p.lse != nullptr)
-            p.lse[row.at] = attn_lse(ml.x, ml.y);
+          if (c == 0 && p.lse != nullptr) p.lse[row.at] = attn_lse(ml.x, ml.y);
         } else {
-          reinterpret_cast<float4*>(ws.o)[(slot * ws.rows + r) * (kD / 4) + c] = x;
-          if (c == 0) ws.ml[slot * ws.rows + r] = ml;
+          reinterpret_cast<float4*>(ws.o)[(slot * ws.rows + row_at) * (kD / 4) + c] = x;
+          if (c == 0) ws.ml[slot * ws.rows + row_at] = ml;
         }
       }
-      if (threadIdx.x == 0) tell_cut(w, ws.cut + blockIdx.x, total, end);
+      __syncthreads();  // the rows' place is free
     }
-  } while (walk_piece<FewDeal>(w, p, deal, places));
+    if (threadIdx.x == 0) tell_cut(w, ws.cut + blockIdx.x, total, end);
+  } while (walk_piece<Deal>(w, p, deal, places));
   cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
-// The join of an item's parts: block (c, y) has 16 rows of the item whose first part ends block c's share;
+// The join of an item's parts: block (c, y) has up to 16 rows of the item whose first part ends block c's share;
 // the parts follow in the next blocks' first slots.  The parts' weights are formed once, then a thread adds
 // four columns of a row over the parts, in order.  y = 0: of the launch for few; 1 ..: rows 16 (y - 1) ..
 // of the launch for tiles; of both in one launch.
@@ -773,12 +822,12 @@ __global__ void __launch_bounds__(256)
   griddep_wait();
   const int c = blockIdx.x, tid = static_cast<int>(threadIdx.x), y = static_cast<int>(blockIdx.y) + y0;
   const AttnWs& ws = y == 0 ? few : tiles;
-  const int kRows = y == 0 ? kFewRows : kTileRows, slot_rows = ws.rows;
+  const int kRows = ws.tile, slot_rows = ws.rows;
   const AttnCut cut = ws.cut[c];
   if (!cut.valid) return;
   const AttnSeq s = load_seq(p, cut.b);
   const int r0 = y == 0 ? 0 : (y - 1) * kGroup;
-  const int rows = min(kGroup, s.n * p.group - cut.tile * kRows - r0);
+  const int rows = min(min(kGroup, kRows - r0), s.n * p.group - cut.tile * kRows - r0);
   if (rows <= 0) return;
   // blocks c .. c + parts - 1; one whose share is empty (fewer units than blocks) has no part
   const int parts = static_cast<int>((cut.end * blocks + cut.cost - 1) / cut.cost) - c;

@@ -383,10 +383,14 @@ coda_status_t device_setup(int* sms, int* max_pairs = nullptr, void** noalloc_sc
                                  TileSmem<64>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(&attn_q8_tile_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  TileSmem<128>::kBytes) == cudaSuccess;
-      ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 FewSmem<64>::kBytes) == cudaSuccess;
-      ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 FewSmem<128>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<64, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<64, 1>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<64, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<64, 2>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<128, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<128, 1>::kBytes) == cudaSuccess;
+      ok &= cudaFuncSetAttribute(&attn_q8_few_kernel<128, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewSmem<128, 2>::kBytes) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kDgradGivenS, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kDgradGivenSSmem) == cudaSuccess;
       ok &= cudaFuncSetAttribute(kPairDgradGivenS, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1176,6 +1180,7 @@ cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t*
 // ---------------------------------------------------------------------------
 // The 8-bit paged cache (cache_q8.cuh, attn_q8.cuh)
 // ---------------------------------------------------------------------------
+constexpr int kFewRows = 16;  // of its largest tile
 constexpr int kFewMost = 48;  // packed rows of a sequence that go to the kernel for few
 constexpr int64_t kMaxSequences = 8192, kMaxHeads = 1024;
 
@@ -1261,6 +1266,7 @@ size_t attn_ws_bytes(int tile_rows, int64_t rows, int64_t D) {
 
 AttnWs attn_ws(char* at, int tile_rows, int64_t rows, int64_t D) {
   AttnWs w;
+  w.tile = tile_rows;
   w.rows = attn_ws_rows(tile_rows, rows);
   w.cut = reinterpret_cast<AttnCut*>(at);
   at += align256(kAttnMaxBlocks * sizeof(AttnCut));
@@ -1273,18 +1279,24 @@ AttnWs attn_ws(char* at, int tile_rows, int64_t rows, int64_t D) {
 // Sequences of up to kFewMost packed rows go to the kernel for few, the others to the one for tiles, each with
 // its own share of the blocks; one join serves both.  Without a hint of `rows` (the most of a sequence) both
 // run, and one of them may find nothing; a single sequence goes to tiles if it may have more than a few rows.  If a
-// sequence has more rows than the hint says, the kernel for few takes it.
+// sequence has more rows than the hint says, the kernel for few takes it.  Its tiles are of 8 rows where no sequence has
+// more, and beside tiles where one token has no more (single tokens among chunks: 67 us with four, 72 with tiles of
+// 16), else of 16 (five tokens of 8 heads: 23 us, and each key is read 3 times, not 5).
 template <int kD>
 cudaError_t launch_attn(const AttnQ8Params& p, char* at, int64_t rows, int blocks, cudaStream_t stream) {
   const bool tiles = rows > kFewMost, few = !tiles || p.batch.B > 1;
   const int64_t all = static_cast<int64_t>(p.batch.rows) * p.group;  // (a hint may be too small)
-  const AttnWs wf = attn_ws(at, kFewRows, all, kD);
+  const bool eight = rows <= 8 || (tiles && p.group <= 8);
+  const AttnWs wf = attn_ws(at, eight ? 8 : kFewRows, all, kD);
   const AttnWs wt = attn_ws(at + attn_ws_bytes(kFewRows, all, kD), kTileRows, kTileRows, kD);
   int k = 0;
   cudaError_t e = cudaSuccess;
   if (few) {
-    e = launch(&attn_q8_few_kernel<kD>, blocks, 32 * kFewWarps, FewSmem<kD>::kBytes, stream, false, p, wf,
-               AttnDeal{0, tiles ? kFewMost : 0x7fffffff});
+    const AttnDeal deal = {0, tiles ? kFewMost : 0x7fffffff};
+    e = eight ? launch(&attn_q8_few_kernel<kD, 1>, blocks, FewDeal<1>::kThreads, FewSmem<kD, 1>::kBytes, stream, false, p, wf,
+                       deal)
+              : launch(&attn_q8_few_kernel<kD, 2>, blocks, FewDeal<2>::kThreads, FewSmem<kD, 2>::kBytes, stream, false, p, wf,
+                       deal);
     if (e == cudaSuccess) after_launch(k++, stream);
   }
   if (e == cudaSuccess && tiles) {

@@ -171,6 +171,13 @@ def test_wrong_hints_change_nothing_but_time(B, most):
     check(B, batch, queries(batch, 6, 1), batch.random_cache(B), most=most)
 
 
+@pytest.mark.parametrize("group,most", [(3, 1), (3, 5), (8, 1), (1, 49)])
+def test_wrong_hints_with_items_over_several_blocks(B, group, most):
+    # few key heads and many keys: the tiles of the sequence with more rows than the hint says are cut between blocks
+    batch = Batch([50, 2], [6001, 900], 1, 64, 16)
+    check(B, batch, queries(batch, group, 1), batch.random_cache(B), most=most)
+
+
 def test_nothing_to_do(B):
     batch = Batch([2], [20], 2, 64, 16)
     cache = batch.random_cache(B)
