@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   int64_t end;
   bool some;
   const int64_t total = walk_start<TileDeal>(w, p, deal, places, reinterpret_cast<int64_t*>(smem), end, some);
-  if (tid == 0) ws.cut[blockIdx.x].valid = 0;
+  if (tid == 0) ws.cut[blockIdx.x].cut.valid = 0;
   // (the first piece; each role walks the others by itself)
   if (!some || !walk_piece<TileDeal>(w, p, deal, places)) return;
   if (tid == 0) {
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             p.lse[row[k].at] = attn_lse(bs[k], l[k]);
         }
       tc_fence_before();
-      if (tid == 0) tell_cut(w, ws.cut + blockIdx.x, total, end);
+      if (tid == 0) tell_cut(w, &ws.cut[blockIdx.x].cut, total, end);
     } while (walk_piece<TileDeal>(w, p, deal, places));
   }
   tc_fence_before();

@@ -1261,15 +1261,15 @@ int attn_ws_rows(int tile_rows, int64_t rows) { return static_cast<int>(std::min
 
 size_t attn_ws_bytes(int tile_rows, int64_t rows, int64_t D) {
   const size_t parts = size_t(2) * kAttnMaxBlocks * attn_ws_rows(tile_rows, rows);
-  return align256(kAttnMaxBlocks * sizeof(AttnCut)) + align256(parts * sizeof(float2)) + align256(parts * D * sizeof(float));
+  return align256(kAttnMaxBlocks * sizeof(AttnCutFew)) + align256(parts * sizeof(float2)) + align256(parts * D * sizeof(float));
 }
 
 AttnWs attn_ws(char* at, int tile_rows, int64_t rows, int64_t D) {
   AttnWs w;
   w.tile = tile_rows;
   w.rows = attn_ws_rows(tile_rows, rows);
-  w.cut = reinterpret_cast<AttnCut*>(at);
-  at += align256(kAttnMaxBlocks * sizeof(AttnCut));
+  w.cut = reinterpret_cast<AttnCutFew*>(at);
+  at += align256(kAttnMaxBlocks * sizeof(AttnCutFew));
   w.ml = reinterpret_cast<float2*>(at);
   at += align256(size_t(2) * kAttnMaxBlocks * w.rows * sizeof(float2));
   w.o = reinterpret_cast<float*>(at);
