@@ -16,6 +16,8 @@
 // the same call gives the same bits every time.
 #pragma once
 
+#include <type_traits>
+
 #include "cache_q8.cuh"
 
 namespace coda {
@@ -870,24 +872,46 @@ __global__ void __launch_bounds__(256)
     if (l == 0) row_ml[r] = make_float2(top, sum);
   }
   __syncthreads();
-  for (int i = tid; i < rows * (kD / 4); i += 256) {
-    const int r = i / (kD / 4), col = i % (kD / 4);
-    const float4* const part = reinterpret_cast<const float4*>(ws.o) + static_cast<size_t>(r0 + r) * (kD / 4) + col;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  // a thread's rows (r1 and on, kStep apart) go through the parts together, so that their loads are in flight together
+  // (a prompt of 8192 tokens, 32 heads: 17 us, 20.5 one row after another)
+  constexpr int kMost = kGroup * (kD / 4) / 256, kStep = 256 / (kD / 4);
+  const int r1 = tid / (kD / 4), col = tid % (kD / 4);
+  const float4* const part = reinterpret_cast<const float4*>(ws.o) + static_cast<size_t>(r0 + r1) * (kD / 4) + col;
+  const auto add_up = [&](auto each) {
+    constexpr int kEach = decltype(each)::value;
+    if (r1 >= rows) return;
+    float4 x[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int j = 0; j < parts; ++j) {
       if (slots[j] < 0) continue;
-      const float4 y = part[static_cast<size_t>(slots[j]) * slot_rows * (kD / 4)];
-      const float f = weight[j][r];
-      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+      const float4* const from = part + static_cast<size_t>(slots[j]) * slot_rows * (kD / 4);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (i > 0 && r1 + i * kStep >= rows) continue;
+        const float4 y = from[i * kStep * (kD / 4)];
+        const float f = weight[j][r1 + i * kStep];
+        x[i].x = fmaf(y.x, f, x[i].x), x[i].y = fmaf(y.y, f, x[i].y);
+        x[i].z = fmaf(y.z, f, x[i].z), x[i].w = fmaf(y.w, f, x[i].w);
+      }
     }
-    const float2 ml = row_ml[r];
-    const AttnRow row = attn_row(p, s, cut.hk, cut.tile * kRows + r0 + r);
-    const float inv = ml.y == 0.f ? 0.f : 1.0f / ml.y;
-    *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * col) =
-        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-    if (col == 0 && p.lse != nullptr) p.lse[row.at] = attn_lse(ml.x, ml.y);
-  }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int r = r1 + i * kStep;
+      if (r >= rows) continue;
+      const float2 ml = row_ml[r];
+      const AttnRow row = attn_row(p, s, cut.hk, cut.tile * kRows + r0 + r);
+      const float inv = ml.y == 0.f ? 0.f : 1.0f / ml.y;
+      *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * col) =
+          make_uint2(pack_bf16x2(x[i].x * inv, x[i].y * inv), pack_bf16x2(x[i].z * inv, x[i].w * inv));
+      if (col == 0 && p.lse != nullptr) p.lse[row.at] = attn_lse(ml.x, ml.y);
+    }
+  };
+  if (rows > kStep)
+    add_up(std::integral_constant<int, kMost>{});
+  else
+    add_up(std::integral_constant<int, 1>{});
 }
 
 }  // namespace coda
