@@ -164,6 +164,59 @@ def test_bad_pages(B, n):
     clean(B)
 
 
+FEW = [  # new, lens, Hq, Hk, D, page: tiles of 8 rows and of 16, alone and beside sequences of many rows
+    ([5, 2, 1], [4000, 129, 77], 16, 4, 128, 64),
+    ([2, 1, 1], [6000, 383, 385], 4, 1, 128, 16),
+    ([1, 1, 1, 1], [768, 769, 767, 4001], 8, 1, 64, 32),
+    ([70, 1, 2, 3], [90, 700, 300, 5000], 16, 1, 128, 32),
+    ([70, 1, 2, 3], [90, 700, 300, 5000], 9, 1, 64, 256),
+    ([70, 1, 2, 6], [90, 700, 300, 5000], 8, 1, 128, 16),
+    ([100, 1, 40, 0, 3], [5000, 1, 2000, 9, 2], 2, 2, 64, 16),
+]
+
+
+@pytest.mark.parametrize("hint", [False, True])
+@pytest.mark.parametrize("new,lens,Hq,Hk,D,page", FEW)
+def test_attention_of_few_rows(B, new, lens, Hq, Hk, D, page, hint):
+    batch = Batch(new, lens, Hk, D, page, seed=len(new), extra_rows=2)
+    q = queries(batch, Hq, D + len(new), 2.0)
+    check(B, batch, q, batch.random_cache(B, seed=3), most=max(new) if hint else 0)
+
+
+@pytest.mark.parametrize("new,lens,Hq,Hk,D,page", FEW)
+def test_few_rows_same_result_every_time(B, new, lens, Hq, Hk, D, page):
+    batch = Batch(new, lens, Hk, D, page)
+    cache, q = batch.random_cache(B), queries(batch, Hq, 1, 2.0)
+    args = (q, cache, batch.cu, batch.lens, batch.table)
+    runs = [B.coda_attn_q8(*args, most=max(new)) for _ in range(60)]
+    rows = int(batch.cu[-1])
+    assert all(torch.equal(r[:rows], runs[0][:rows]) for r in runs)
+    clean(B)
+
+
+@pytest.mark.parametrize("n", [1, 7, 300])
+def test_pages_beyond_2_31_codes(B, n):
+    """The same bits as from a small cache with the same two pages."""
+    Hk, D, page, g = 8, 128, 256, gen(4)
+    pages = (2 ** 31 + 2 ** 28) // (Hk * page * D) + 1
+    near = B.coda_cache_q8(2, Hk, page, D)
+    for i in (0, 2):
+        near[i].copy_(torch.randint(-127, 128, near[i].shape, device="cuda", generator=g))
+        near[i + 1].copy_(torch.rand(near[i + 1].shape, device="cuda", generator=g) * 0.02)
+    far = B.coda_cache_q8(pages, Hk, page, D)
+    for a, b in zip(near, far):
+        b[pages - 1] = a[1]
+        b[0] = a[0]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu, lens = torch.tensor([0, n], **i32), torch.tensor([300], **i32)
+    q = torch.randn(n, 2 * Hk * D, device="cuda", generator=g).to(torch.bfloat16)
+    here = B.coda_attn_q8(q, near, cu, lens, torch.tensor([[1, 0]], **i32), want_lse=True)
+    there = B.coda_attn_q8(q, far, cu, lens, torch.tensor([[pages - 1, 0]], **i32), want_lse=True)
+    assert all(torch.equal(a, b) for a, b in zip(here, there))
+    assert torch.isfinite(here[0]).all() and here[0].any()
+    clean(B)
+
+
 SAME = [  # new, lens, Hq, Hk, D, page
     ([1] * 5 + [70], [400, 3000, 17, 900, 5000, 2000], 16, 2, 128, 64),
     ([515], [3001], 4, 1, 128, 256),
