@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
       amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       float up, down;
       row_power(amax, up, down);
-      const float factor = exponent_factor(p.scale_log2, down);
+      // (a row that sees no token is zero whatever it holds: its scores, all -inf, times a NaN would not be)
+      const float factor = row.limit < 0 ? 1.0f : exponent_factor(p.scale_log2, down);
 #pragma unroll
       for (int i = 0; i < kSteps / 2; ++i) {
         float v[8];

@@ -449,9 +449,10 @@ CODA_API coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, c
  * One token per sequence, a few, a chunk and a whole prompt (lens = rows) are the same call.  most: a
  * hint, the largest number of rows of a sequence (0: not known); with any other value the result is
  * the same and the time may be longer.
- * fp32 sums and softmax; weights times v's scales are rounded to fp16 (by 2^-11 of them at most) before their
- * products with v's codes (scales below 2^-60 of a sequence's values lose bits).  A NaN in a row of q, or a NaN scale of
- * a token that it sees, makes the row NaN.
+ * fp32 sums and softmax; weights times v's scales are rounded to fp16 before their products with v's codes: by 2^-11 of
+ * each at most or, where that is more, by 2^-24 of the row's largest weight times the sequence's largest scale (scales
+ * below 2^-60 count as 2^-60).  A NaN or an infinity in a row of q, or a NaN scale of a token that it sees, makes the row
+ * NaN; a row that sees none is zero whatever it holds.
  * Results do not depend on other sequences but in the order of fp32 sums, and are the same on
  * every run of the same call.
  *   workspace: at least coda_attn_q8_workspace_bytes(T, B, Hq, Hk, D) */

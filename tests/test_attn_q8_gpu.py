@@ -140,6 +140,23 @@ def test_lost_values_stay_visible(B, n):
     clean(B)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("n,group", [(4, 1), (4, 8), (7, 5), (300, 2)])
+def test_rows_before_the_first_token_whatever_they_hold(B, n, group, value):
+    """Padding in front sees nothing: zeros and -inf, beside rows that see something and in a sequence without a token."""
+    batch = Batch([n, 3], [n // 2, 0], 1, 128, 16)
+    cache, q = batch.random_cache(B), queries(batch, group, 1)
+    bare = n - n // 2
+    want, lwant = B.coda_attn_q8(q, cache, batch.cu, batch.lens, batch.table, want_lse=True)
+    q[:bare, 5::128] = value
+    q[n:, 7::128] = value
+    o, lse = B.coda_attn_q8(q, cache, batch.cu, batch.lens, batch.table, want_lse=True)
+    for rows in (slice(0, bare), slice(n, n + 3)):
+        assert (o[rows] == 0).all() and (lse[rows] == -float("inf")).all()
+    assert torch.equal(o[bare:n], want[bare:n]) and torch.equal(lse[bare:n], lwant[bare:n])
+    clean(B)
+
+
 @pytest.mark.parametrize("n", [1, 6, 200])
 def test_bad_pages(B, n):
     batch = Batch([n, n], [n + 70, n + 90], 2, 64, 16)
