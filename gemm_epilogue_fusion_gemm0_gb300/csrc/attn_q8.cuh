@@ -8,7 +8,7 @@
 //
 // The rows of a sequence that share a key head, n tokens of `group` query heads each, are packed
 // (row r is token r / group, head r % group) and cut into tiles; a tile with its keys is an item, and
-// 128 or 256 keys of it a unit.  Lengths are known to the device alone, so each block of a persistent grid
+// 128, 256 or 384 keys of it a unit.  Lengths are known to the device alone, so each block of a persistent grid
 // adds up the units of all sequences, takes an equal, contiguous share of them, and walks it: whatever
 // the lengths, all SMs end together, and a long sequence's keys are spread over as many blocks as its
 // share of the work.  A part of an item leaves its running maximum, sum and unnormalised
