@@ -505,7 +505,23 @@ def _cache_args(c: _Call, cache, cu, lens, table, T: int) -> tuple:
     codes = pages, Hk, page, D = k_q.shape
     scales, seqs = codes[:3], table.shape
     B, width = seqs
-    i8, f32, i32 = torch.int8, torch.float32, torch.int32
+    i8, f32, i32, index = torch.int8, torch.float32, torch.int32, c.index
+    # the common case in few steps (1.4 us less of a call's host time on Grace than a tensor at a time); anything
+    # else is told apart (and raised) below
+    try:
+        good = (k_q.dtype is i8 and v_q.dtype is i8 and k_s.dtype is f32 and v_s.dtype is f32
+                and cu.dtype is i32 and lens.dtype is i32 and table.dtype is i32
+                and v_q.shape == codes and k_s.shape == scales and v_s.shape == scales
+                and cu.shape == (B + 1,) and lens.shape == (B,)
+                and k_q.is_contiguous() and k_s.is_contiguous() and v_q.is_contiguous() and v_s.is_contiguous()
+                and cu.is_contiguous() and lens.is_contiguous() and table.is_contiguous()
+                and index == k_q.get_device() == k_s.get_device() == v_q.get_device() == v_s.get_device()
+                == cu.get_device() == lens.get_device() == table.get_device())
+    except AttributeError:
+        good = False
+    if good:
+        return (k_q.data_ptr(), k_s.data_ptr(), v_q.data_ptr(), v_s.data_ptr(), pages, Hk, page, D,
+                cu.data_ptr(), lens.data_ptr(), table.data_ptr(), B, width, T)
     return (c.t(k_q, i8, codes, "k_q"), c.t(k_s, f32, scales, "k_s"), c.t(v_q, i8, codes, "v_q"),
             c.t(v_s, f32, scales, "v_s"), pages, Hk, page, D, c.t(cu, i32, (B + 1,), "cu"),
             c.t(lens, i32, (B,), "lens"), c.t(table, i32, seqs, "table"), B, width, T)

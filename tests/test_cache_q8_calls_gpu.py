@@ -239,3 +239,25 @@ def test_nonsense_touches_nothing_else(B, name, group):
     for n, (whole, _) in outs.items():
         assert (whole[:guard] == 3).all() and (whole[-guard:] == 3).all(), n
     check(B, batch, queries(batch, 4, 1), batch.random_cache(B))  # and the next call is right
+
+
+@pytest.mark.parametrize("name", ["k_q", "k_s", "v_q", "v_s", "cu", "lens", "table"])
+def test_binding_refuses_a_wrong_tensor(B, name):
+    batch = Batch([2, 1], [20, 9], 2, 64, 16)
+    held = dict(zip(("k_q", "k_s", "v_q", "v_s"), batch.random_cache(B)), cu=batch.cu, lens=batch.lens, table=batch.table)
+    right = held[name]
+    wide = torch.cat([right, right], -1)
+    other = torch.cat([right, right]) if name == "table" else wide  # (a wider table is a right one)
+    wrong = [(right.to(torch.int16), TypeError), (right.cpu(), TypeError), (other, ValueError),
+             (wide[..., ::2], ValueError)]  # the right shape, every other number
+    if name not in ("k_q", "table"):
+        wrong.append((right.tolist(), TypeError))
+    y, q = torch.zeros(3, 8 * 64, device="cuda", dtype=bf), torch.zeros(3, 4 * 64, device="cuda", dtype=bf)
+    for value, error in wrong:
+        args = dict(held, **{name: value})
+        rest = (tuple(args[n] for n in ("k_q", "k_s", "v_q", "v_s")), args["cu"], args["lens"], args["table"])
+        for call in (lambda: B.coda_cache_write_q8(y, *rest), lambda: B.coda_cache_read_q8(*rest, 3),
+                     lambda: B.coda_attn_q8(q, *rest)):
+            with pytest.raises(error):
+                call()
+    clean(B)
