@@ -123,6 +123,7 @@ struct AttnCutFew {
 struct AttnWs {
   AttnCutFew* cut;  // [blocks]; of tiles `cut` alone
   float2* ml;       // [2 blocks][rows]: what was taken out of the exponents (base 2), and the sum
+  float* unit;      // [2 blocks][rows]: what the outputs are to be multiplied by
   float* o;         // [2 blocks][rows][D]
   int tile;         // rows of a tile
   int rows;         // of a part: as many as the call's tiles may have
@@ -328,10 +329,11 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 // values (8 for D = 64) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, rows g and g + 8 of tile j being values 2 j and 2 j + 1 of
 // the g-th 16.  Both reads are free of bank conflicts with the 16-byte groups of a key exchanged as below.
 //
-// Scales: a key's multiplies its row of S^T; a value's its row of p^T.  So that their product stays within fp16, what is
-// taken out of the exponents is not the largest score alone but that and log2 of the largest value scale (rounded up to
-// a power of two): the sums and outputs share it.  It moves, and the outputs with it, only where p would pass 2^8,
-// which a thread sees in its own scores; only then is a row's maximum found.
+// Scales: a key's multiplies its row of S^T; a value's, less a power of two, its row of p^T.  What is taken out of the
+// exponents is a row's largest score; it moves, and sum and outputs with it, only where p would pass 2^8, which a thread
+// sees in its own scores; only then is a row's maximum found.  The power of two is the largest value scale's, rounded up,
+// so that weights times scales stay within fp16.  It is the outputs' alone: a sum that shared it (weights of
+// 2^(score - maximum - power)) lost its small terms, then all, with scales from 2^102 on.
 // ---------------------------------------------------------------------------
 template <int kD, int kN>
 struct FewSmem {
@@ -389,11 +391,23 @@ __device__ __forceinline__ float exponent_factor(float scale_log2, float down) {
   return f < 1.17549435e-38f ? 1.17549435e-38f : f;
 }
 
-// log2 of the power of two that a value scale is at most (2^-60 for smaller ones, a NaN among them)
-constexpr float kLeastScale = -60.f;
+// The power of two that a value scale is at most (2^-60 for smaller ones, a NaN among them; an infinity stands for 2^128).
+constexpr float kLeastScale = 0x1p-60f;
 __device__ __forceinline__ float scale_power(float s) {
-  return s > 0x1p-60f ? static_cast<float>(static_cast<int>((__float_as_uint(s) + 0x7fffffu) >> 23) - 127)
-                      : kLeastScale;
+  return s > kLeastScale ? __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u) : kLeastScale;
+}
+// A value scale goes into the weights divided by power / 2^kPowerUp, and the outputs are multiplied by that in the end
+// (both are fp32 numbers for all powers).
+constexpr uint32_t kPowerUp = 2;
+__device__ __forceinline__ float power_unit(float power) {
+  return __uint_as_float(__float_as_uint(power) - (kPowerUp << 23));
+}
+__device__ __forceinline__ float power_inverse(float power) {
+  return __uint_as_float(((254u + kPowerUp) << 23) - __float_as_uint(power));
+}
+// log2 of a / b, powers of two
+__device__ __forceinline__ float power_log2(float a, float b) {
+  return static_cast<float>(static_cast<int>(__float_as_uint(a) >> 23) - static_cast<int>(__float_as_uint(b) >> 23));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -520,6 +534,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
     uint32_t qb[kN][kSteps][2];
     float acc[kN][kTiles][4];
     float l[kN][2], rf[kN][2], base[kN][2];
+    float power = kLeastScale;  // of the value scales, in the outputs
     int limit[kN][2];
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
@@ -629,21 +644,22 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
               for (int e = 0; e < 4; ++e)
                 if (key_of(q, e >> 1) > limit[n][e & 1]) s[q][n][e] = -INFINITY;
         }
-        const float vm = fmaxf(max3_abs(0.f, vs[0][0], vs[0][1]), max3_abs(0.f, vs[1][0], vs[1][1]));
-        const float lv = scale_power(vm);
+        float vm = fmaxf(max3_abs(0.f, vs[0][0], vs[0][1]), max3_abs(0.f, vs[1][0], vs[1][1]));
         float mx[kN][2];
-        bool fits = true;
+        bool fits = vm <= power;
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             mx[n][e] = max3(fmaxf(s[0][n][e], s[0][n][2 + e]), s[1][n][e], s[1][n][2 + e]);
-            fits = fits && mx[n][e] * rf[n][e] + lv <= base[n][e] + 8.0f;
+            fits = fits && mx[n][e] * rf[n][e] <= base[n][e] + 8.0f;
           }
         if (!__all_sync(0xffffffffu, fits)) {
-          float most = lv;
 #pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          for (int o = 4; o <= 16; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+          const float before = power;
+          power = fmaxf(power, scale_power(vm));
+          const float less = ex2(power_log2(before, power));
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
             float c[2];
@@ -652,13 +668,14 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
 #pragma unroll
               for (int o = 4; o <= 16; o <<= 1)
                 mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
-              const float to_be = mx[n][e] * rf[n][e] + most;
+              const float to_be = mx[n][e] * rf[n][e];
               c[e] = 1.0f;
               if (to_be > base[n][e] + 8.0f) {
                 c[e] = ex2(base[n][e] - to_be);
                 base[n][e] = to_be;
               }
               l[n][e] *= c[e];
+              c[e] *= less;
             }
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
@@ -667,6 +684,11 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
           }
         }
         uint32_t pb[2][kN][2];  // weights of keys 2 t, 2 t + 1 (and 8 further) of row 8 n + g
+        const float by = power_inverse(power);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) vs[q][e] *= by;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           const float less[2] = {base[n][0] == -INFINITY ? 0.f : base[n][0],  // (no key seen yet)
@@ -767,7 +789,8 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
           sum = fmaf(x.y, ex2(x.x - less), sum);
         }
         if (warp == 0 && g == 0) row_ml[r] = make_float2(top, sum);
-        f[n][e] = ex2(base[n][e] - less);
+        // (as quotients by the sum, within 2 ulp, which stay in range whatever the power)
+        f[n][e] = ex2(base[n][e] - less) * (sum == 0.f ? 0.f : __fdividef(power_unit(power), sum));
       }
     const bool whole = w.begins && w.ends;
     const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.begins ? 1 : 0);
@@ -801,13 +824,15 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
         const float2 ml = row_ml[row_at];
         if (whole) {
           const AttnRow row = attn_row(p, w.s, w.hk, w.tile * Deal::kRows + row_at);
-          const float inv = ml.y == 0.f ? 0.f : 1.0f / ml.y;
           *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * c) =
-              make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+              make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
           if (c == 0 && p.lse != nullptr) p.lse[row.at] = attn_lse(ml.x, ml.y);
         } else {
           reinterpret_cast<float4*>(ws.o)[(slot * ws.rows + row_at) * (kD / 4) + c] = x;
-          if (c == 0) ws.ml[slot * ws.rows + row_at] = ml;
+          if (c == 0) {
+            ws.ml[slot * ws.rows + row_at] = ml;
+            ws.unit[slot * ws.rows + row_at] = ml.y;
+          }
         }
       }
       __syncthreads();  // the rows' place is free
@@ -857,7 +882,10 @@ __global__ void __launch_bounds__(256)
     const int r = tid >> 4, l = tid & 15;
     float top = -INFINITY, sum = 0.f;
     for (int j = l; j < parts; j += 16)
-      if (slots[j] >= 0 && r < rows) top = fmaxf(top, ws.ml[slots[j] * slot_rows + r0 + r].x);
+      if (slots[j] >= 0 && r < rows) {
+        top = fmaxf(top, ws.ml[slots[j] * slot_rows + r0 + r].x);
+        weight[j][r] = ws.unit[slots[j] * slot_rows + r0 + r];
+      }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float less = top == -INFINITY ? 0.f : top;
@@ -865,11 +893,13 @@ __global__ void __launch_bounds__(256)
       if (slots[j] >= 0 && r < rows) {
         const float2 ml = ws.ml[slots[j] * slot_rows + r0 + r];
         const float f = ex2(ml.x - less);
-        weight[j][r] = f;
+        weight[j][r] *= f;
         sum = fmaf(ml.y, f, sum);
       }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.f ? 0.f : __fdividef(1.0f, sum);
+    for (int j = l; j < parts; j += 16) weight[j][r] *= inv;  // (this thread's own)
     if (l == 0) row_ml[r] = make_float2(top, sum);
   }
   __syncthreads();
@@ -903,9 +933,8 @@ __global__ void __launch_bounds__(256)
       if (r >= rows) continue;
       const float2 ml = row_ml[r];
       const AttnRow row = attn_row(p, s, cut.hk, cut.tile * kRows + r0 + r);
-      const float inv = ml.y == 0.f ? 0.f : 1.0f / ml.y;
       *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * col) =
-          make_uint2(pack_bf16x2(x[i].x * inv, x[i].y * inv), pack_bf16x2(x[i].z * inv, x[i].w * inv));
+          make_uint2(pack_bf16x2(x[i].x, x[i].y), pack_bf16x2(x[i].z, x[i].w));
       if (col == 0 && p.lse != nullptr) p.lse[row.at] = attn_lse(ml.x, ml.y);
     }
   };

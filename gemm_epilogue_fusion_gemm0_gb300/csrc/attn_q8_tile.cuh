@@ -3,7 +3,7 @@
 //
 // A block holds two tiles of 128 rows of q (fp16, shared memory) and walks the keys 128 at a time:
 //   S_w = q_w k^T     128 x 128, tensor memory, fp32     (w = 0, 1: the two tiles)
-//   P_w = 2^(S_w scale - base) * v's scale, fp16, over the first half of S_w's columns of the same keys
+//   P_w = 2^(S_w scale - base) * v's scale / power, fp16, over the first half of S_w's columns of the same keys
 //   o_w += P_w v      128 x D, tensor memory; P_w is the first operand, from tensor memory
 // in two halves of 64 keys each, so that a tile's softmax has one half to work at while the products of the other
 // run (with all 128 together it waited for them: 4900 cycles a unit, of which the softmax was 2800).
@@ -23,8 +23,8 @@
 //                      of them 2350 cycles.)
 //   warp 20            issues tcgen05.mma: of each half of each tile, P v of a unit, then S of the next
 //   warp 21            looks up pages, asks for their codes and puts a unit's scales into shared memory
-// o is rescaled only where a row's maximum has grown by more than 2^8 (P stays below fp16's largest): hardly ever
-// after the first units.
+// o is rescaled only where a row's maximum has grown by more than 2^8 or the largest of v's scales by a power of two (P
+// stays below fp16's largest): hardly ever after the first units.
 #pragma once
 
 #include "attn_q8.cuh"
@@ -44,7 +44,7 @@ struct TileSmem {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + 2 * kOperand;
   static constexpr uint32_t kV = kK + kTileStages * kOperand;
-  static constexpr uint32_t kScale = kV + kTileStages * kOperand;  // [slot][k's 128, v's 128, the largest of v's]
+  static constexpr uint32_t kScale = kV + kTileStages * kOperand;  // [slot][k's 128, v's 128, their power]
   static constexpr uint32_t kScaleSlot = 2 * 512 + 16;
   static constexpr uint32_t kRawBytes = 64 * kD;
   static constexpr uint32_t kRaw = (kScale + kTileScales * kScaleSlot + 127) / 128 * 128;
@@ -316,8 +316,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int entry = entry_at(w);
     uint32_t half = 0;
     bool ok = true, more = true;
+    float power = kLeastScale;  // of the largest scale of v so far in the piece
     for (uint32_t i = 0; more; ++i) {
       const int key0 = w.unit * kAttnUnit, extent = w.extent, hk = w.hk;
+      const bool last = w.unit + 1 == w.last;  // of the piece
       const bool bad = static_cast<unsigned>(entry) >= static_cast<unsigned>(p.cache.pages);
       if (bad && lane < kAttnUnit / keys && key0 + lane * keys < extent) atomicCAS(&g_coda_status, 0u, 0x200u | kChkPage);
       const int page = bad ? -1 : entry;
@@ -362,12 +364,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = warp_wait(sc_empty(sl), (i / kTileScales & 1u) ^ 1u, kSiteAttn);
       if (!ok) break;
       float* const sc = reinterpret_cast<float*>(smem + Smem::kScale + sl * Smem::kScaleSlot);
-      *reinterpret_cast<float4*>(sc + 4 * lane) = ks;
-      *reinterpret_cast<float4*>(sc + 128 + 4 * lane) = vs;
       const auto size = [](float s) { return fabsf(s) <= 3.402823466e38f ? fabsf(s) : 0.f; };
       const float top = fmaxf(fmaxf(size(vs.x), size(vs.y)), fmaxf(size(vs.z), size(vs.w)));
       const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      if (lane == 0) sc[256] = __uint_as_float(all);
+      power = fmaxf(power, scale_power(__uint_as_float(all)));
+      const float by = power_inverse(power);
+      *reinterpret_cast<float4*>(sc + 4 * lane) = ks;
+      *reinterpret_cast<float4*>(sc + 128 + 4 * lane) = make_float4(vs.x * by, vs.y * by, vs.z * by, vs.w * by);
+      if (lane == 0) sc[256] = power;
+      if (last) power = kLeastScale;
       __syncwarp();
       if (lane == 0) mbar_arrive(sc_full(sl));
       ok = ask(p.cache.v_q, 0) && ask(p.cache.v_q, 1);
@@ -456,6 +461,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t ts = tmem + 128u * tl + (r0 << 16), to = tmem + 256u + kD * tl + (r0 << 16);
     const int g = lane >> 2, t2 = 2 * (lane & 3);
     const float* const scales = reinterpret_cast<const float*>(smem + Smem::kScale);
+    const auto rescale = [&](const float (&by)[2]) {  // o, a row of the thread each
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 32) {
+        uint32_t o[16];
+        tmem_ld_16x32(to + c, o);
+        tmem_ld_wait(o);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by[e >> 1 & 1]);
+        tmem_st_16x256b_x4(to + c, o);
+      }
+    };
     uint32_t i = 0;
     bool ok = true;
     do {
@@ -499,6 +516,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const AttnRow row[2] = {attn_row(p, w.s, w.hk, packed + g), attn_row(p, w.s, w.hk, packed + g + 8)};
       const int low = __shfl_sync(0xffffffffu, row[0].limit, 0);  // the smallest of the warp's rows
       float bs[2];
+      float power = kLeastScale;  // of v's scales, in o
       uint64_t sum[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -511,8 +529,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = warp_wait(sc_full(sl), i / kTileScales & 1u, kSiteAttn + 8);
         if (!ok) break;
         const float* const sc = scales + sl * (Smem::kScaleSlot / 4);
-        const float lv = scale_power(sc[256]);
+        const float given = sc[256];  // the power that v's scales are divided by
         const bool edge = key + kAttnUnit - 1 > low;
+        if (given != power) {  // (the same in the whole warp; hardly ever after a piece's first units)
+          if (i > begin) {
+            ok = warp_wait(pv_done(2 * tl + 1), uph ^ 1u, kSiteAttn + 10);
+            if (!ok) break;
+            const float by = ex2(power_log2(power, given));
+            const float corr[2] = {by, by};
+            rescale(corr);
+          }
+          power = given;
+        }
 #pragma unroll 1
         for (uint32_t h = 0; h < 2; ++h) {
           ok = warp_wait(s_full(2 * tl + h), uph, kSiteAttn + 9);
@@ -529,9 +557,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             scaled<true>(v, hsc, seen, mx);
           else
             scaled<false>(v, hsc, seen, mx);
-          // What is taken out of the exponents moves where P would leave fp16: to the row's largest score of these
-          // keys and log2 of the largest of their values' scales.
-          const bool fits = mx[0] * rf[0] + lv <= bs[0] + 8.0f && mx[1] * rf[1] + lv <= bs[1] + 8.0f;
+          // What is taken out of the exponents, and of the values' scales, moves where P would leave fp16: to the row's
+          // largest score of these keys, and to the largest of their scales.
+          const bool fits = mx[0] * rf[0] <= bs[0] + 8.0f && mx[1] * rf[1] <= bs[1] + 8.0f;
           if (!__all_sync(0xffffffffu, fits)) {
             bool move = false;
             float corr[2];
@@ -539,7 +567,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int k = 0; k < 2; ++k) {
               mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
               mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-              const float to_be = (mx[k] == -INFINITY ? mx[k] : mx[k] * rf[k]) + lv;
+              const float to_be = mx[k] == -INFINITY ? mx[k] : mx[k] * rf[k];
               corr[k] = 1.0f;
               if (to_be > bs[k] + 8.0f) {
                 move = true;
@@ -551,16 +579,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if ((i > begin || h > 0) && __any_sync(0xffffffffu, move)) {
               ok = warp_wait(pv_done(2 * tl + (h ^ 1u)), h == 0 ? uph ^ 1u : uph, kSiteAttn + 10);
               if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < kD; c += 32) {
-                uint32_t o[16];
-                tmem_ld_16x32(to + c, o);
-                tmem_ld_wait(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr[e >> 1 & 1]);
-                tmem_st_16x256b_x4(to + c, o);
-              }
+              rescale(corr);
             }
           }
           const float less[2] = {bs[0] == -INFINITY ? 0.f : bs[0], bs[1] == -INFINITY ? 0.f : bs[1]};  // (no key seen yet)
@@ -596,49 +615,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const bool whole = w.begins && w.ends;
       const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (w.begins ? 1 : 0)) * kTileRows + 128 * tl + r0;
       // The outputs go through the warp's rows of q's place, which the products have left, so that whole rows, or
-      // halves of them in fp32, are written at a time.
+      // 128 bytes of them in fp32, are written at a time.  (32 columns together: with 64 the loops' registers spill.)
       const uint32_t stage = base + Smem::kQ + tl * Smem::kOperand;
       const int in_rows = min(16, max(0, w.s.n * p.group - packed));
+      // (the quotient within 2 ulp; no sum is near 2^126)
+      const float unit = power_unit(power);
+      const float by[2] = {l[0] == 0.f ? 0.f : __fdividef(unit, l[0]), l[1] == 0.f ? 0.f : __fdividef(unit, l[1])};
 #pragma unroll 1
-      for (int c = 0; c < kD; c += 64) {
-        uint32_t v[32];
-        tmem_ld_16x64(to + c, v);
+      for (int c = 0; c < kD; c += 32) {
+        uint32_t v[16];
+        tmem_ld_16x32(to + c, v);
         tmem_ld_wait(v);
         if (whole) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float inv = l[k] == 0.f ? 0.f : 1.0f / l[k];
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
               st_shared_u32(stage + panel_at(r0 + g + 8 * k, c / 8 + j) + 2 * t2,
-                            pack_bf16x2(__uint_as_float(v[4 * j + 2 * k]) * inv, __uint_as_float(v[4 * j + 2 * k + 1]) * inv));
-          }
+                            pack_bf16x2(__uint_as_float(v[4 * j + 2 * k]) * by[k], __uint_as_float(v[4 * j + 2 * k + 1]) * by[k]));
         } else {
-          // 16 rows of 256 bytes: 32 columns in one panel's row, 32 in the other's (D = 64: in the row of another 16)
-          const auto place = [&](uint32_t r, uint32_t c16) {  // the 16-byte group c16 of row r
-            return kD == 128 ? stage + panel_at(r0 + r, c16)
-                             : stage + (r0 + r) * 128u + (((c16 & 7u) ^ (r & 7u)) << 4);
+          const auto place = [&](uint32_t r, uint32_t c16) {  // 16 rows of 128 bytes: the 16-byte group c16 of row r
+            return stage + (r0 + r) * 128u + ((c16 ^ (r & 7u)) << 4);
           };
 #pragma unroll
-          for (int b = 0; b < (kD == 128 ? 1 : 2); ++b) {
-            if (b > 0) __syncwarp();
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                if (kD == 64 && j / 4 != b) continue;
-                const uint32_t at = place(g + 8 * k, 2 * j + (t2 >> 2)) + 4 * (t2 & 2);
-                st_shared_u32(at, v[4 * j + 2 * k]);
-                st_shared_u32(at + 4, v[4 * j + 2 * k + 1]);
-              }
-            __syncwarp();
-            constexpr int kLanes = kD == 128 ? 16 : 8;  // of a row
-#pragma unroll
-            for (int j = 0; j < 16 * kLanes / 32; ++j) {
-              const int r = j * (32 / kLanes) + lane / kLanes, c16 = lane % kLanes;
-              if (r < in_rows)
-                *reinterpret_cast<uint4*>(ws.o + (slot + r) * kD + c + 32 * b + 4 * c16) = ld_shared_v4(place(r, c16));
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t at = place(g + 8 * k, 2 * j + (t2 >> 2)) + 4 * (t2 & 2);
+              st_shared_u32(at, v[4 * j + 2 * k]);
+              st_shared_u32(at + 4, v[4 * j + 2 * k + 1]);
             }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = 4 * j + (lane >> 3), c16 = lane & 7;
+            if (r < in_rows) *reinterpret_cast<uint4*>(ws.o + (slot + r) * kD + c + 4 * c16) = ld_shared_v4(place(r, c16));
           }
           __syncwarp();
         }
@@ -659,9 +670,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (row[k].in && t2 == 0) {
-          if (!whole)
+          if (!whole) {
             ws.ml[slot + g + 8 * k] = make_float2(bs[k], l[k]);
-          else if (p.lse != nullptr)
+            ws.unit[slot + g + 8 * k] = unit;
+          } else if (p.lse != nullptr)
             p.lse[row[k].at] = attn_lse(bs[k], l[k]);
         }
       tc_fence_before();

@@ -1255,13 +1255,14 @@ coda_status_t rope_of(const double* inv_freq, const int32_t* axis, int64_t half,
   return CODA_OK;
 }
 
-// Parts of the attention's items: [cuts | maxima and sums | outputs], two parts per block, of as many rows as
+// Parts of the attention's items: [cuts | maxima and sums | units | outputs], two parts per block, of as many rows as
 // a tile may have (`rows`: packed rows of the call at most)
 int attn_ws_rows(int tile_rows, int64_t rows) { return static_cast<int>(std::min<int64_t>(tile_rows, rows)); }
 
 size_t attn_ws_bytes(int tile_rows, int64_t rows, int64_t D) {
   const size_t parts = size_t(2) * kAttnMaxBlocks * attn_ws_rows(tile_rows, rows);
-  return align256(kAttnMaxBlocks * sizeof(AttnCutFew)) + align256(parts * sizeof(float2)) + align256(parts * D * sizeof(float));
+  return align256(kAttnMaxBlocks * sizeof(AttnCutFew)) + align256(parts * sizeof(float2)) + align256(parts * sizeof(float)) +
+         align256(parts * D * sizeof(float));
 }
 
 AttnWs attn_ws(char* at, int tile_rows, int64_t rows, int64_t D) {
@@ -1272,6 +1273,8 @@ AttnWs attn_ws(char* at, int tile_rows, int64_t rows, int64_t D) {
   at += align256(kAttnMaxBlocks * sizeof(AttnCutFew));
   w.ml = reinterpret_cast<float2*>(at);
   at += align256(size_t(2) * kAttnMaxBlocks * w.rows * sizeof(float2));
+  w.unit = reinterpret_cast<float*>(at);
+  at += align256(size_t(2) * kAttnMaxBlocks * w.rows * sizeof(float));
   w.o = reinterpret_cast<float*>(at);
   return w;
 }

@@ -1,0 +1,62 @@
+"""Attention over the 8-bit paged cache at the ends of its numeric range, on the GPU against the definition in 64 bits.
+
+The tolerances are cache_q8_ref.attend's unless a test says otherwise."""
+
+import pytest
+import torch
+
+from cache_q8_ref import U, Batch, gen
+from test_attn_q8_gpu import check, clean, queries
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    import __graft_entry__ as g
+
+    g.build()
+    from gemm_epilogue_fusion_gemm0_gb300 import binding
+
+    torch.cuda.set_device(0)
+    return binding
+
+
+SHAPES = [  # new, lens, Hq, Hk, D: tiles of 8 rows, of 16, and of 256
+    ([1, 1], [1000, 37], 4, 2, 128),
+    ([5, 1], [1003, 60], 8, 2, 64),
+    ([200, 3], [900, 300], 4, 1, 128),
+]
+
+
+# ------------------------------------------------------------------ large value scales
+@pytest.mark.parametrize("power", [60, 100, 115, 121, 126])
+@pytest.mark.parametrize("new,lens,Hq,Hk,D", SHAPES)
+def test_large_value_scales(B, new, lens, Hq, Hk, D, power):
+    """Whatever v's scales, a row's weights and their sum are the scores': o is the definition's and lse does not
+    change.  (The codes keep o within fp32.)"""
+    batch = Batch(new, lens, Hk, D, 16)
+    cache = batch.random_cache(B)
+    q = queries(batch, Hq, power, 2.0)
+    _, lse = B.coda_attn_q8(q, cache, batch.cu, batch.lens, batch.table, want_lse=True)
+    most = 2 if power > 121 else 63
+    cache[2].clamp_(-most, most)
+    cache[3].mul_(50.0).mul_(2.0 ** power)  # 2^power times 0.1 to 1
+    check(B, batch, q, cache)
+    _, lse2 = B.coda_attn_q8(q, cache, batch.cu, batch.lens, batch.table, want_lse=True)
+    # two lse of the same scores, whose sums may be taken in other units: each off by its sum's rounding
+    t = max(lens)
+    assert ((lse - lse2).abs() <= 2 * (2 * (t // 16 + 1) + 64) * U + 8 * U * lse.abs()).all()
+
+
+def test_the_largest_values_that_a_write_keeps(B):
+    """Values near bf16's end through the cache: what is read back, attended to, is its mean."""
+    T, Hk, D = 300, 1, 64
+    batch = Batch([T], [T], Hk, D, 16)
+    y = torch.randn(T, 3, D, device="cuda", generator=gen(1))
+    y[:, 2] = (torch.rand(T, D, device="cuda", generator=gen(2)) * 2 - 1) * 3e38
+    y = y.to(torch.bfloat16).view(T, -1)
+    cache = B.coda_cache_q8(batch.pages, Hk, 16, D)
+    q = B.coda_cache_write_q8(y, cache, batch.cu, batch.lens, batch.table)
+    assert cache[3][batch.table[0, 0].long()].amax() > 2.0 ** 119
+    check(B, batch, q, cache)
