@@ -332,8 +332,9 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 // Scales: a key's multiplies its row of S^T; a value's, less a power of two, its row of p^T.  What is taken out of the
 // exponents is a row's largest score; it moves, and sum and outputs with it, only where p would pass 2^8, which a thread
 // sees in its own scores; only then is a row's maximum found.  The power of two is the largest value scale's, rounded up,
-// so that weights times scales stay within fp16.  It is the outputs' alone: a sum that shared it (weights of
-// 2^(score - maximum - power)) lost its small terms, then all, with scales from 2^102 on.
+// so that weights times scales stay within fp16; a row's own, of the keys that it sees, where a unit has keys that some
+// rows do not see.  It is the outputs' alone: a sum that shared it (weights of 2^(score - maximum - power)) lost its small
+// terms, then all, with scales from 2^102 on.
 // ---------------------------------------------------------------------------
 template <int kD, int kN>
 struct FewSmem {
@@ -393,6 +394,7 @@ __device__ __forceinline__ float exponent_factor(float scale_log2, float down) {
 
 // The power of two that a value scale is at most (2^-60 for smaller ones, a NaN among them; an infinity stands for 2^128).
 constexpr float kLeastScale = 0x1p-60f;
+__device__ __forceinline__ float finite_size(float s) { return fabsf(s) <= 3.402823466e38f ? fabsf(s) : 0.f; }
 __device__ __forceinline__ float scale_power(float s) {
   return s > kLeastScale ? __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u) : kLeastScale;
 }
@@ -404,6 +406,13 @@ __device__ __forceinline__ float power_unit(float power) {
 }
 __device__ __forceinline__ float power_inverse(float power) {
   return __uint_as_float(((254u + kPowerUp) << 23) - __float_as_uint(power));
+}
+// a / b of powers of two at most 2^126 apart; and the power half way between two, which is that near to any between them.
+__device__ __forceinline__ float power_ratio(float a, float b) {
+  return __uint_as_float(__float_as_uint(a) - __float_as_uint(b) + (127u << 23));
+}
+__device__ __forceinline__ float power_between(float a, float b) {
+  return __uint_as_float((__float_as_uint(a) / 2 + __float_as_uint(b) / 2) & 0x7f800000u);
 }
 // log2 of a / b, powers of two
 __device__ __forceinline__ float power_log2(float a, float b) {
@@ -449,6 +458,18 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+
+// The power of the largest scale that a row sees of a warp's 32 keys: s0 .. s3 are those of this thread's first key and of
+// those 8, apart and apart + 8 behind it, of which the row sees 0 .. seen.  (Not inlined: hardly ever called.)
+__device__ __noinline__ float seen_power(float s0, float s1, float s2, float s3, int seen, int apart) {
+  float top = 0 <= seen ? finite_size(s0) : 0.f;
+  if (8 <= seen) top = fmaxf(top, finite_size(s1));
+  if (apart <= seen) top = fmaxf(top, finite_size(s2));
+  if (apart + 8 <= seen) top = fmaxf(top, finite_size(s3));
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return scale_power(top);
 }
 
 template <int kD, int kN>
@@ -534,7 +555,9 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
     uint32_t qb[kN][kSteps][2];
     float acc[kN][kTiles][4];
     float l[kN][2], rf[kN][2], base[kN][2];
-    float power = kLeastScale;  // of the value scales, in the outputs
+    float power[kN][2];  // of the value scales, in the outputs
+    // what the value scales are divided by: the power where all of the warp's rows have one (`fit` too; else it is negative)
+    float common = kLeastScale, fit = kLeastScale;
     int limit[kN][2];
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
@@ -576,6 +599,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
         limit[n][e] = __shfl_sync(0xffffffffu, row.limit, 4 * (2 * t + e));
         base[n][e] = -INFINITY;
         l[n][e] = 0.f;
+        power[n][e] = kLeastScale;
       }
 #pragma unroll
       for (int j = 0; j < kTiles; ++j)
@@ -644,9 +668,8 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
               for (int e = 0; e < 4; ++e)
                 if (key_of(q, e >> 1) > limit[n][e & 1]) s[q][n][e] = -INFINITY;
         }
-        float vm = fmaxf(max3_abs(0.f, vs[0][0], vs[0][1]), max3_abs(0.f, vs[1][0], vs[1][1]));
         float mx[kN][2];
-        bool fits = vm <= power;
+        bool fits = fmaxf(max3_abs(0.f, vs[0][0], vs[0][1]), max3_abs(0.f, vs[1][0], vs[1][1])) <= fit;
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -655,11 +678,38 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
             fits = fits && mx[n][e] * rf[n][e] <= base[n][e] + 8.0f;
           }
         if (!__all_sync(0xffffffffu, fits)) {
+          float less[kN][2];  // what the outputs are multiplied by for the powers
+          const auto most = [&](int limit) {
+            return seen_power(vs[0][0], vs[0][1], vs[1][0], vs[1][1], max(limit, -1) - key - g, Deal::kApart);
+          };
+          const float all = fmaxf(common, most(0x7fffffff));
+          if (!edge || all <= fit) {
+            const float by = ex2(power_log2(common, all));
 #pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-          const float before = power;
-          power = fmaxf(power, scale_power(vm));
-          const float less = ex2(power_log2(before, power));
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) power[n][e] = all, less[n][e] = by;
+            common = fit = all;
+          } else {
+            float high = 0.f, low_power = INFINITY;
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float before = power[n][e];
+                power[n][e] = fmaxf(before, most(limit[n][e]));
+                less[n][e] = ex2(power_log2(before, power[n][e]));
+                high = fmaxf(high, power[n][e]);
+                low_power = fminf(low_power, power[n][e]);
+              }
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+              high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+              low_power = fminf(low_power, __shfl_xor_sync(0xffffffffu, low_power, o));
+            }
+            common = power_between(low_power, high);
+            fit = low_power == high ? high : -1.0f;
+          }
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
             float c[2];
@@ -675,7 +725,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
                 base[n][e] = to_be;
               }
               l[n][e] *= c[e];
-              c[e] *= less;
+              c[e] *= less[n][e];
             }
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
@@ -684,7 +734,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
           }
         }
         uint32_t pb[2][kN][2];  // weights of keys 2 t, 2 t + 1 (and 8 further) of row 8 n + g
-        const float by = power_inverse(power);
+        const float by = power_inverse(common);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -702,15 +752,16 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
               s[q][n][e] = x * vs[q][e >> 1];
             }
         }
-        if (edge) {  // (a scale behind a row's last key may be NaN)
+        if (edge) {  // (a scale behind a row's last key may be anything)
           __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
+            for (int e = 0; e < 4; ++e) {
+              const float own = power_ratio(common, power[n][e & 1]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (key_of(q, e >> 1) > limit[n][e & 1]) s[q][n][e] = 0.f;
+              for (int q = 0; q < 2; ++q) s[q][n][e] = key_of(q, e >> 1) > limit[n][e & 1] ? 0.f : s[q][n][e] * own;
+            }
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -790,7 +841,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
         }
         if (warp == 0 && g == 0) row_ml[r] = make_float2(top, sum);
         // (as quotients by the sum, within 2 ulp, which stay in range whatever the power)
-        f[n][e] = ex2(base[n][e] - less) * (sum == 0.f ? 0.f : __fdividef(power_unit(power), sum));
+        f[n][e] = ex2(base[n][e] - less) * (sum == 0.f ? 0.f : __fdividef(power_unit(power[n][e]), sum));
       }
     const bool whole = w.begins && w.ends;
     const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.begins ? 1 : 0);

@@ -23,8 +23,8 @@
 //                      of them 2350 cycles.)
 //   warp 20            issues tcgen05.mma: of each half of each tile, P v of a unit, then S of the next
 //   warp 21            looks up pages, asks for their codes and puts a unit's scales into shared memory
-// o is rescaled only where a row's maximum has grown by more than 2^8 or the largest of v's scales by a power of two (P
-// stays below fp16's largest): hardly ever after the first units.
+// o is rescaled only where a row's maximum has grown by more than 2^8 or the largest of v's scales that it sees by a power
+// of two (P stays below fp16's largest): hardly ever after the first units.
 #pragma once
 
 #include "attn_q8.cuh"
@@ -44,8 +44,9 @@ struct TileSmem {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + 2 * kOperand;
   static constexpr uint32_t kV = kK + kTileStages * kOperand;
-  static constexpr uint32_t kScale = kV + kTileStages * kOperand;  // [slot][k's 128, v's 128, their power]
-  static constexpr uint32_t kScaleSlot = 2 * 512 + 16;
+  // [slot][k's 128, v's 128 divided by the power, v's 128, the power: of the largest of v's of the piece so far]
+  static constexpr uint32_t kScale = kV + kTileStages * kOperand;
+  static constexpr uint32_t kScaleSlot = 3 * 512 + 16;
   static constexpr uint32_t kRawBytes = 64 * kD;
   static constexpr uint32_t kRaw = (kScale + kTileScales * kScaleSlot + 127) / 128 * 128;
   static constexpr uint32_t kBar = kRaw + kRawStages * kRawBytes;
@@ -121,8 +122,8 @@ __device__ __forceinline__ uint32_t panel_at(uint32_t row, uint32_t c) {
 
 // The softmax of 64 columns of a warp's 16 rows.  A thread has 16 columns of two rows, so a column's scale, read
 // once, serves two products (with a row to a thread, the reads of scales alone took as long on shared memory as the
-// operands of the products).  `sc`: k's scales (v's 128 numbers on) from the thread's first column.  kEdge: row k
-// sees columns 0 .. seen[k] of those from there on.
+// operands of the products).  `sc`: k's scales (v's 128 and 256 numbers on) from the thread's first column.
+// kEdge: row k sees columns 0 .. seen[k] of those from there on, and has a power of its own.
 
 // S times k's scales, and its largest.
 template <bool kEdge>
@@ -146,13 +147,14 @@ __device__ __forceinline__ void scaled(uint32_t (&v)[32], const float* sc, const
   }
 }
 
-// P = 2^(what `scaled` left * rf - less) v's scale in fp16; the sums without v's scale.
+// P = 2^(what `scaled` left * rf - less) v's scale / power in fp16; the sums without these two.
 template <bool kEdge>
 __device__ __forceinline__ void weights(const uint32_t (&v)[32], const float* sc, const int (&seen)[2], const float (&rf)[2],
-                                        const float (&less)[2], uint32_t (&pk)[16], uint64_t (&sum)[2]) {
+                                        const float (&less)[2], const float (&power)[2], uint32_t (&pk)[16],
+                                        uint64_t (&sum)[2]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float2 v2 = *reinterpret_cast<const float2*>(sc + 128 + 8 * i);
+    const float2 v2 = *reinterpret_cast<const float2*>(sc + (kEdge ? 256 : 128) + 8 * i);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float x, y;
@@ -167,13 +169,33 @@ __device__ __forceinline__ void weights(const uint32_t (&v)[32], const float* sc
       }
       const uint64_t xy = pack2(x, y);
       sum[k] = add2(sum[k], xy);
-      unpack2(mul2(xy, pack2(v2.x, v2.y)), x, y);
+      if constexpr (kEdge) {
+        const float by = power_inverse(power[k]);
+        unpack2(mul2(xy, mul2(pack2(v2.x, v2.y), pack2(by, by))), x, y);
+      } else {
+        unpack2(mul2(xy, pack2(v2.x, v2.y)), x, y);
+      }
       if constexpr (kEdge) {  // (a scale behind the row's last key may be NaN)
         if (8 * i > seen[k]) x = 0.f;
         if (8 * i + 1 > seen[k]) y = 0.f;
       }
       pk[2 * i + k] = pack_f16x2(x, y);
     }
+  }
+}
+
+// o of a warp's rows, two of the thread's, times a number each.  (Not inlined: hardly ever called.)
+template <int kD>
+__device__ __noinline__ void rescale_rows(uint32_t to, float by0, float by1) {
+  tc_fence_after();
+#pragma unroll 1
+  for (int c = 0; c < kD; c += 32) {
+    uint32_t o[16];
+    tmem_ld_16x32(to + c, o);
+    tmem_ld_wait(o);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e >> 1 & 1 ? by1 : by0));
+    tmem_st_16x256b_x4(to + c, o);
   }
 }
 
@@ -364,14 +386,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = warp_wait(sc_empty(sl), (i / kTileScales & 1u) ^ 1u, kSiteAttn);
       if (!ok) break;
       float* const sc = reinterpret_cast<float*>(smem + Smem::kScale + sl * Smem::kScaleSlot);
-      const auto size = [](float s) { return fabsf(s) <= 3.402823466e38f ? fabsf(s) : 0.f; };
-      const float top = fmaxf(fmaxf(size(vs.x), size(vs.y)), fmaxf(size(vs.z), size(vs.w)));
+      const float top = fmaxf(fmaxf(finite_size(vs.x), finite_size(vs.y)), fmaxf(finite_size(vs.z), finite_size(vs.w)));
       const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
       power = fmaxf(power, scale_power(__uint_as_float(all)));
       const float by = power_inverse(power);
       *reinterpret_cast<float4*>(sc + 4 * lane) = ks;
       *reinterpret_cast<float4*>(sc + 128 + 4 * lane) = make_float4(vs.x * by, vs.y * by, vs.z * by, vs.w * by);
-      if (lane == 0) sc[256] = power;
+      *reinterpret_cast<float4*>(sc + 256 + 4 * lane) = vs;
+      if (lane == 0) sc[384] = power;
       if (last) power = kLeastScale;
       __syncwarp();
       if (lane == 0) mbar_arrive(sc_full(sl));
@@ -461,18 +483,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t ts = tmem + 128u * tl + (r0 << 16), to = tmem + 256u + kD * tl + (r0 << 16);
     const int g = lane >> 2, t2 = 2 * (lane & 3);
     const float* const scales = reinterpret_cast<const float*>(smem + Smem::kScale);
-    const auto rescale = [&](const float (&by)[2]) {  // o, a row of the thread each
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < kD; c += 32) {
-        uint32_t o[16];
-        tmem_ld_16x32(to + c, o);
-        tmem_ld_wait(o);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by[e >> 1 & 1]);
-        tmem_st_16x256b_x4(to + c, o);
-      }
-    };
     uint32_t i = 0;
     bool ok = true;
     do {
@@ -516,10 +526,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const AttnRow row[2] = {attn_row(p, w.s, w.hk, packed + g), attn_row(p, w.s, w.hk, packed + g + 8)};
       const int low = __shfl_sync(0xffffffffu, row[0].limit, 0);  // the smallest of the warp's rows
       float bs[2];
-      float power = kLeastScale;  // of v's scales, in o
+      float power[2];  // of v's scales, in o
       uint64_t sum[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+        power[k] = kLeastScale;
         bs[k] = -INFINITY;
         sum[k] = 0;
       }
@@ -529,17 +540,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = warp_wait(sc_full(sl), i / kTileScales & 1u, kSiteAttn + 8);
         if (!ok) break;
         const float* const sc = scales + sl * (Smem::kScaleSlot / 4);
-        const float given = sc[256];  // the power that v's scales are divided by
+        const float given = sc[384];
         const bool edge = key + kAttnUnit - 1 > low;
-        if (given != power) {  // (the same in the whole warp; hardly ever after a piece's first units)
+        // (hardly ever after a piece's first units)
+        if (__any_sync(0xffffffffu, given > power[0] || given > power[1])) {
+          float corr[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float to_be = given;
+            if (edge) {  // what its rows see alone
+              const int seen = row[k].limit - (key + t2);
+              float vm = 0.f;
+#pragma unroll 1
+              for (int c = 0; c < kAttnUnit; c += 8) {
+                const float2 vs = *reinterpret_cast<const float2*>(sc + 256 + t2 + c);
+                if (c <= seen) vm = fmaxf(vm, finite_size(vs.x));
+                if (c + 1 <= seen) vm = fmaxf(vm, finite_size(vs.y));
+              }
+              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+              to_be = fmaxf(power[k], scale_power(vm));
+            }
+            corr[k] = ex2(power_log2(power[k], to_be));
+            power[k] = to_be;
+          }
           if (i > begin) {
             ok = warp_wait(pv_done(2 * tl + 1), uph ^ 1u, kSiteAttn + 10);
             if (!ok) break;
-            const float by = ex2(power_log2(power, given));
-            const float corr[2] = {by, by};
-            rescale(corr);
+            rescale_rows<kD>(to, corr[0], corr[1]);
           }
-          power = given;
         }
 #pragma unroll 1
         for (uint32_t h = 0; h < 2; ++h) {
@@ -579,15 +608,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if ((i > begin || h > 0) && __any_sync(0xffffffffu, move)) {
               ok = warp_wait(pv_done(2 * tl + (h ^ 1u)), h == 0 ? uph ^ 1u : uph, kSiteAttn + 10);
               if (!ok) break;
-              rescale(corr);
+              rescale_rows<kD>(to, corr[0], corr[1]);
             }
           }
           const float less[2] = {bs[0] == -INFINITY ? 0.f : bs[0], bs[1] == -INFINITY ? 0.f : bs[1]};  // (no key seen yet)
           uint32_t pk[16];
           if (edge)
-            weights<true>(v, hsc, seen, rf, less, pk, sum);
+            weights<true>(v, hsc, seen, rf, less, power, pk, sum);
           else
-            weights<false>(v, hsc, seen, rf, less, pk, sum);
+            weights<false>(v, hsc, seen, rf, less, power, pk, sum);
           tmem_st_16x128b_x8(ts + 64u * h, pk);  // over S, which is read
           tmem_st_wait();
           tc_fence_before();
@@ -619,8 +648,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint32_t stage = base + Smem::kQ + tl * Smem::kOperand;
       const int in_rows = min(16, max(0, w.s.n * p.group - packed));
       // (the quotient within 2 ulp; no sum is near 2^126)
-      const float unit = power_unit(power);
-      const float by[2] = {l[0] == 0.f ? 0.f : __fdividef(unit, l[0]), l[1] == 0.f ? 0.f : __fdividef(unit, l[1])};
+      const float by[2] = {l[0] == 0.f ? 0.f : __fdividef(power_unit(power[0]), l[0]),
+                           l[1] == 0.f ? 0.f : __fdividef(power_unit(power[1]), l[1])};
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
         uint32_t v[16];
@@ -672,7 +701,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (row[k].in && t2 == 0) {
           if (!whole) {
             ws.ml[slot + g + 8 * k] = make_float2(bs[k], l[k]);
-            ws.unit[slot + g + 8 * k] = unit;
+            ws.unit[slot + g + 8 * k] = power_unit(power[k]);
           } else if (p.lse != nullptr)
             p.lse[row[k].at] = attn_lse(bs[k], l[k]);
         }

@@ -60,3 +60,28 @@ def test_the_largest_values_that_a_write_keeps(B):
     q = B.coda_cache_write_q8(y, cache, batch.cu, batch.lens, batch.table)
     assert cache[3][batch.table[0, 0].long()].amax() > 2.0 ** 119
     check(B, batch, q, cache)
+
+
+# ------------------------------------------------------------------ tokens that a row does not see
+@pytest.mark.parametrize("value", [2.0 ** 12, 2.0 ** 20, 2.0 ** 100, 2.0 ** 121, float("inf"), float("nan")])
+@pytest.mark.parametrize("new,lens,Hq,Hk,D", [([5, 1], [1003, 60], 8, 2, 64), ([6, 1], [30, 9], 8, 8, 128),
+                                              ([200, 1], [900, 30], 4, 1, 128), ([330, 70], [330, 2000], 2, 2, 64)])
+def test_scales_of_unseen_tokens(B, new, lens, Hq, Hk, D, value):
+    """Rows before a token give the same bits whatever that token's v scale is."""
+    batch = Batch(new, lens, Hk, D, 16)
+    cache, q = batch.random_cache(B), queries(batch, Hq, 3, 2.0)
+    args = (q, cache, batch.cu, batch.lens, batch.table)
+    o, lse = B.coda_attn_q8(*args, want_lse=True)
+    for back in (1, 2, new[0] // 2):  # the last token, the last but one, one in the middle
+        page, slot = batch.slot(0, lens[0] - back)
+        was = cache[3][page, :, slot].clone()
+        cache[3][page, :, slot] = value
+        o2, lse2 = B.coda_attn_q8(*args, want_lse=True)
+        cache[3][page, :, slot] = was
+        before, behind = slice(0, new[0] - back), slice(new[0], None)
+        for rows in (before, behind):
+            assert torch.equal(o2[rows], o[rows]) and torch.equal(lse2[rows], lse[rows])
+        assert torch.equal(lse2, lse)  # which knows no v
+        seen = o2[new[0] - back:new[0]]
+        assert not torch.equal(seen, o[new[0] - back:new[0]])
+    clean(B)
