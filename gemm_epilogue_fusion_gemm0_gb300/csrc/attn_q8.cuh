@@ -399,8 +399,10 @@ __device__ __forceinline__ float scale_power(float s) {
   return s > kLeastScale ? __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u) : kLeastScale;
 }
 // A value scale goes into the weights divided by power / 2^kPowerUp, and the outputs are multiplied by that in the end
-// (both are fp32 numbers for all powers).
-constexpr uint32_t kPowerUp = 2;
+// (both are fp32 numbers for all powers).  A weight is at most 2^8, so the products reach 2^15 at most (fp16 has 65504), and
+// a row's largest weights begin at 2^6 or above: those down to 2^-20 of them keep fp16's 11 bits.  (With products from one
+// down, 131072 alike of 2^-17 beside a large one were 5e-3 off, all to one side.)
+constexpr uint32_t kPowerUp = 7;
 __device__ __forceinline__ float power_unit(float power) {
   return __uint_as_float(__float_as_uint(power) - (kPowerUp << 23));
 }

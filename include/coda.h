@@ -450,7 +450,7 @@ CODA_API coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, c
  * hint, the largest number of rows of a sequence (0: not known); with any other value the result is
  * the same and the time may be longer.
  * fp32 sums and softmax; weights times v's scales are rounded to fp16 before their products with v's codes: by 2^-11 of
- * each at most or, where that is more, by 2^-24 of the row's largest weight times the largest scale that it sees (scales
+ * each at most or, where that is more, by 2^-30 of the row's largest weight times the largest scale that it sees (scales
  * below 2^-60 count as 2^-60).  A NaN or an infinity in a row of q, or a NaN scale of a token that it sees, makes the row
  * NaN; a row that sees none is zero whatever it holds.
  * Results do not depend on other sequences but in the order of fp32 sums, and are the same on

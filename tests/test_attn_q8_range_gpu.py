@@ -2,10 +2,12 @@
 
 The tolerances are cache_q8_ref.attend's unless a test says otherwise."""
 
+import math
+
 import pytest
 import torch
 
-from cache_q8_ref import U, Batch, gen
+from cache_q8_ref import U, UB, UH, Batch, gen
 from test_attn_q8_gpu import check, clean, queries
 
 pytestmark = pytest.mark.gpu
@@ -84,4 +86,44 @@ def test_scales_of_unseen_tokens(B, new, lens, Hq, Hk, D, value):
         assert torch.equal(lse2, lse)  # which knows no v
         seen = o2[new[0] - back:new[0]]
         assert not torch.equal(seen, o[new[0] - back:new[0]])
+    clean(B)
+
+
+# ------------------------------------------------------------------ many small weights
+@pytest.mark.parametrize("n,group,seqs", [(1, 1, 1), (2, 8, 1), (60, 1, 160)])
+@pytest.mark.parametrize("bits,steps", [(17.0, 106.5), (17.5, 75.5), (18.0, 53.5), (18.5, 40.5)])
+def test_many_small_weights_beside_a_large_one(B, n, group, seqs, bits, steps):
+    """A first token of weight one and 131072 others of weight 2^-bits each, alike, with values of the other sign: what
+    their weights lose together is within fp16's 2^-11 of each.  (`steps`: their weight times scale in steps of 2^-24 if
+    the first one's is near one: midway between two.)  160 sequences of the same pages, so that whole rows of keys are one
+    block's.
+
+    The bound, relative to the sum of |weights times values|, which is v: as attend's for scores of size bits log 2,
+    without a term for what lies below fp16's range; and o's rounding."""
+    t, D = 131072 + n, 64
+    pages = -(-t // 256)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.randperm(pages, device="cuda", generator=gen(1)).to(torch.int32)
+    k_q, k_s, v_q, v_s = cache = B.coda_cache_q8(pages, 1, 256, D)
+    k_q.zero_()
+    k_s.fill_(1.0 / 64)
+    v_q.fill_(100)
+    v_s.fill_(steps * 2.0 ** (bits - 24) * 2.0 ** -6)
+    first = int(table[0])
+    k_q[first, 0, 0] = 64
+    v_q[first, 0, 0] = -100
+    q = torch.zeros(seqs * n, group, D, device="cuda", dtype=torch.bfloat16)
+    q[:, :, 5] = 16.0
+    size = bits * math.log(2)
+    o = B.coda_attn_q8(q.view(seqs * n, -1), cache, torch.arange(seqs + 1, device="cuda", dtype=torch.int32) * n,
+                       torch.full((seqs,), t, **i32), table.repeat(seqs, 1), scale=size / 16, most=n)
+    others = torch.arange(t - n, t, device="cuda").double().repeat(seqs)  # that each row sees
+    small = math.exp(-16 * torch.tensor(size / 16, dtype=torch.float32).item())
+    v = 100 * v_s[0, 0, 0].item()
+    want = (v * (others * small - 1) / (1 + others * small))[:, None]
+    rel = (2 * (D // 16) + 12) * U * size + 16 * U
+    sums = (2 * (t // 16 + 1) + 64) * U
+    off = (o.double() - want).abs()
+    bound = UB * want.abs() + (2 * rel + UH + sums) * 1.05 * v
+    assert (off <= bound).all(), (off / bound).max().item()
     clean(B)
