@@ -330,11 +330,12 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 // the g-th 16.  Both reads are free of bank conflicts with the 16-byte groups of a key exchanged as below.
 //
 // Scales: a key's multiplies its row of S^T; a value's, less a power of two, its row of p^T.  What is taken out of the
-// exponents is a row's largest score; it moves, and sum and outputs with it, only where p would pass 2^8, which a thread
-// sees in its own scores; only then is a row's maximum found.  The power of two is the largest value scale's, rounded up,
-// so that weights times scales stay within fp16; a row's own, of the keys that it sees, where a unit has keys that some
-// rows do not see.  It is the outputs' alone: a sum that shared it (weights of 2^(score - maximum - power)) lost its small
-// terms, then all, with scales from 2^102 on.
+// exponents is a row's largest score, rounded up to a whole number, so that a weight's rounding to fp16 is the same whatever
+// keys a part began with (else 11 % of the outputs changed with the rest of the batch); it moves, and sum and outputs
+// with it, only where p would pass 2^8, which a thread sees in its own scores; only then is a row's maximum found.  The
+// power of two is the largest value scale's, rounded up, so that weights times scales stay within fp16; a row's own, of the
+// keys that it sees, where a unit has keys that some rows do not see.  It is the outputs' alone: a sum that shared it
+// (weights of 2^(score - maximum - power)) lost its small terms, then all, with scales from 2^102 on.
 // ---------------------------------------------------------------------------
 template <int kD, int kN>
 struct FewSmem {
@@ -400,7 +401,7 @@ __device__ __forceinline__ float scale_power(float s) {
 }
 // A value scale goes into the weights divided by power / 2^kPowerUp, and the outputs are multiplied by that in the end
 // (both are fp32 numbers for all powers).  A weight is at most 2^8, so the products reach 2^15 at most (fp16 has 65504), and
-// a row's largest weights begin at 2^6 or above: those down to 2^-20 of them keep fp16's 11 bits.  (With products from one
+// a row's largest weights begin at 2^5 or above: those down to 2^-20 of them keep fp16's 11 bits.  (With products from one
 // down, 131072 alike of 2^-17 beside a large one were 5e-3 off, all to one side.)
 constexpr uint32_t kPowerUp = 7;
 __device__ __forceinline__ float power_unit(float power) {
@@ -723,8 +724,8 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
               const float to_be = mx[n][e] * rf[n][e];
               c[e] = 1.0f;
               if (to_be > base[n][e] + 8.0f) {
-                c[e] = ex2(base[n][e] - to_be);
-                base[n][e] = to_be;
+                c[e] = ex2(base[n][e] - ceilf(to_be));
+                base[n][e] = ceilf(to_be);
               }
               l[n][e] *= c[e];
               c[e] *= less[n][e];

@@ -600,8 +600,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               corr[k] = 1.0f;
               if (to_be > bs[k] + 8.0f) {
                 move = true;
-                corr[k] = ex2(bs[k] - to_be);
-                bs[k] = to_be;
+                corr[k] = ex2(bs[k] - ceilf(to_be));
+                bs[k] = ceilf(to_be);  // (a whole number: see the kernel for few)
               }
               sum[k] = mul2(sum[k], pack2(corr[k], corr[k]));
             }

@@ -448,13 +448,14 @@ CODA_API coda_status_t coda_cache_read_q8(const int8_t* k_q, const float* k_s, c
  *   scale > 0, finite.  A row that sees no token: o = 0, lse = -infinity.
  * One token per sequence, a few, a chunk and a whole prompt (lens = rows) are the same call.  most: a
  * hint, the largest number of rows of a sequence (0: not known); with any other value the result is
- * the same and the time may be longer.
+ * the same to fp32 rounding (see below) and the time may be longer.
  * fp32 sums and softmax; weights times v's scales are rounded to fp16 before their products with v's codes: by 2^-11 of
  * each at most or, where that is more, by 2^-30 of the row's largest weight times the largest scale that it sees (scales
  * below 2^-60 count as 2^-60).  A NaN or an infinity in a row of q, or a NaN scale of a token that it sees, makes the row
  * NaN; a row that sees none is zero whatever it holds.
- * Results do not depend on other sequences but in the order of fp32 sums, and are the same on
- * every run of the same call.
+ * Other sequences and the hint change a result by fp32 rounding alone: weights round to fp16 relative to powers of two
+ * whatever else is in the batch (but for a weight that fp32 rounding takes over fp16's border, and the smallest ones, within
+ * 2^-30 as above).  The same call gives the same bits on every run.
  *   workspace: at least coda_attn_q8_workspace_bytes(T, B, Hq, Hk, D) */
 CODA_API size_t coda_attn_q8_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D);
 CODA_API coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k_s,

@@ -127,3 +127,65 @@ def test_many_small_weights_beside_a_large_one(B, n, group, seqs, bits, steps):
     bound = UB * want.abs() + (2 * rel + UH + sums) * 1.05 * v
     assert (off <= bound).all(), (off / bound).max().item()
     clean(B)
+
+
+# ------------------------------------------------------------------ one sequence in many batches
+def exact_scores(B, n, t, Hq, Hk, D, seed):
+    """A sequence whose scores are multiples of 1/4 in base 2 and whose weighted sums of codes are exact in fp32, so that
+    nothing but the weights' rounding to fp16, relative to a power of two, and a last rounding of a quotient is left.
+    (q, codes, scales, scale) and the definition with its weights rounded so."""
+    g = gen(seed)
+    q = torch.zeros(n, Hq, D, device="cuda")
+    q[:, :, :2] = torch.tensor([1.0, 0.25], device="cuda")
+    q[:, :, 2] = torch.randint(0, 2, (n, Hq), device="cuda", generator=g).float()
+    k = torch.zeros(t, Hk, D, dtype=torch.int8, device="cuda")
+    k[:, :, 0] = torch.randint(-1, 2, (t, Hk), device="cuda", generator=g).to(torch.int8)
+    k[:, :, 1] = torch.randint(-2, 3, (t, Hk), device="cuda", generator=g).to(torch.int8)
+    k[:, :, 2] = torch.randint(0, 2, (t, Hk), device="cuda", generator=g).to(torch.int8)
+    # values that go by the fraction of a score (k's second column), so that its weights' roundings do not average out
+    sign = torch.randint(-1, 2, (5, D), device="cuda", generator=g).to(torch.int8)
+    v = sign[k[:, :, 1].long() + 2]
+    # a scale whose product with log2 e is one in fp32
+    e = torch.tensor(1.44269504088896, dtype=torch.float32)
+    near = [torch.tensor(math.log(2), dtype=torch.float32) + i * 2.0 ** -24 for i in range(-4, 5)]
+    scale = next(float(s) for s in near if s * e == 1.0)
+    group = Hq // Hk
+    x = torch.einsum("ihd,jhd->ihj", q.double(), k.double().repeat_interleave(group, 1))
+    unseen = (torch.arange(t, device="cuda") > torch.arange(t - n, t, device="cuda")[:, None])[:, None]
+    w = torch.exp2(x).masked_fill(unseen, 0.0)
+    # fp16 has 11 bits: its rounding of a number between two powers of two
+    unit = torch.exp2(torch.floor(x) - 10)
+    frac = w / unit
+    assert ((frac - frac.floor() - 0.5).abs() > 2.0 ** -8)[~unseen.expand_as(frac)].all()  # none near a tie
+    w16 = torch.round(frac) * unit
+    vv = v.double().repeat_interleave(group, 1)
+    o = torch.einsum("ihj,jhd->ihd", w16.masked_fill(unseen, 0.0), vv) / w.sum(2)[..., None]
+    return q.to(torch.bfloat16).view(n, -1), k, v, scale, o
+
+
+@pytest.mark.parametrize("most", [0, 1, 1000])
+@pytest.mark.parametrize("others", [[], [(1, 5000)] * 3, [(1, 700)] * 40, [(300, 900)], [(77, 300), (1, 9), (2, 4000), (500, 500)]])
+@pytest.mark.parametrize("n,t,Hq,Hk,D", [(1, 300, 4, 2, 128), (3, 257, 8, 2, 64), (90, 300, 2, 2, 128), (70, 200, 4, 1, 64)])
+def test_one_sequence_in_many_batches(B, n, t, Hq, Hk, D, others, most):
+    """Other sequences and the hint decide where a sequence's keys are cut and which kernel takes it; its weights round the
+    same way all the same.  Off by fp32 rounding alone: the sum of weights and the quotient (t + 64 roundings of the
+    result), the parts and their joins (24 and 160 of numbers up to 0.25); then bf16's, which keeps order: what lies
+    between two numbers before it lies between their roundings behind it."""
+    q1, k, v, scale, want = exact_scores(B, n, t, Hq, Hk, D, 7)
+    new, lens = [m for m, _ in others], [m for _, m in others]
+    at = len(others) // 2
+    new.insert(at, n)
+    lens.insert(at, t)
+    batch = Batch(new, lens, Hk, D, 16)
+    cache, q = batch.random_cache(B), queries(batch, Hq, 5)
+    row = sum(new[:at])
+    q[row:row + n] = q1
+    ids, slot = batch.table[at, torch.arange(t, device="cuda") // 16].long(), torch.arange(t, device="cuda") % 16
+    cache[0][ids, :, slot], cache[1][ids, :, slot] = k, 1.0
+    cache[2][ids, :, slot], cache[3][ids, :, slot] = v, 0.25
+    o = B.coda_attn_q8(q, cache, batch.cu, batch.lens, batch.table, scale=scale, most=most)
+    got, want = o[row:row + n].view(n, Hq, D), want * 0.25
+    slack = ((t + 64) * want.abs() + (24 + 160) * 0.25) * U
+    low, high = (want - slack).float().to(torch.bfloat16), (want + slack).float().to(torch.bfloat16)
+    assert ((got >= low) & (got <= high)).all(), int(((got < low) | (got > high)).sum())
+    clean(B)
