@@ -90,8 +90,9 @@ __device__ __forceinline__ RowPlace place_of(const BatchQ8& bt, const CacheQ8& c
 // fp32) and v become codes.
 //
 // Angles: a turn is 2^64, turn[i] = inv_freq / (2 pi) of it, and the product with the position modulo
-// 2^64 is the angle's fraction of a turn to |pos| 2^-54 of a turn, whatever the number of turns: no
-// position is too far.  Its upper 32 bits go to sincospif (2 ulp).
+// 2^64 is the angle's fraction of a turn to |pos| 2^-64 of a turn (frequencies up to 2^40), whatever the number of
+// turns: no position is too far.  Its upper 32 bits go, rounded to fp32 (2^-26 of a turn, 1.6 ulp of an fp32 sine
+// or cosine near one at most), to sincospif (2 ulp).
 //
 // Bound by HBM: 2 (Hq + 2 Hk) D bytes in, 2 Hq D + 2 Hk (D + 4) out per token.  A block takes kTokens
 // tokens: its threads find the tokens' places and form their angles' cos and sin once, one each, then D / 8

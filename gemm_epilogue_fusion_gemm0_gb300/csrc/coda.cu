@@ -1233,7 +1233,15 @@ coda_status_t check_cache(const int8_t* k_q, const float* k_s, const int8_t* v_q
   return CODA_OK;
 }
 
-// turn[i]: inv_freq[i] / (2 pi) modulo one turn, a turn being 2^64
+// The part of x that is no whole number, in -1/2 .. 1/2 (exact), in steps of 2^-64, modulo 2^64
+uint64_t fraction64(double x) {
+  const double part = (x - std::nearbyint(x)) * 0x1p64;  // -2^63 .. 2^63
+  return part < 0x1p63 ? static_cast<uint64_t>(std::llrint(part)) : uint64_t(1) << 63;
+}
+
+// turn[i]: inv_freq[i] / (2 pi) modulo one turn, a turn being 2^64.  1 / (2 pi) is the sum of two doubles, 2^-110 off, and
+// its product with a frequency of two more, so that a turn is off by a step or less: a double's own 2^-54 of a turn would be
+// 2^-23 of one at positions near 2^31.
 coda_status_t rope_of(const double* inv_freq, const int32_t* axis, int64_t half, const int32_t* pos,
                       int64_t axes, int pairs, int64_t D, RopeQ8* r) {
   if (half < 0 || axes < 1 || axes > kRopeAxes || (pos == nullptr && axes != 1)) return CODA_ERR_INVALID_ARG;
@@ -1244,9 +1252,9 @@ coda_status_t rope_of(const double* inv_freq, const int32_t* axis, int64_t half,
   for (int64_t i = 0; i < half; ++i) {
     if (!std::isfinite(inv_freq[i])) return CODA_ERR_INVALID_ARG;
     if (axis != nullptr && (axis[i] < 0 || axis[i] >= axes)) return CODA_ERR_INVALID_ARG;
-    const double turns = inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    const double part = turns - std::floor(turns);
-    r->turn[i] = part < 1.0 ? static_cast<uint64_t>(std::ldexp(part, 64)) : 0;
+    constexpr double kHigh = 0.15915494309189535, kLow = -9.839338337591243e-18;
+    const double f = inv_freq[i], turns = f * kHigh, rest = std::fma(f, kHigh, -turns) + f * kLow;
+    r->turn[i] = fraction64(turns) + fraction64(rest);
     r->axis[i] = static_cast<uint8_t>(axis != nullptr ? axis[i] : 0);
   }
   r->pos = pos;

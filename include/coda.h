@@ -421,8 +421,8 @@ CODA_API coda_status_t coda_bwd_swiglu_dgrad_q8(const coda_bf16* dout, const cod
  *     width of an image's or a video's patches); NULL: axis 0 for all
  *   pos [axes, T] int32: the rows' positions on each axis (1 to 4 axes); NULL: a row's token number
  *     (then axes = 1)
- * inv_freq and axis are read before the call returns.  Angles are exact to 2^-30 of a turn at any
- * position.  The rows of a call have to be distinct tokens: of two rows at one place either's codes
+ * inv_freq and axis are read before the call returns.  Angles are within 2^-26 of a turn (their rounding to fp32) and
+ * 2^-31 more at any position, for frequencies up to 2^40.  The rows of a call have to be distinct tokens: of two rows at one place either's codes
  * and scale may stay. */
 CODA_API coda_status_t coda_cache_write_q8(const coda_bf16* y, int8_t* k_q, float* k_s, int8_t* v_q,
                                            float* v_s, int64_t pages, int64_t Hk, int64_t page,
