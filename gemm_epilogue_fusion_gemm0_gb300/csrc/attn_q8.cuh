@@ -304,6 +304,15 @@ __device__ __forceinline__ AttnRow attn_row(const AttnQ8Params& p, const AttnSeq
   return r;
 }
 
+// That row's head lies within q and o (in the checked build).
+__device__ __forceinline__ bool row_ok(const AttnQ8Params& p, const AttnRow& r, uint32_t site) {
+  return checked(r.at >= 0 && r.at < static_cast<int64_t>(p.batch.rows) * p.Hq, site);
+}
+// Row `row` of a block's part `slot` lies within the workspace (the same).
+__device__ __forceinline__ bool part_ok(const AttnWs& ws, size_t slot, int row) {
+  return checked(slot < size_t(2) * kAttnMaxBlocks && row >= 0 && row < ws.rows, kChkPart);
+}
+
 // Natural logarithm of a row's sum (0: it sees no key) with the maximum `top` taken out, in base 2.
 __device__ __forceinline__ float attn_lse(float top, float sum) {
   return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
@@ -528,6 +537,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
       const uint32_t sc = gr + 2 * Smem::kCodes + 4u * lane;  // k's 16 scales, then v's
       if (static_cast<unsigned>(page) < static_cast<unsigned>(p.cache.pages)) {
         const size_t e = cache_entry(p.cache, page, ahead.hk, key & mask);
+        if (!entries_ok(p.cache, e, kFewKeys)) continue;
         const uint8_t* const k = p.cache.k_q + e * kD + lane_at;
         const uint8_t* const v = p.cache.v_q + e * kD + lane_at;
 #pragma unroll
@@ -570,7 +580,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kSteps / 2; ++i) {
         c[i] = Chunk8{{0u, 0u, 0u, 0u}};
-        if (row.in) c[i] = ldg8(p.q + row.at * kD + 64 * (i / 2) + 16 * t + 8 * (i % 2));
+        if (row.in && row_ok(p, row, kChkLoad)) c[i] = ldg8(p.q + row.at * kD + 64 * (i / 2) + 16 * t + 8 * (i % 2));
       }
 #pragma unroll
       for (int i = 0; i < kSteps / 2; ++i) {
@@ -878,10 +888,11 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
         const float2 ml = row_ml[row_at];
         if (whole) {
           const AttnRow row = attn_row(p, w.s, w.hk, w.tile * Deal::kRows + row_at);
+          if (!row_ok(p, row, kChkStore)) continue;
           *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * c) =
               make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
           if (c == 0 && p.lse != nullptr) p.lse[row.at] = attn_lse(ml.x, ml.y);
-        } else {
+        } else if (part_ok(ws, slot, row_at)) {
           reinterpret_cast<float4*>(ws.o)[(slot * ws.rows + row_at) * (kD / 4) + c] = x;
           if (c == 0) {
             ws.ml[slot * ws.rows + row_at] = ml;
@@ -928,7 +939,8 @@ __global__ void __launch_bounds__(256)
   // blocks c .. c + parts - 1; one whose share is empty (fewer units than blocks) has no part
   const int parts = static_cast<int>((cut.end * blocks + cut.cost - 1) / cut.cost) - c;
   for (int j = tid; j < parts; j += 256) {
-    const bool has = attn_share(cut.cost, c + j, blocks) < attn_share(cut.cost, c + j + 1, blocks);
+    const bool has = attn_share(cut.cost, c + j, blocks) < attn_share(cut.cost, c + j + 1, blocks) &&
+                     part_ok(ws, 2 * static_cast<size_t>(c + j) + 1, r0 + rows - 1);
     slots[j] = has ? 2 * (c + j) + (j == 0 ? 1 : 0) : -1;
   }
   __syncthreads();
@@ -987,6 +999,7 @@ __global__ void __launch_bounds__(256)
       if (r >= rows) continue;
       const float2 ml = row_ml[r];
       const AttnRow row = attn_row(p, s, cut.hk, cut.tile * kRows + r0 + r);
+      if (!row_ok(p, row, kChkStore)) continue;
       *reinterpret_cast<uint2*>(p.o + row.at * kD + 4 * col) =
           make_uint2(pack_bf16x2(x[i].x, x[i].y), pack_bf16x2(x[i].z, x[i].w));
       if (col == 0 && p.lse != nullptr) p.lse[row.at] = attn_lse(ml.x, ml.y);

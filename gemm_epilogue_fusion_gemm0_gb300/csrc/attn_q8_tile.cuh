@@ -349,15 +349,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // its scales: of keys 4 lane .. 4 lane + 3
       const int spage = __shfl_sync(0xffffffffu, page, 4 * lane >> log2), skey = key0 + 4 * lane;
       const size_t se = cache_entry(p.cache, max(spage, 0), hk, skey & mask);
-      float4 ks = *reinterpret_cast<const float4*>(p.cache.k_s + se);
-      float4 vs = *reinterpret_cast<const float4*>(p.cache.v_s + se);
+      float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), vs = ks;
+      if (entries_ok(p.cache, se, 4)) {
+        ks = *reinterpret_cast<const float4*>(p.cache.k_s + se);
+        vs = *reinterpret_cast<const float4*>(p.cache.v_s + se);
+      }
       // The codes of 64 keys; where there are none (behind the last key, or a page that does not exist) any will do:
       // their scales are zero or NaN.
       const auto ask = [&](const uint8_t* codes, int h) {
         const uint32_t slot = half % kRawStages;
         if (!warp_wait(raw_empty(slot), (half / kRawStages & 1u) ^ 1u, kSiteAttn + 13)) return false;
         ++half;
-        const bool mine = page >= 0 && lane >> (6 - log2) == h;
+        const bool mine = page >= 0 && lane >> (6 - log2) == h && entries_ok(p.cache, at / kD, keys);
         const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine));
         const uint32_t bytes = static_cast<uint32_t>(keys) * kD;
         if (lane == 0) {
@@ -497,7 +500,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const AttnRow row = attn_row(p, w.s, w.hk, packed + j * (32 / kLanes) + up_row);
-          x[j] = ldg8(p.q + row.at * kD + 8 * c);
+          x[j] = Chunk8{{0u, 0u, 0u, 0u}};
+          if (row_ok(p, row, kChkLoad)) x[j] = ldg8(p.q + row.at * kD + 8 * c);
         }
         float mine = 0.f;  // what row lane % 16 is multiplied by afterwards
 #pragma unroll
@@ -678,7 +682,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int r = 4 * j + (lane >> 3), c16 = lane & 7;
-            if (r < in_rows) *reinterpret_cast<uint4*>(ws.o + (slot + r) * kD + c + 4 * c16) = ld_shared_v4(place(r, c16));
+            if (r < in_rows && part_ok(ws, (slot + r) / kTileRows, static_cast<int>((slot + r) % kTileRows)))
+              *reinterpret_cast<uint4*>(ws.o + (slot + r) * kD + c + 4 * c16) = ld_shared_v4(place(r, c16));
           }
           __syncwarp();
         }
@@ -691,6 +696,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const int r = j * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
           if (r < in_rows) {
             const AttnRow at = attn_row(p, w.s, w.hk, packed + r);
+            if (!row_ok(p, at, kChkStore)) continue;
             *reinterpret_cast<uint4*>(p.o + at.at * kD + 8 * c) = ld_shared_v4(stage + panel_at(r0 + r, c));
           }
         }
@@ -700,9 +706,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int k = 0; k < 2; ++k)
         if (row[k].in && t2 == 0) {
           if (!whole) {
+            if (!part_ok(ws, (slot + g + 8 * k) / kTileRows, static_cast<int>((slot + g + 8 * k) % kTileRows))) continue;
             ws.ml[slot + g + 8 * k] = make_float2(bs[k], l[k]);
             ws.unit[slot + g + 8 * k] = power_unit(power[k]);
-          } else if (p.lse != nullptr)
+          } else if (p.lse != nullptr && row_ok(p, row[k], kChkStore))
             p.lse[row[k].at] = attn_lse(bs[k], l[k]);
         }
       tc_fence_before();

@@ -47,6 +47,15 @@ __device__ __forceinline__ size_t cache_entry(const CacheQ8& c, int page, int he
   return ((static_cast<size_t>(page) * c.Hk + head) << c.page_log2) + slot;
 }
 
+// n entries from e on, of the cache (in the checked build)
+__device__ __forceinline__ bool entries_ok(const CacheQ8& c, size_t e, int n) {
+  return checked(e + n <= (static_cast<size_t>(c.pages) * c.Hk) << c.page_log2, kChkCache);
+}
+// head h of `heads` of a row of the call
+__device__ __forceinline__ bool head_ok(const BatchQ8& bt, size_t row, int h, int heads, uint32_t site) {
+  return checked(row < static_cast<size_t>(bt.rows) && h >= 0 && h < heads, site);
+}
+
 // The sequence that a row belongs to, by a whole warp: the count of b in 1 .. B with cu[b] <= row.
 // 32 bounds at a time, so two loads one after the other serve 1024 sequences.  B for a row behind the
 // last sequence.
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(kCacheThreads, 3)
     for (int b = 0; b < kWriteBatch; ++b) {
       const int h = first + (r + b) * step;
       x[b] = Chunk8{{0u, 0u, 0u, 0u}};
-      if (there && h < heads) x[b] = ldg8(y + h * kD);
+      if (there && h < heads && head_ok(p.batch, row, h, heads, kChkLoad)) x[b] = ldg8(y + h * kD);
     }
   };
   load(0);
@@ -217,12 +226,14 @@ __global__ void __launch_bounds__(kCacheThreads, 3)
         amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o2));
       if (!in) continue;
       if (h < p.Hq) {
+        if (!head_ok(p.batch, row, h, p.Hq, kChkStore)) continue;
         uint32_t v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = pack_bf16x2(u[0][2 * e], u[0][2 * e + 1]);
         stg8(p.q_out + (row * p.Hq + h) * kD + 8 * c, v);
       } else if (pl.page >= 0) {
         const size_t e = cache_entry(p.cache, pl.page, is_v ? h - p.Hq - Hk : h - p.Hq, pl.slot);
+        if (!entries_ok(p.cache, e, 1)) continue;
         const Q8Factors f(amax);
         f.prepare(u);
         // (a key that is not turned is a bf16 number: the quantiser's rounding)
@@ -277,8 +288,10 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_q8_kernel(const Cach
       const RowPlace pl = place[min(t, kReadTokens - 1)];
       in[b] = u < units && pl.seq >= 0;
       out[b] = (static_cast<size_t>(row0 + t) * Hk + h) * kD + 16 * c;
-      const bool held = in[b] && pl.page >= 0;
-      const size_t e = held ? cache_entry(p.cache, pl.page, h, pl.slot) : 0;
+      in[b] = in[b] && head_ok(p.batch, static_cast<size_t>(row0 + t), h, Hk, kChkStore);
+      const bool there = in[b] && pl.page >= 0;
+      const size_t e = there ? cache_entry(p.cache, pl.page, h, pl.slot) : 0;
+      const bool held = there && entries_ok(p.cache, e, 1);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         q[b][kv] = make_uint4(0u, 0u, 0u, 0u);

@@ -37,7 +37,8 @@ __device__ uint32_t g_coda_status = 0;  // device status word (see WaitSite)
 // against its length), every TMA box start against its tensor map's extent and
 // the 16-byte alignment of its innermost coordinate, and every index into the
 // workspace (partial sums, completion flags, split-tail slots) against the
-// size the host gave it.  A failed check records 0x200 | site in the status
+// size the host gave it; of the 8-bit cache's kernels every row of a tensor,
+// every entry of the cache and every part in the workspace.  A failed check records 0x200 | site in the status
 // word (first failure wins; coda_get_device_status reports
 // CODA_ERR_DEVICE_BOUNDS) and skips the access; a failed TMA check also makes
 // the producer leave its role like a wait that ran out.  Nothing traps.  In the
@@ -58,6 +59,8 @@ enum CheckSite : uint32_t {
   kChkFlag = 6,        // row-block completion flag
   kChkSplitSlot = 7,   // split-tail partial slot or its flag
   kChkColPartial = 8,  // column partial of dgamma
+  kChkCache = 9,       // codes and scales of the 8-bit cache
+  kChkPart = 10,       // part of an item of attention in the workspace
 };
 
 __device__ __forceinline__ bool checked(bool ok, uint32_t site) {
