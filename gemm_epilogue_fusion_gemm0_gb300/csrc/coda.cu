@@ -1181,7 +1181,11 @@ cudaError_t launch_product_mid(MidQ8Params p, const uint8_t* a_q, const uint8_t*
 // The 8-bit paged cache (cache_q8.cuh, attn_q8.cuh)
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 16;  // of its largest tile
-constexpr int kFewMost = 48;  // packed rows of a sequence that go to the kernel for few
+// Packed rows of a sequence that go to the kernel for few.  Measured, few / tiles: 64 sequences over 8000 keys, 8 key heads of
+// 128, 32 rows 353 / 454 us, 40 515 / 455, 64 682 / 457; 16 over 3000, 4 of 64, 40 rows 34 / 43, 64 41 / 43, 128 66 / 43; 4
+// over 1000, 8 of 128, 40 rows 24 / 30, 64 25 / 30, 128 34 / 31.  The border is at 32 rows where the keys' bytes are the
+// bound and near 100 where latency is: one in between.
+constexpr int kFewMost = 48;
 constexpr int64_t kMaxSequences = 8192, kMaxHeads = 1024;
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -1289,15 +1293,19 @@ AttnWs attn_ws(char* at, int tile_rows, int64_t rows, int64_t D) {
 
 // Sequences of up to kFewMost packed rows go to the kernel for few, the others to the one for tiles, each with
 // its own share of the blocks; one join serves both.  Without a hint of `rows` (the most of a sequence) both
-// run, and one of them may find nothing; a single sequence goes to tiles if it may have more than a few rows.  If a
-// sequence has more rows than the hint says, the kernel for few takes it.  Its tiles are of 8 rows where no sequence has
-// more, and beside tiles where one token has no more (single tokens among chunks: 67 us with four, 72 with tiles of
-// 16), else of 16 (five tokens of 8 heads: 23 us, and each key is read 3 times, not 5).
+// run, and one of them may find nothing (64 single tokens over 8000 keys: 164 us, 159 with the hint); a single sequence goes to
+// tiles if it may have more than a few rows.  If a sequence has more rows than the hint says, the kernel for few takes it.
+//
+// Its tiles are of 8 rows where no sequence has more; else of 16, which read a key once where tiles of 8 read it twice (64
+// sequences of six tokens of 8 heads over 3000 keys: 240 us with the hint).  Beside tiles the short sequences' rows are not
+// known: with a hint they are taken for single tokens (two chunks beside four: 139 us, 143 with tiles of 16; beside 16
+// drafts of five 176 and 171), without one where there are as many rows as sequences (64 single tokens: 164 us, 193 with
+// tiles of 16), and not where there are more (the drafts of six: 247 us, 356 with tiles of 8).
 template <int kD>
-cudaError_t launch_attn(const AttnQ8Params& p, char* at, int64_t rows, int blocks, cudaStream_t stream) {
+cudaError_t launch_attn(const AttnQ8Params& p, char* at, int64_t rows, bool hint, int blocks, cudaStream_t stream) {
   const bool tiles = rows > kFewMost, few = !tiles || p.batch.B > 1;
   const int64_t all = static_cast<int64_t>(p.batch.rows) * p.group;  // (a hint may be too small)
-  const bool eight = rows <= 8 || (tiles && p.group <= 8);
+  const bool eight = rows <= 8 || (tiles && p.group <= 8 && (hint || p.batch.rows <= p.batch.B));
   const AttnWs wf = attn_ws(at, eight ? 8 : kFewRows, all, kD);
   const AttnWs wt = attn_ws(at + attn_ws_bytes(kFewRows, all, kD), kTileRows, kTileRows, kD);
   int k = 0;
@@ -2176,8 +2184,8 @@ coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k
   char* const wsb = static_cast<char*>(workspace) + kSlotBytes;
   // the most packed rows that a sequence may have
   const int64_t rows = std::min(most > 0 ? most : T, T) * p.group;
-  const cudaError_t e = D == 64 ? launch_attn<64>(p, wsb, rows, blocks, stream)
-                                : launch_attn<128>(p, wsb, rows, blocks, stream);
+  const cudaError_t e = D == 64 ? launch_attn<64>(p, wsb, rows, most > 0, blocks, stream)
+                                : launch_attn<128>(p, wsb, rows, most > 0, blocks, stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return CODA_ERR_LAUNCH;
