@@ -550,7 +550,7 @@ def coda_cache_write_q8(y, cache, cu, lens, table, inv_freq=None, axis=None, pos
     token's number is its position.  pairs: pair i is values (2 i, 2 i + 1) and not (i, i + half)."""
     T, n = y.shape
     _, Hk, _, D = cache[0].shape
-    if n % D or n // D <= 2 * Hk:
+    if not D or n % D or n // D <= 2 * Hk:
         raise ValueError(f"y must have Hq + 2 * {Hk} heads of {D} values, got {n} values")
     Hq = n // D - 2 * Hk
     c = _Call("coda_cache_write_q8", y.device, stream)
@@ -592,7 +592,7 @@ def coda_attn_q8(q, cache, cu, lens, table, scale=None, most=0, o=None, lse=None
     (o, lse) with want_lse=True (lse [T, Hq] fp32, natural logarithm)."""
     T, n = q.shape
     _, Hk, _, D = cache[0].shape
-    if n % D:
+    if not D or n % D:
         raise ValueError(f"q must have heads of {D} values, got {n} values")
     Hq = n // D
     c = _Call("coda_attn_q8", q.device, stream)

@@ -389,7 +389,7 @@ CODA_API coda_status_t coda_bwd_swiglu_dgrad_q8(const coda_bf16* dout, const cod
  * Keys and values are INT8 codes with one fp32 scale per token and head, as coda_quant_q8's
  * over the head's D values, in pages of `page` tokens:
  *   k_q, v_q [pages, Hk, page, D] INT8;  k_s, v_s [pages, Hk, page] fp32
- *   D 64 or 128; page a power of two from 16 to 256.
+ *   D 64 or 128; page a power of two from 16 to 256; at least one page, and a table at least one page wide.
  * Token p of sequence b lies in page table[b, p / page], slot p % page:
  *   table [B, width] int32; entries that no token of the call needs are not read.
  * A call's rows are the last tokens of the sequences, packed one sequence after the other:
