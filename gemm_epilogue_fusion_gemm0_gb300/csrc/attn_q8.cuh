@@ -47,7 +47,11 @@ struct AttnQ8Params {
   CacheQ8 cache;
   BatchQ8 batch;
   int Hq, group;           // query heads; of them per key head
-  float scale_log2;        // scale * log2 e
+  // scale * log2 e, the part that is no power of two and the power.  The part goes into k's scales; what a row's products are
+  // multiplied by in the exponents is then a power of two, so that a score less the largest is exact however large both are
+  // (where the largest was a rounded product and the others were not, weights passed 2^15 with scores from 2^27 on, and
+  // fp16's largest).
+  float scale_part, scale_power;
 };
 
 // ---------------------------------------------------------------------------
@@ -397,8 +401,8 @@ __device__ __forceinline__ void row_power(float amax, float& up, float& down) {
 }
 
 // What a row's products are multiplied by in the exponents; never zero, which times a masked score's -inf is NaN.
-__device__ __forceinline__ float exponent_factor(float scale_log2, float down) {
-  const float f = scale_log2 * down;
+__device__ __forceinline__ float exponent_factor(float scale_power, float down) {
+  const float f = scale_power * down;
   return f < 1.17549435e-38f ? 1.17549435e-38f : f;
 }
 
@@ -594,7 +598,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
       float up, down;
       row_power(amax, up, down);
       // (a row that sees no token is zero whatever it holds: its scores, all -inf, times a NaN would not be)
-      const float factor = row.limit < 0 ? 1.0f : exponent_factor(p.scale_log2, down);
+      const float factor = row.limit < 0 ? 1.0f : exponent_factor(p.scale_power, down);
 #pragma unroll
       for (int i = 0; i < kSteps / 2; ++i) {
         float v[8];
@@ -651,7 +655,7 @@ __global__ void __launch_bounds__(FewDeal<kN>::kThreads, 1)
           }
           const float* const sc =
               reinterpret_cast<const float*>(smem_few + (gr - smem_u32(smem_few)) + 2 * Smem::kCodes) + g;
-          ks[q][0] = sc[0], ks[q][1] = sc[8];
+          ks[q][0] = sc[0] * p.scale_part, ks[q][1] = sc[8] * p.scale_part;
           vs[q][0] = sc[16], vs[q][1] = sc[24];
         }
         if (!two) ks[1][0] = ks[1][1] = vs[1][0] = vs[1][1] = 0.f;

@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const auto given = [&](float s, int e) {  // nothing behind the last key is looked at; NaN for a page that does not exist
         return skey + e >= extent ? 0.f : spage < 0 ? __int_as_float(0x7fffffff) : s;
       };
-      ks = make_float4(given(ks.x, 0), given(ks.y, 1), given(ks.z, 2), given(ks.w, 3));
+      const float part = p.scale_part;
+      ks = make_float4(given(ks.x, 0) * part, given(ks.y, 1) * part, given(ks.z, 2) * part, given(ks.w, 3) * part);
       vs = make_float4(given(vs.x, 0), given(vs.y, 1), given(vs.z, 2), given(vs.w, 3));
       const uint32_t sl = i % kTileScales;
       ok = warp_wait(sc_empty(sl), (i / kTileScales & 1u) ^ 1u, kSiteAttn);
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                        pack_f16x2(v[0] * up, v[1] * up), pack_f16x2(v[2] * up, v[3] * up),
                        pack_f16x2(v[4] * up, v[5] * up), pack_f16x2(v[6] * up, v[7] * up));
         }
-        mine = exponent_factor(p.scale_log2, mine);
+        mine = exponent_factor(p.scale_power, mine);
         rf[0] = __shfl_sync(0xffffffffu, mine, g);
         rf[1] = __shfl_sync(0xffffffffu, mine, g + 8);
       }

@@ -2179,7 +2179,9 @@ coda_status_t coda_attn_q8(const coda_bf16* q, const int8_t* k_q, const float* k
   p.lse = lse_out;
   p.Hq = static_cast<int>(Hq);
   p.group = static_cast<int>(Hq / Hk);
-  p.scale_log2 = scale * 1.44269504088896f;
+  int power = 0;
+  p.scale_part = 2.0f * std::frexp(scale, &power) * 1.44269504088896f;
+  p.scale_power = std::ldexp(1.0f, power - 1);
   const int blocks = std::min(sms, kAttnMaxBlocks);
   char* const wsb = static_cast<char*>(workspace) + kSlotBytes;
   // the most packed rows that a sequence may have

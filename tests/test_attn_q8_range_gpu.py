@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from cache_q8_ref import U, UB, UH, Batch, gen
+from cache_q8_ref import U, UB, UH, Batch, attend, gen
 from test_attn_q8_gpu import check, clean, queries
 
 pytestmark = pytest.mark.gpu
@@ -188,4 +188,28 @@ def test_one_sequence_in_many_batches(B, n, t, Hq, Hk, D, others, most):
     slack = ((t + 64) * want.abs() + (24 + 160) * 0.25) * U
     low, high = (want - slack).float().to(torch.bfloat16), (want + slack).float().to(torch.bfloat16)
     assert ((got >= low) & (got <= high)).all(), int(((got < low) | (got > high)).sum())
+    clean(B)
+
+
+# ------------------------------------------------------------------ large scores
+@pytest.mark.parametrize("scale", [3e5, 1e7, 1e8, 7e8, 1e10, 3e15])
+@pytest.mark.parametrize("new,lens,Hq,Hk,D", SHAPES)
+def test_large_scores(B, new, lens, Hq, Hk, D, scale):
+    """Scores that fp32 holds to whole numbers or worse: whichever keys win, the outputs are means of their values.  All
+    values of a head are the same, so o is: off by the weights' rounding, which its sum does not have (2^-11), the sums'
+    (t / 16 truncations, joins) and bf16's.  lse is the largest score, to the rounding of a score (rel of attend)."""
+    batch = Batch(new, lens, Hk, D, 16)
+    cache = batch.random_cache(B)
+    cache[2].copy_(torch.arange(D, device="cuda") % 101 - 50)
+    cache[3].fill_(0.25)
+    cache[0][:, :, 8:].copy_(cache[0][:, :, :8].clone())  # pairs of keys with one score
+    cache[1][:, :, 8:].copy_(cache[1][:, :, :8].clone())
+    q = queries(batch, Hq, 3, 2.0)
+    o, lse = B.coda_attn_q8(q, cache, batch.cu, batch.lens, batch.table, scale=scale, want_lse=True)
+    want = ((torch.arange(D, device="cuda") % 101 - 50) * 0.25).double()
+    t = max(lens)
+    slack = (UH + (2 * (t // 16 + 1) + 64) * U) * 1.05 + UB
+    assert ((o.double().view(batch.T, Hq, D) - want).abs() <= slack * want.abs()).all()
+    _, lwant, _, lbound = attend(batch, q, cache, scale)
+    assert ((lse.double() - lwant).abs() <= lbound).all()
     clean(B)
