@@ -333,7 +333,8 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 //   S^T = k q^T,  o^T += v^T p^T    mma.sync.m16n8k16 on fp16
 // which takes half the instructions of the products and of the softmax that 16 query rows to an instruction take where
 // there are at most 8 (one token of 8 heads to a key head), and registers for 12 warps in place of 8: 64 tokens over up
-// to 8192 keys each, 64 / 8 heads of 128, 124 us, 5.5 TB/s (rows as the instruction's rows: 144).
+// to 8192 keys each, 64 / 8 heads of 128, 127 us, 5.4 TB/s (rows as the instruction's rows, before the powers below: 144,
+// with these 124).
 //
 // q's rows are brought into fp16's range by a power of two each (exact); codes are exact in fp16 (1024 + 128 + code by
 // bits, less 1152).  A thread (g = lane / 4, t = lane % 4) reads 16 codes of keys g and g + 8 at a time: its operand k
@@ -349,6 +350,10 @@ __device__ __forceinline__ float attn_lse(float top, float sum) {
 // power of two is the largest value scale's, rounded up, so that weights times scales stay within fp16; a row's own, of the
 // keys that it sees, where a unit has keys that some rows do not see.  It is the outputs' alone: a sum that shared it
 // (weights of 2^(score - maximum - power)) lost its small terms, then all, with scales from 2^102 on.
+//
+// The product with v's codes, which are exact in fp16, takes weights times scales in fp16 too: 2^-11 of each at most, an
+// eighth of what the outputs' rounding to bf16 may take.  (A second product for what is rounded away would cost as much as
+// the first.)  The sum of weights is of the numbers before that.
 // ---------------------------------------------------------------------------
 template <int kD, int kN>
 struct FewSmem {

@@ -11,7 +11,7 @@
 // Products are 4 * 256 * 128 * D operations per unit, 2048 cycles for D = 128.  Bound by shared memory: per unit 2048
 // cycles of operands (S's 64 columns at a time read q again), 1024 of scales to the softmax, 1024 of codes in, read and
 // widened out, 600 of the rest; measured 4300 to 5500 a unit with the pieces' ends.  A prompt of 8192 tokens of 32 heads of
-// 128: 577 us, 0.95 PFLOP/s.
+// 128: 582 us, 0.94 PFLOP/s.
 //
 // One block of 704 threads per SM:
 //   warps 0..7, 8..15  softmax of tile 0, 1: a warp has 16 rows, a thread 16 columns of a half of two of them.  (Four

@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kCacheThreads, 3)
         if (!entries_ok(p.cache, e, 1)) continue;
         const Q8Factors f(amax);
         f.prepare(u);
-        // (a key that is not turned is a bf16 number: the quantiser's rounding)
+        // (a key that is not turned is a bf16 number: the quantiser's rounding, whose first step, to 2^-15, takes 2^-16 of a
+        // code from a turned one at most, a twentieth of what the turn's own rounding does)
         q8_store8<true>((is_v ? p.cache.v_q : p.cache.k_q) + e * kD + 8 * c, u[0], f);
         if (c == 0) (is_v ? p.cache.v_s : p.cache.k_s)[e] = q8_scale(amax);
       }
